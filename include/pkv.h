@@ -382,6 +382,115 @@ int pkv_decode_step_static(const pkv_plan_t* plan, const pkv_problem* problem, c
                            const void* v_pool, const int32_t* block_table, const int32_t* seq_lens_dev, float scale,
                            void* out, uint32_t* status_dev, void* stream);
 
+/* ---- prompts and the 4-bit cache ---------------------------------------------------------------------------------
+ * The paper decodes over an FP16 cache that is already there. The calls below are how a serving program gets a
+ * prompt's tokens in (attention over the prompt, its K/V into the pages) and a second cache type of 4 bits a value.
+ *
+ * Packed prompts: the tokens of num_seqs sequences one after the other. cu_seqlens [num_seqs + 1] (int32, device)
+ * gives sequence s the packed rows [cu_seqlens[s], cu_seqlens[s + 1]); a sequence may be empty, and rows that belong
+ * to no sequence are neither read for another row's result nor written. A sequence whose bounds are not ordered
+ * inside [0, total_tokens] raises PKV_STATUS_BAD_LEN and is skipped.
+ *   q [total_tokens][Hq][d], k, v [total_tokens][Hkv][d], out [total_tokens][Hq][d]: fp16, 16-byte aligned, the heads
+ *   of one token contiguous; the distance between tokens is a stride, so q, k and v may be slices of one projection.
+ *
+ * 4-bit pages: pool [num_pages][Hkv][PKV_Q4_BLOCK_BYTES] bytes, 16-byte aligned; the block of a (page, KV head) holds
+ * the K and V of the page's 16 tokens:
+ *   [0, 1024)     K codes     [1024, 1152)  K parameters
+ *   [1152, 2176)  V codes     [2176, 2304)  V parameters
+ * A group is 64 dims of one token (dims 0-63, 64-127). Its parameters are two fp16, (scale, offset), at 4 * (2 * slot +
+ * group) of the parameters, and code c stands for c * scale + offset. offset is the group's least value, scale =
+ * fp16((greatest - least) / 15) (the difference and the quotient in fp32, each rounded to nearest even), c =
+ * (value - offset) / scale rounded to nearest even and clamped to 0..15 (0 where scale is 0). A group with an infinity
+ * or a NaN stands for NaN throughout. A byte holds one token's dims d (low 4 bits) and d + 64 (high 4 bits), d < 64:
+ *   K codes, slot r:  byte r * 64 + (d / 2 % 4) * 16 + (d / 16) * 4 + 2 * (d % 2) + d / 8 % 2
+ *   V codes, slot r:  byte (r / 8) * 512 + (d % 8) * 64 + (r / 2 % 4) * 16 + (d / 16) * 4 + 2 * (r % 2) + d / 8 % 2
+ * (the order in which the decode's matrix instructions take them). A (token, KV head) takes 144 bytes, 512 in FP16.
+ * num_sms below is the SM count of the current GPU.
+ */
+#define PKV_Q4_BLOCK_BYTES 2304
+#define PKV_PROMPT_WS_BYTES 256 /* workspace of the prompt calls and of pkv_q4_read: the header */
+
+typedef struct pkv_prompt {
+    int32_t num_seqs;      /* sequences, at most PKV_MAX_BATCH */
+    int32_t total_tokens;  /* rows of q, k, v and out */
+    int32_t num_q_heads;   /* Hq */
+    int32_t num_kv_heads;  /* Hkv; Hq / Hkv in {1, 2, 4, 8, 16} */
+    int32_t head_dim;      /* d (128) */
+    int32_t reserved;      /* 0 */
+    int64_t q_stride;      /* elements from one token to the next: at least heads * d, a multiple of 8 */
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t out_stride;
+} pkv_prompt;
+
+/* Validates a prompt description against the supported set. Host only. */
+int pkv_check_prompt(const pkv_prompt* prompt);
+
+/*
+ * Causal grouped-query attention over whole packed prompts: for token i of a sequence and query head hq (KV head
+ * hq / G), out = softmax(scale * q_i . k_j over the sequence's tokens j <= i) V. scale must be finite and >= 0.
+ * A value in k or v of a token that a row does not attend to (a later token, another sequence) never reaches that
+ * row, infinities and NaN included. ws: PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once (pkv_workspace_init). out
+ * must not overlap q, k or v.
+ */
+int pkv_prompt_attention(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
+                         const int32_t* cu_seqlens, float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out,
+                         void* stream);
+
+/*
+ * Packed prompts' K/V into the FP16 pages that pkv_decode reads. Token i of sequence s goes to position start[s] + i of
+ * row s: slot (start[s] + i) % 16 of page block_table[s][(start[s] + i) / 16]; start [num_seqs] int32, NULL = 0 (tokens
+ * behind others that the row holds already). problem->batch must equal prompt->num_seqs and the KV heads must agree;
+ * of prompt only num_seqs, total_tokens, num_kv_heads, head_dim, k_stride and v_stride matter beyond that check. A
+ * row that would outgrow its block table raises PKV_STATUS_BAD_LEN and is skipped; a token whose page is outside the
+ * pool raises PKV_STATUS_BAD_PAGE and is skipped. Two tokens must not share a slot. Other slots keep their values.
+ */
+int pkv_prompt_append(const pkv_problem* problem, const pkv_prompt* prompt, const void* k, const void* v,
+                      const int32_t* cu_seqlens, const int32_t* start, void* k_pool, void* v_pool,
+                      const int32_t* block_table, int32_t num_sms, void* ws, size_t ws_bytes, void* stream);
+
+/* The same into 4-bit pages: every token is quantised as "4-bit pages" above says. */
+int pkv_q4_prompt_append(const pkv_problem* problem, const pkv_prompt* prompt, const void* k, const void* v,
+                         const int32_t* cu_seqlens, const int32_t* start, void* pool, const int32_t* block_table,
+                         int32_t num_sms, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Tokens of 4-bit pages back as packed FP16 rows (the values that the codes stand for, rounded once): row
+ * cu_seqlens[s] + i of k_out and v_out receives token start[s] + i of row s. Arguments as for pkv_q4_prompt_append;
+ * k_stride and v_stride are those of k_out and v_out.
+ */
+int pkv_q4_read(const pkv_problem* problem, const pkv_prompt* prompt, const int32_t* cu_seqlens, const int32_t* start,
+                const void* pool, const int32_t* block_table, void* k_out, void* v_out, int32_t num_sms, void* ws,
+                size_t ws_bytes, void* stream);
+
+/* Bytes of a 4-bit pool of problem->num_pages pages. Host only. */
+int pkv_q4_pool_bytes(const pkv_problem* problem, size_t* bytes);
+
+/* Bytes of the workspace of a 4-bit decode step on a GPU of num_sms SMs; zero it once (pkv_workspace_init). It does not
+ * depend on the batch or the lengths. Host only. */
+int pkv_q4_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size_t* bytes);
+
+/*
+ * One decode step over 4-bit pages: as pkv_decode_step, with q, block_table, seq_lens and out of the same layouts and
+ * attention over the values that the codes stand for (the products take the codes as they are; scales and offsets are
+ * applied in fp32). There is no plan: the division of the step's pages over the GPU is worked out on the device from
+ * seq_lens, so one captured graph serves every step of a batch. scale may be any finite number. A row of length 0
+ * gets 0. Errors the kernels detect: PKV_STATUS_BAD_PAGE (a page outside the pool: its tokens are left out),
+ * PKV_STATUS_BAD_LEN (the row counts as empty), PKV_STATUS_TIMEOUT.
+ */
+int pkv_q4_decode_step(const pkv_problem* problem, const void* q, const void* pool, const int32_t* block_table,
+                       const int32_t* seq_lens_dev, float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out,
+                       void* stream);
+
+/*
+ * The same with the new token's K/V appended (as pkv_decode_step_append): k_new, v_new [B][Hkv][d] fp16 are quantised
+ * into slot (L_b - 1) % 16 of page block_table[b][(L_b - 1) / 16], and the step attends to the quantised token. No two
+ * rows may append to one page.
+ */
+int pkv_q4_decode_step_append(const pkv_problem* problem, const void* q, const void* k_new, const void* v_new,
+                              void* pool, const int32_t* block_table, const int32_t* seq_lens_dev, float scale,
+                              int32_t num_sms, void* ws, size_t ws_bytes, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

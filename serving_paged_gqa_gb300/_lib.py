@@ -42,17 +42,29 @@ EXPORTS = (
     "pkv_workspace_init", "pkv_build_worklist", "pkv_decode", "pkv_merge", "pkv_decode_step", "pkv_read_status",
     "pkv_plan_launches", "pkv_decode_step_static", "pkv_decode_step_append", "pkv_step_input_layout",
     "pkv_serve_step", "pkv_session_create", "pkv_session_step", "pkv_session_stats", "pkv_session_destroy",
+    "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append", "pkv_q4_read",
+    "pkv_q4_pool_bytes", "pkv_q4_workspace_bytes", "pkv_q4_decode_step", "pkv_q4_decode_step_append",
 )
 
 PKV_SESSION_GRAPHS = 16
 
 PKV_STATIC_SCRATCH_BYTES = 16 << 20
 
+PKV_Q4_BLOCK_BYTES = 2304
+PKV_PROMPT_WS_BYTES = 256
+
 
 class Problem(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("max_pages_per_seq", ctypes.c_int32)]
+
+
+class Prompt(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64)]
 
 
 class Policy(ctypes.Structure):
@@ -149,6 +161,19 @@ def load(path: str | None = None):
         lib.pkv_session_stats.argtypes = [_vp, _P(ctypes.c_int64), _P(ctypes.c_int64)]
         lib.pkv_session_destroy.restype = ctypes.c_int
         lib.pkv_session_destroy.argtypes = [_vp]
+        i32, f32, size = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        for name, args in (
+                ("pkv_check_prompt", [_P(Prompt)]),
+                ("pkv_prompt_attention", [_P(Prompt), _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
+                ("pkv_prompt_append", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp, size, _vp]),
+                ("pkv_q4_prompt_append", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp, size, _vp]),
+                ("pkv_q4_read", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp, size, _vp]),
+                ("pkv_q4_pool_bytes", [_P(Problem), _P(size)]),
+                ("pkv_q4_workspace_bytes", [_P(Problem), i32, _P(size)]),
+                ("pkv_q4_decode_step", [_P(Problem), _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
+                ("pkv_q4_decode_step_append", [_P(Problem), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp])):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = args
         _lib = lib
         return lib
 

@@ -67,6 +67,48 @@ struct MergeParams {
     int32_t task_capacity;  // tasks whose states the workspace holds
 };
 
+// Arguments of the prompt attention (prompt_attention.cu).
+struct PromptParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    const int32_t* cu_seqlens;
+    pkv_ws_header* hdr;
+    int64_t q_stride, k_stride, v_stride, out_stride;  // elements between tokens
+    int32_t num_seqs, total_tokens, Hq, Hkv;
+    float scale_log2;
+};
+
+// Arguments of the kernels that move packed prompts into pages and back (prompt_pages.cu).
+struct PagesParams {
+    const void* k;      // packed rows (append)
+    const void* v;
+    void* k_pool;       // FP16 pools (pkv_prompt_append), or the packed outputs (pkv_q4_read)
+    void* v_pool;
+    void* pool;         // 4-bit blocks
+    const int32_t* cu_seqlens;
+    const int32_t* start;
+    const int32_t* block_table;
+    pkv_ws_header* hdr;
+    int64_t k_stride, v_stride;
+    int32_t num_seqs, total_tokens, Hkv, num_pages, max_pages;
+};
+
+// Arguments of the 4-bit decode (q4_decode.cu).
+struct Q4Params {
+    const void* q;
+    const void* k_new;
+    const void* v_new;
+    void* pool;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    void* out;
+    pkv_ws_header* hdr;
+    int32_t B, Hq, Hkv, num_pages, max_pages;
+    float scale_log2;
+};
+
 // Kernel launchers (defined in the .cu files). They return the CUDA error of the launch.
 int launch_decode(const DecodeParams& p, int group, int grid, bool pdl, void* stream);
 int launch_build(const BuildParams& p, int grid, void* stream);
@@ -74,6 +116,14 @@ int launch_merge(const MergeParams& p, void* stream);
 // Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) from src to dst on the device; src may be pinned
 // host memory through its device-visible address.
 int launch_stage_copy(const void* src, void* dst, size_t bytes, void* stream);
+int launch_prompt_attention(const PromptParams& p, int num_sms, void* stream);
+int launch_prompt_append(const PagesParams& p, int num_sms, void* stream);
+int launch_q4_append(const PagesParams& p, int num_sms, void* stream);
+int launch_q4_read(const PagesParams& p, int num_sms, void* stream);
+int launch_q4_decode(const Q4Params& p, int num_sms, void* stream);
+
+// Workspace of a 4-bit decode step on a GPU of num_sms SMs.
+size_t q4_workspace_bytes(const pkv_problem& pr, int num_sms);
 
 // Validation shared by pkv_decode and the step entry points (PKV_OK or a PKV_E_* code; enqueues nothing).
 int check_decode_args(const pkv_plan_t* plan, const pkv_problem* pr, const void* q, const void* k_pool,

@@ -1,0 +1,346 @@
+"""Python binding of the prompt and 4-bit-cache calls of libpkv.so (include/pkv.h, "prompts and the 4-bit cache").
+
+The ``pkv_*`` functions are thin wrappers of the same-named C calls; ``prompt_attention``, ``prompt_append``,
+``q4_prompt_append``, ``q4_read`` and ``q4_decode`` take the description of the problem from the tensors. Argument
+marshalling only: the work runs in the library's CUDA kernels, on the device of the tensors.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from ._lib import PKV_PROMPT_WS_BYTES, PKV_Q4_BLOCK_BYTES, Problem, Prompt, check, load
+from .binding import _ptr, _stream, alloc_workspace, make_problem
+
+__all__ = [
+    "make_prompt", "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append",
+    "pkv_q4_read", "pkv_q4_pool_bytes", "pkv_q4_workspace_bytes", "pkv_q4_decode_step", "pkv_q4_decode_step_append",
+    "prompt_attention", "prompt_append", "q4_problem", "q4_prompt_append", "q4_read", "q4_decode",
+]
+
+_sms: dict[int, int] = {}
+
+
+def _num_sms(device: torch.device) -> int:
+    i = device.index if device.index is not None else torch.cuda.current_device()
+    n = _sms.get(i)
+    if n is None:
+        n = _sms[i] = torch.cuda.get_device_properties(i).multi_processor_count
+    return n
+
+
+def _on(device: torch.device):
+    """The library launches on the current device: makes the tensors' device current where it is not."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"the tensors must be on one device: {t.device} and {device}")
+
+
+def _rows(t: torch.Tensor, name: str, heads: int | None = None, rows: int | None = None, d: int | None = None) -> int:
+    """Checks a packed [tokens, heads, d] tensor whose tokens may be strided; returns the distance between tokens."""
+    if t.dim() != 3 or t.dtype != torch.float16:
+        raise ValueError(f"{name} must be a float16 tensor [tokens, heads, d]")
+    n, h, dim = t.shape
+    if (heads is not None and h != heads) or (rows is not None and n != rows) or (d is not None and dim != d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {heads}, {d}]")
+    s0, s1, s2 = t.stride()
+    if (dim > 1 and s2 != 1) or (h > 1 and s1 != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if n > 1 else h * dim
+
+
+def _rows_ptr(t: torch.Tensor) -> ctypes.c_void_p:
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def make_prompt(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, q_stride=None, k_stride=None,
+                v_stride=None, out_stride=None) -> Prompt:
+    """A prompt description; a stride that is not given is that of a contiguous tensor."""
+    hq, hkv, d = int(num_q_heads), int(num_kv_heads), int(head_dim)
+    return Prompt(int(num_seqs), int(total_tokens), hq, hkv, d, 0, hq * d if q_stride is None else int(q_stride),
+                  hkv * d if k_stride is None else int(k_stride), hkv * d if v_stride is None else int(v_stride),
+                  hq * d if out_stride is None else int(out_stride))
+
+
+def pkv_check_prompt(prompt: Prompt) -> int:
+    return load().pkv_check_prompt(ctypes.byref(prompt))
+
+
+def _seqs(cu_seqlens: torch.Tensor, num_seqs: int) -> ctypes.c_void_p:
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() != num_seqs + 1:
+        raise ValueError(f"cu_seqlens must have {num_seqs + 1} entries")
+    return _ptr(cu_seqlens, torch.int32, "cu_seqlens")
+
+
+def pkv_prompt_attention(prompt: Prompt, q, k, v, cu_seqlens, scale, ws, out, stream=None) -> None:
+    dev = q.device
+    _same_device(dev, k, v, cu_seqlens, ws, out)
+    with _on(dev):
+        check(load().pkv_prompt_attention(
+            ctypes.byref(prompt), _rows_ptr(q), _rows_ptr(k), _rows_ptr(v), _seqs(cu_seqlens, prompt.num_seqs), scale,
+            _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(), _rows_ptr(out), _stream(stream)),
+            "pkv_prompt_attention")
+
+
+def _start(start, num_seqs: int) -> ctypes.c_void_p:
+    if start is not None and start.numel() != num_seqs:
+        raise ValueError(f"start must have {num_seqs} entries")
+    return _ptr(start, torch.int32, "start")
+
+
+def _table(block_table: torch.Tensor, problem: Problem) -> ctypes.c_void_p:
+    if tuple(block_table.shape) != (problem.batch, problem.max_pages_per_seq):
+        raise ValueError(f"block_table must have shape ({problem.batch}, {problem.max_pages_per_seq})")
+    return _ptr(block_table, torch.int32, "block_table")
+
+
+def pkv_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws,
+                      stream=None) -> None:
+    dev = k.device
+    _same_device(dev, v, cu_seqlens, start, k_pool, v_pool, block_table, ws)
+    with _on(dev):
+        check(load().pkv_prompt_append(
+            ctypes.byref(problem), ctypes.byref(prompt), _rows_ptr(k), _rows_ptr(v),
+            _seqs(cu_seqlens, prompt.num_seqs), _start(start, prompt.num_seqs), _ptr(k_pool, torch.float16, "k_pool"),
+            _ptr(v_pool, torch.float16, "v_pool"), _table(block_table, problem), _num_sms(dev),
+            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "pkv_prompt_append")
+
+
+def pkv_q4_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, pool, block_table, ws,
+                         stream=None) -> None:
+    dev = k.device
+    _same_device(dev, v, cu_seqlens, start, pool, block_table, ws)
+    with _on(dev):
+        check(load().pkv_q4_prompt_append(
+            ctypes.byref(problem), ctypes.byref(prompt), _rows_ptr(k), _rows_ptr(v),
+            _seqs(cu_seqlens, prompt.num_seqs), _start(start, prompt.num_seqs), _ptr(pool, torch.uint8, "pool"),
+            _table(block_table, problem), _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)),
+            "pkv_q4_prompt_append")
+
+
+def pkv_q4_read(problem: Problem, prompt: Prompt, cu_seqlens, start, pool, block_table, k_out, v_out, ws,
+                stream=None) -> None:
+    dev = pool.device
+    _same_device(dev, k_out, v_out, cu_seqlens, start, block_table, ws)
+    with _on(dev):
+        check(load().pkv_q4_read(
+            ctypes.byref(problem), ctypes.byref(prompt), _seqs(cu_seqlens, prompt.num_seqs),
+            _start(start, prompt.num_seqs), _ptr(pool, torch.uint8, "pool"), _table(block_table, problem),
+            _rows_ptr(k_out), _rows_ptr(v_out), _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+            _stream(stream)), "pkv_q4_read")
+
+
+def pkv_q4_pool_bytes(problem: Problem) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().pkv_q4_pool_bytes(ctypes.byref(problem), ctypes.byref(n)), "pkv_q4_pool_bytes")
+    return int(n.value)
+
+
+def pkv_q4_workspace_bytes(problem: Problem, num_sms: int | None = None) -> int:
+    """Bytes of the workspace of a 4-bit decode step (num_sms None: that of the current device)."""
+    if num_sms is None:
+        num_sms = _num_sms(torch.device("cuda", torch.cuda.current_device()))
+    n = ctypes.c_size_t(0)
+    check(load().pkv_q4_workspace_bytes(ctypes.byref(problem), int(num_sms), ctypes.byref(n)),
+          "pkv_q4_workspace_bytes")
+    return int(n.value)
+
+
+def pkv_q4_decode_step(problem: Problem, q, pool, block_table, seq_lens, scale, ws, out, stream=None) -> None:
+    dev = q.device
+    _same_device(dev, pool, block_table, seq_lens, ws, out)
+    with _on(dev):
+        check(load().pkv_q4_decode_step(
+            ctypes.byref(problem), _ptr(q, torch.float16, "q"), _ptr(pool, torch.uint8, "pool"),
+            _table(block_table, problem), _ptr(seq_lens, torch.int32, "seq_lens"), scale, _num_sms(dev),
+            _ptr(ws, torch.uint8, "ws"), ws.numel(), _ptr(out, torch.float16, "out"), _stream(stream)),
+            "pkv_q4_decode_step")
+
+
+def pkv_q4_decode_step_append(problem: Problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out,
+                              stream=None) -> None:
+    dev = q.device
+    _same_device(dev, k_new, v_new, pool, block_table, seq_lens, ws, out)
+    with _on(dev):
+        check(load().pkv_q4_decode_step_append(
+            ctypes.byref(problem), _ptr(q, torch.float16, "q"), _ptr(k_new, torch.float16, "k_new"),
+            _ptr(v_new, torch.float16, "v_new"), _ptr(pool, torch.uint8, "pool"), _table(block_table, problem),
+            _ptr(seq_lens, torch.int32, "seq_lens"), scale, _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+            _ptr(out, torch.float16, "out"), _stream(stream)), "pkv_q4_decode_step_append")
+
+
+# ------------------------------------------------------------------------------- the same, described by the tensors
+def _torch_stream(stream, device) -> torch.cuda.Stream | None:
+    """`stream` as a torch stream where it is not the current one (what the call allocates is recorded on it)."""
+    if stream is None:
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return None if stream == torch.cuda.current_stream(device) else stream
+
+
+def _scratch(nbytes: int, ws, device, stream):
+    """The caller's workspace, or one for this call alone."""
+    if ws is not None:
+        return ws
+    other = _torch_stream(stream, device)
+    if other is None:
+        return alloc_workspace(nbytes, device)
+    with torch.cuda.stream(other):
+        return alloc_workspace(nbytes, device)
+
+
+def _new(shape, device, stream) -> torch.Tensor:
+    out = torch.empty(shape, dtype=torch.float16, device=device)
+    other = _torch_stream(stream, device)
+    if other is not None:
+        other.wait_stream(torch.cuda.current_stream(device))  # the memory may still be read on the current stream
+        out.record_stream(other)
+    return out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float | None = None, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Causal grouped-query attention over packed prompts (include/pkv.h, pkv_prompt_attention). Returns out.
+
+    q [tokens, Hq, d], k, v [tokens, Hkv, d] fp16, the heads of a token contiguous and the tokens at any distance (q, k
+    and v may be slices of one projection); cu_seqlens [num_seqs + 1] int32 on the device. Rows of an `out` given by
+    the caller that belong to no sequence keep their values; in one made here they are undefined.
+    """
+    qs = _rows(q, "q")
+    t, hq, d = q.shape
+    ks = _rows(k, "k", None, t, d)
+    hkv = k.shape[1]
+    vs = _rows(v, "v", hkv, t, d)
+    dev = q.device
+    with _on(dev):
+        if out is None:
+            out = _new((t, hq, d), dev, stream)
+        prompt = Prompt(cu_seqlens.numel() - 1, t, hq, hkv, d, 0, qs, ks, vs, _rows(out, "out", hq, t, d))
+        pkv_prompt_attention(prompt, q, k, v, cu_seqlens, 1.0 / math.sqrt(d) if scale is None else scale,
+                             _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), out, stream)
+    return out
+
+
+def prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, k_pool: torch.Tensor,
+                  v_pool: torch.Tensor, block_table: torch.Tensor, start: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, stream=None) -> None:
+    """Packed prompts' K/V into the FP16 pages (include/pkv.h, pkv_prompt_append).
+
+    k, v [tokens, Hkv, d] as for prompt_attention; k_pool, v_pool [num_pages, page_size, Hkv, d]; block_table
+    [num_seqs, max_pages] int32; start [num_seqs] int32: tokens that each row holds already (None: none).
+    """
+    ks = _rows(k, "k")
+    t, hkv, d = k.shape
+    vs = _rows(v, "v", hkv, t, d)
+    if k_pool.dim() != 4 or k_pool.shape[2:] != (hkv, d) or v_pool.shape != k_pool.shape:
+        raise ValueError(f"k_pool and v_pool must be [num_pages, page_size, {hkv}, {d}]")
+    b, pages = block_table.shape
+    problem = make_problem(b, hkv, hkv, d, k_pool.shape[1], k_pool.shape[0], pages)
+    prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
+    with _on(k.device):
+        pkv_prompt_append(problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table,
+                          _scratch(PKV_PROMPT_WS_BYTES, ws, k.device, stream), stream)
+
+
+def _check_pool(pool: torch.Tensor) -> int:
+    if pool.dim() != 3 or pool.dtype != torch.uint8 or pool.shape[2] != PKV_Q4_BLOCK_BYTES:
+        raise ValueError(f"pool must be a uint8 tensor [num_pages, Hkv, {PKV_Q4_BLOCK_BYTES}]")
+    return pool.shape[1]
+
+
+def q4_problem(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor) -> Problem:
+    """The problem of a decode step over 4-bit pages: q [B, Hq, d], pool [num_pages, Hkv, block], block_table."""
+    hkv = _check_pool(pool)
+    b, hq, d = q.shape
+    return make_problem(b, hq, hkv, d, 16, pool.shape[0], block_table.shape[1])
+
+
+def q4_prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
+                     block_table: torch.Tensor, start: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """Packed prompts' K/V quantised into 4-bit pages (include/pkv.h, pkv_q4_prompt_append); arguments as for
+    prompt_append, pool [num_pages, Hkv, PKV_Q4_BLOCK_BYTES] uint8."""
+    ks = _rows(k, "k")
+    t, hkv, d = k.shape
+    vs = _rows(v, "v", hkv, t, d)
+    if _check_pool(pool) != hkv:
+        raise ValueError(f"pool has {pool.shape[1]} KV heads, k has {hkv}")
+    b, pages = block_table.shape
+    problem = make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages)
+    prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
+    with _on(k.device):
+        pkv_q4_prompt_append(problem, prompt, k, v, cu_seqlens, start, pool, block_table,
+                             _scratch(PKV_PROMPT_WS_BYTES, ws, k.device, stream), stream)
+
+
+def q4_read(cu_seqlens: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor,
+            start: torch.Tensor | None = None, total_tokens: int | None = None, k_out: torch.Tensor | None = None,
+            v_out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Tokens of 4-bit pages as packed fp16 rows (include/pkv.h, pkv_q4_read). Returns k_out, v_out
+    [total_tokens, Hkv, d]; give either both of them or total_tokens."""
+    hkv, d = _check_pool(pool), 128
+    dev = pool.device
+    b, pages = block_table.shape
+    with _on(dev):
+        if k_out is None and v_out is None:
+            if total_tokens is None:
+                raise ValueError("give k_out and v_out, or total_tokens")
+            k_out = _new((int(total_tokens), hkv, d), dev, stream)
+            v_out = _new((int(total_tokens), hkv, d), dev, stream)
+        elif k_out is None or v_out is None:
+            raise ValueError("give both of k_out and v_out, or neither")
+        t = k_out.shape[0]
+        if total_tokens is not None and total_tokens != t:
+            raise ValueError(f"k_out has {t} rows, total_tokens is {total_tokens}")
+        prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, _rows(k_out, "k_out", hkv, t, d),
+                        _rows(v_out, "v_out", hkv, t, d), hkv * d)
+        pkv_q4_read(make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages), prompt, cu_seqlens, start, pool,
+                    block_table, k_out, v_out, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    return k_out, v_out
+
+
+def q4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+              k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, scale: float | None = None,
+              out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One decode step over 4-bit pages (include/pkv.h, pkv_q4_decode_step; with k_new and v_new [B, Hkv, d],
+    pkv_q4_decode_step_append). Returns out [B, Hq, d] fp16.
+
+    q [B, Hq, d] fp16; pool [num_pages, Hkv, PKV_Q4_BLOCK_BYTES] uint8; block_table [B, max_pages] int32; seq_lens [B]
+    int32 on the device. Keep ws (pkv_q4_workspace_bytes, alloc_workspace) over the steps of a loop.
+    """
+    problem = q4_problem(q, pool, block_table)
+    b, hq, d = q.shape
+    if seq_lens.numel() != b:
+        raise ValueError(f"seq_lens must have {b} entries")
+    if (k_new is None) != (v_new is None):
+        raise ValueError("give both of k_new and v_new, or neither")
+    dev = q.device
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(dev):
+        if out is None:
+            out = _new((b, hq, d), dev, stream)
+        elif out.shape != q.shape:
+            raise ValueError(f"out must have shape {tuple(q.shape)}")
+        if ws is None:
+            ws = _scratch(pkv_q4_workspace_bytes(problem, _num_sms(dev)), None, dev, stream)
+        if k_new is None:
+            pkv_q4_decode_step(problem, q, pool, block_table, seq_lens, scale, ws, out, stream)
+        else:
+            if k_new.shape != (b, pool.shape[1], d) or v_new.shape != k_new.shape:
+                raise ValueError(f"k_new and v_new must have shape {(b, pool.shape[1], d)}")
+            pkv_q4_decode_step_append(problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out, stream)
+    return out
