@@ -132,7 +132,8 @@ extern "C" int pkv_prompt_attention(const pkv_prompt* pm, const void* q, const v
     p.total_tokens = pm->total_tokens;
     p.Hq = pm->num_q_heads;
     p.Hkv = pm->num_kv_heads;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // above 0, so that a masked score of -inf stays one; 1e-30 times any fp16 score is a weight of 1 all the same
+    p.scale_log2 = std::fmax(scale * 1.4426950408889634f, 1e-30f);
     return cuda_rc(launch_prompt_attention(p, num_sms, stream));
 }
 

@@ -1,17 +1,81 @@
-// Causal grouped-query attention over packed prompts (include/pkv.h, pkv_prompt_attention).
+// Causal grouped-query attention over packed prompts on the 5th-generation tensor cores (include/pkv.h,
+// pkv_prompt_attention).
+//
+// For token i of a sequence and query head hq of KV head h: out = sum_{j <= i} p_j v_j / sum p_j with p_j = 2^(x_j - m),
+// x_j = scale * log2(e) * q_i.k_j, one pass over the keys with a running m and sum (online softmax).
+//
+// Work: a tile is 128 rows of the score matrix: the G query heads of 128 / G consecutive tokens of one KV head (row =
+// token * G + head, which one TMA box of q gives), so that short and ragged prompts fill tiles G times better than
+// tiles of one head would and K and V are read once for all G heads. A CTA works on two neighbouring tiles (A, B) at
+// a time, over 128 keys per step. Causality cuts the keys of a tile at its last token, so only its last step is
+// masked, and that step's matrix products are cut to the 16-key steps that it needs.
+//
+// One CTA per SM, persistent; pairs of tiles are claimed from an atomic counter, longest sequences and latest tokens
+// first. Warp roles:
+//   warps 0-3, 4-7  softmax of tile A, of tile B: thread = row. The row's 128 scores come from TMEM into registers
+//                   (tcgen05.ld), the weights go back to TMEM as fp16 over the scores. The running maximum is raised
+//                   only when a row's scores exceed it by more than 8 (in log2): weights then reach 2^8 at most, far
+//                   inside fp16, and the accumulator is rescaled (by these warps) in the first steps only. Finally
+//                   they divide, round and store the output rows.
+//   warp 8          one lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P from
+//                   TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
+//                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
+//   warp 9          one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
+//   warp 10         claims work, one pair ahead, and publishes it.
+// TMEM (512 columns): S_A, S_B (P in the first 64 columns of each), O_A, O_B. Instructions of one thread run in order,
+// so S(j+1) may be issued over P(j) right after PV(j).
+//
+// A value that a row does not attend to is multiplied by a weight of 0, which does not remove an infinity or a NaN of
+// V. Output rows that are not finite are therefore computed again by a warp that reads the row's own keys alone
+// (row_attention): exact in every case, and costs nothing where the data are finite.
+//
+// Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
+// have in flight, and the CTA frees its TMEM and returns.
+#include <cuda.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 
 #include "pkv_internal.h"
-#include "pkv_ptx.cuh"
+#include "pkv_tcgen05.cuh"
+#include "pkv_wait.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 8;
+constexpr int kRows = 128;                   // rows of a tile, keys of a step
+constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two boxes of 64 dims
+constexpr int kBoxBytes = kTileBytes / 2;
+constexpr int kStages = 4;
+constexpr int kSlots = 1;  // a CTA claims its next pair when its softmax begins the current one
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
+constexpr float kRaise = 8.f;                // log2 by which scores may exceed the running maximum before it is raised
 
+struct Work {
+    int32_t first, n, t0, h;  // sequence's first packed row and length; first token of tile A; KV head (-1: no more work)
+};
+
+constexpr int off_q = 0;
+constexpr int off_ring = 2 * kTileBytes;
+constexpr int off_prefix = off_ring + kStages * kTileBytes;  // work pairs before the i-th sequence of the order
+constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
+constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
+constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
+constexpr int off_bars = off_hist + 32 * 4;
+constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 2 + 2 + 1;
+constexpr int off_misc = off_bars + kBars * 8;  // abort flag, TMEM address
+constexpr int kSmem = off_misc + 16 + 1024;     // slack to align the base to 1024 bytes
+static_assert(off_order % 16 == 0 && off_work % 16 == 0 && off_bars % 8 == 0, "alignment");
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Params {
+    CUtensorMap q, k, v;
+    PromptParams p;
+};
+
+// ---- one row on the CUDA cores ------------------------------------------------------------------------------------
 struct Row4 {
     float x[4];
 };
@@ -24,7 +88,7 @@ __device__ __forceinline__ Row4 load4(const __half* p) {
 }
 
 // One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, lane l holds dims 4l..4l+3.
-__device__ __forceinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int lane) {
+__device__ __noinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int lane) {
     const int h = hq / (p.Hq / p.Hkv);
     const __half* k = static_cast<const __half*>(p.k) + first * p.k_stride + h * kHeadDim + lane * 4;
     const __half* v = static_cast<const __half*>(p.v) + first * p.v_stride + h * kHeadDim + lane * 4;
@@ -43,34 +107,554 @@ __device__ __forceinline__ void row_attention(const PromptParams& p, int64_t fir
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * b.x[i];
         m = mn;
+        if (isnan(l)) break;  // the row's result is NaN whatever follows
     }
-    const float inv = 1.f / l;
+    const float inv = isnan(l) ? l : 1.f / l;
     uint2 u;
     u.x = pack_half2(o[0] * inv, o[1] * inv);
     u.y = pack_half2(o[2] * inv, o[3] * inv);
     *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (first + pos) * p.out_stride + hq * kHeadDim + lane * 4) = u;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) prompt_attention_kernel(const PromptParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int s = blockIdx.y; s < p.num_seqs; s += gridDim.y) {
-        const int first = p.cu_seqlens[s], last = p.cu_seqlens[s + 1];
-        if (first < 0 || last < first || last > p.total_tokens) {
-            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&p.hdr->status, PKV_STATUS_BAD_LEN);
-            continue;
+// ---- the tensor-core kernel ---------------------------------------------------------------------------------------
+__device__ __forceinline__ int tiles_of(int n, int pair_tokens) { return (n + pair_tokens - 1) / pair_tokens; }
+
+// Tokens that tile x (0: A, 1: B) of a work pair ends at (its keys are the tokens before that); <= its start: no row.
+__device__ __forceinline__ int tile_end(const Work& w, int x, int tokens) {
+    const int start = w.t0 + x * tokens;
+    return start < w.n ? min(start + tokens, w.n) : 0;
+}
+
+// Length of sequence s, 0 where its bounds are not ordered inside [0, total_tokens].
+__device__ __forceinline__ int seq_length(const PromptParams& p, int s, int& first, bool& bad) {
+    first = p.cu_seqlens[s];
+    const int last = p.cu_seqlens[s + 1];
+    bad = first < 0 || last < first || last > p.total_tokens;
+    return bad ? 0 : last - first;
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Params prm) {
+    constexpr int kTokens = kRows / G;  // tokens of a tile
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const PromptParams& p = prm.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + off_bars);
+    uint64_t* kv_empty = kv_full + kStages;
+    uint64_t* w_full = kv_empty + kStages;
+    uint64_t* w_empty = w_full + kSlots;
+    uint64_t* q_full = w_empty + kSlots;  // [2], like those below: tile A, tile B
+    uint64_t* q_empty = q_full + 2;
+    uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
+    uint64_t* p_full = s_full + 2;        // its weights are
+    uint64_t* o_full = p_full + 2;        // its accumulator is complete
+    uint64_t* drain = o_full + 2;
+    Work* work = reinterpret_cast<Work*>(smem + off_work);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
+    const WaitCtx ctx{abort_flag, &p.hdr->status};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
         }
-        const int64_t rows = (int64_t)(last - first) * p.Hq;
-        for (int64_t r = (int64_t)blockIdx.x * kWarps + warp; r < rows; r += (int64_t)gridDim.x * kWarps)
-            row_attention(p, first, (int)(r / p.Hq), (int)(r % p.Hq), lane);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], 10);  // 8 softmax warps, the MMA warp, the loader
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);  // one arrival a warp
+            mbar_init(&o_full[i], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
     }
+    if (warp == 8) tmem_alloc(tmem_at, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    if (warp >= 8) {
+        regs_shrink<kOtherRegs>();
+        if (warp == 10) {
+            // ---------------------------------------------------------------------------------- work claims
+            // Sequences in descending order of the power of two of their tile pairs; within one, the last tokens
+            // (most keys) first.
+            int* prefix = reinterpret_cast<int*>(smem + off_prefix);
+            uint16_t* order = reinterpret_cast<uint16_t*>(smem + off_order);
+            int* hist = reinterpret_cast<int*>(smem + off_hist);
+            const int chunks = (p.num_seqs + 31) / 32;
+            hist[lane] = 0;
+            __syncwarp();
+            for (int c = 0; c < chunks; ++c) {
+                const int s = c * 32 + lane;
+                int first, n = 0;
+                bool bad = false;
+                if (s < p.num_seqs) n = seq_length(p, s, first, bad);
+                if (bad && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
+                const int t = tiles_of(n, 2 * kTokens);
+                if (t > 0) atomicAdd(&hist[__clz(t)], 1);
+            }
+            __syncwarp();
+            int incl = hist[lane];  // by leading zeros: the most tiles first
+            const int mine = incl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int seqs = __shfl_sync(0xffffffffu, incl, 31);
+            __syncwarp();
+            hist[lane] = incl - mine;
+            __syncwarp();
+            for (int c = 0; c < chunks; ++c) {
+                const int s = c * 32 + lane;
+                int first, n = 0;
+                bool bad;
+                if (s < p.num_seqs) n = seq_length(p, s, first, bad);
+                const int t = tiles_of(n, 2 * kTokens);
+                const int key = t > 0 ? __clz(t) : 32;
+                const unsigned same = __match_any_sync(0xffffffffu, key);
+                const int base = t > 0 ? hist[key] : 0;
+                __syncwarp();
+                if (t > 0) {
+                    order[base + __popc(same & ((1u << lane) - 1))] = (uint16_t)s;
+                    if (lane == __ffs(same) - 1) hist[key] = base + __popc(same);
+                }
+                __syncwarp();
+            }
+            int run = 0;
+            for (int c = 0; c * 32 < seqs; ++c) {
+                const int i = c * 32 + lane;
+                int first, t = 0;
+                bool bad;
+                if (i < seqs) t = tiles_of(seq_length(p, order[i], first, bad), 2 * kTokens);
+                int sum = t;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                if (i < seqs) prefix[i] = run + sum - t;
+                run += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            __syncwarp();
+            const int64_t total = (int64_t)run * p.Hkv;
+            for (int k = 0;; ++k) {
+                int64_t t = blockIdx.x;  // the first pair of a CTA is its index, later ones come from the counter
+                if (k > 0) {
+                    uint32_t c = 0;
+                    if (lane == 0) c = atomicAdd(&p.hdr->queue_head, 1u);
+                    t = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, c, 0);
+                }
+                Work w{0, 0, 0, -1};
+                if (t < total) {
+                    const int pair = (int)(t / p.Hkv);
+                    int lo = 0, hi = seqs - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (prefix[mid] <= pair)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    bool bad;
+                    w.n = seq_length(p, order[lo], w.first, bad);
+                    w.t0 = (tiles_of(w.n, 2 * kTokens) - 1 - (pair - prefix[lo])) * 2 * kTokens;
+                    w.h = (int)(t - (int64_t)pair * p.Hkv);
+                }
+                const int slot = k % kSlots;
+                if (!warp_wait(&w_empty[slot], ((k / kSlots) & 1) ^ 1, ctx)) break;
+                if (lane == 0) {
+                    work[slot] = w;
+                    mbar_arrive(&w_full[slot]);
+                }
+                __syncwarp();
+                if (w.h < 0) break;
+            }
+            if (lane == 0) {  // the last CTA to end re-arms the counter for the next call
+                __threadfence();
+                if (atomicAdd(&p.hdr->ctas_done, 1u) == gridDim.x - 1) {
+                    atomicExch(&p.hdr->queue_head, 0u);
+                    atomicExch(&p.hdr->ctas_done, 0u);
+                }
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------------------------------------------- copies
+            if (lane == 0) {
+                prefetch_tensormap(&prm.q);
+                prefetch_tensormap(&prm.k);
+                prefetch_tensormap(&prm.v);
+            }
+            uint64_t keep, stream;
+            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream));
+            int seq = 0, nq[2] = {0, 0};
+            bool stop = false;
+            for (int k = 0; !stop; ++k) {
+                const int slot = k % kSlots;
+                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
+                const Work w = work[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                if (w.h < 0) break;
+                const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
+                const int steps = (end + kRows - 1) / kRows;
+                auto load_q = [&](int x) {
+                    if (tile_end(w, x, kTokens) == 0) return true;
+                    if (!warp_wait(&q_empty[x], (nq[x] & 1) ^ 1, ctx)) return false;
+                    if (lane == 0) {
+                        uint8_t* dst = smem + off_q + x * kTileBytes;
+                        mbar_arrive_expect_tx(&q_full[x], kTileBytes);
+                        for (int b = 0; b < 2; ++b)
+                            tma_load_3d(dst + b * kBoxBytes, &prm.q, b * 64, w.h * G, w.first + w.t0 + x * kTokens,
+                                        &q_full[x], stream);
+                    }
+                    __syncwarp();
+                    ++nq[x];
+                    return true;
+                };
+                auto load_kv = [&](const CUtensorMap* map, int j) {
+                    const int st = seq % kStages;
+                    if (!warp_wait(&kv_empty[st], ((seq / kStages) & 1) ^ 1, ctx)) return false;
+                    if (lane == 0) {
+                        uint8_t* dst = smem + off_ring + st * kTileBytes;
+                        mbar_arrive_expect_tx(&kv_full[st], kTileBytes);
+                        for (int b = 0; b < 2; ++b)
+                            tma_load_3d(dst + b * kBoxBytes, map, b * 64, w.h, w.first + j * kRows, &kv_full[st], keep);
+                    }
+                    __syncwarp();
+                    ++seq;
+                    return true;
+                };
+                stop = !load_q(0) || !load_kv(&prm.k, 0) || !load_q(1) || !load_kv(&prm.v, 0);
+                for (int j = 1; j < steps && !stop; ++j) stop = !load_kv(&prm.k, j) || !load_kv(&prm.v, j);
+            }
+            // every copy that this warp issued lands before the CTA may end
+            for (int j = max(0, seq - kStages); j < seq; ++j) warp_drain(&kv_full[j % kStages], (j / kStages) & 1);
+            for (int x = 0; x < 2; ++x)
+                if (nq[x] > 0) warp_drain(&q_full[x], (nq[x] - 1) & 1);
+        } else if (warp == 8) {
+            // ------------------------------------------------------------------------- matrix instructions
+            int kv = 0;                        // ring position of the next K tile of the current work
+            int nq[2] = {0, 0}, np[2] = {0, 0};  // tiles begun, steps of softmax taken
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int slot = k % kSlots;
+                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
+                const Work w = work[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                if (w.h < 0) break;
+                const int end0 = tile_end(w, 0, kTokens), end1 = tile_end(w, 1, kTokens);
+                const int steps = (max(end0, end1) + kRows - 1) / kRows;
+                // ring positions: K_j at kv + 2j, V_j one behind it
+                auto stage_addr = [&](int pos) { return smem_addr(smem + off_ring + (pos % kStages) * kTileBytes); };
+                auto wait_stage = [&](int pos) { return warp_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
+                // keys of step j that tile x needs (0: none)
+                auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
+                auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
+                    const int n = (keys(x, j) + 15) & ~15;
+                    if (n == 0) return;
+                    if (lane == 0) {
+                        const uint32_t idesc = mma_idesc(n, false);
+                        const uint32_t qa = smem_addr(smem + off_q + x * kTileBytes), ka = stage_addr(kv + 2 * j);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t o = (i >> 2) * kBoxBytes + (i & 3) * 32;
+                            mma_ss(tmem + x * 128, smem_desc_k_major(qa + o), smem_desc_k_major(ka + o), idesc, i > 0);
+                        }
+                        mma_commit(&s_full[x]);
+                        if (keys(x, j + 1) == 0) mma_commit(&q_empty[x]);  // the tile's last use of its queries
+                    }
+                    __syncwarp();
+                };
+                auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
+                    const int n = (keys(x, j) + 15) >> 4;
+                    if (n == 0) return true;
+                    if (!warp_wait(&p_full[x], np[x] & 1, ctx)) return false;
+                    ++np[x];
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t idesc = mma_idesc(kHeadDim, true);
+                        const uint32_t va = stage_addr(kv + 2 * j + 1);
+                        for (int i = 0; i < n; ++i)
+                            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, smem_desc_mn_major(va + i * 2048, kBoxBytes),
+                                   idesc, j > 0 || i > 0);
+                        if (keys(x, j + 1) == 0) mma_commit(&o_full[x]);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto release = [&](int pos) {
+                    if (lane == 0) mma_commit(&kv_empty[pos % kStages]);
+                    __syncwarp();
+                };
+                ok = wait_stage(kv);
+                for (int x = 0; x < 2 && ok; ++x) {
+                    if (keys(x, 0) == 0) continue;
+                    ok = warp_wait(&q_full[x], nq[x] & 1, ctx);
+                    ++nq[x];
+                    tc_fence_after();
+                    if (ok) scores(x, 0);
+                }
+                if (!ok) break;
+                release(kv);
+                for (int j = 0; j < steps && ok; ++j) {
+                    ok = wait_stage(kv + 2 * j + 1) && values(0, j);
+                    if (ok && j + 1 < steps) {
+                        ok = wait_stage(kv + 2 * j + 2);
+                        if (ok) scores(0, j + 1);
+                    }
+                    ok = ok && values(1, j);
+                    if (!ok) break;
+                    release(kv + 2 * j + 1);
+                    if (j + 1 < steps) {
+                        scores(1, j + 1);
+                        release(kv + 2 * j + 2);
+                    }
+                }
+                kv += 2 * steps;
+            }
+            // every matrix instruction has completed before the TMEM is freed and the CTA ends
+            if (lane == 0) mma_commit(drain);
+            __syncwarp();
+            warp_drain(drain, 0);
+        }
+    } else {
+        // ---------------------------------------------------------------------------- softmax and output rows
+        regs_grow<kSoftmaxRegs>();
+        const int x = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + x * 128, o_at = tmem + lanes + 256 + x * 128;
+        const float sl2 = p.scale_log2;
+        const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
+        int ns = 0, no = 0;  // steps, tiles taken
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kSlots;
+            if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
+            const Work w = work[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[slot]);
+            if (w.h < 0) break;
+            const int end = tile_end(w, x, kTokens);
+            if (end == 0) continue;
+            const int steps = (end + kRows - 1) / kRows;
+            const int token = w.t0 + x * kTokens + row / G;
+            float m = -INFINITY, l = 0.f;  // running maximum of the raw scores (scale >= 0 keeps their order)
+            for (int j = 0; j < steps; ++j) {
+                if (!warp_wait(&s_full[x], ns & 1, ctx)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                tc_fence_after();
+                float s[kRows];
+                uint32_t* su = reinterpret_cast<uint32_t*>(s);
+                const int last = end - j * kRows;  // keys of this step, at least 1
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < last) tmem_ld32(s_at + c * 32, su + c * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_use32(su + c * 32);
+                if (j == steps - 1) {  // the step with the diagonal and the sequence's end
+                    const int lim = min(token, end - 1) - j * kRows;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        if (i > lim) s[i] = -INFINITY;
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kRows; i += 4) {
+                    mx0 = fmaxf(fmaxf(mx0, s[i]), s[i + 1]);
+                    mx1 = fmaxf(fmaxf(mx1, s[i + 2]), s[i + 3]);
+                }
+                const float mx = fmaxf(mx0, mx1);
+                const bool raise = (mx - m) * sl2 > kRaise || m == -INFINITY;
+                if (__any_sync(0xffffffffu, raise && j > 0)) {
+                    float f = 1.f;
+                    if (raise) {
+                        const float mn = fmaxf(m, mx);
+                        f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * sl2);
+                        m = mn;
+                    }
+                    if (j > 0) {
+                        l *= f;
+                        const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + c * 32, o);
+                            tmem_wait_ld();
+                            tmem_use32(o);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float a, b;
+                                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), ff),
+                                             a, b);
+                                o[i] = __float_as_uint(a);
+                                o[i + 1] = __float_as_uint(b);
+                            }
+                            tmem_st32(o_at + c * 32, o);
+                        }
+                    }
+                } else if (raise) {
+                    m = fmaxf(m, mx);
+                }
+                const float ref = m == -INFINITY ? 0.f : -m * sl2;
+                const uint64_t refx2 = pack_f32x2(ref, ref);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c * 32 < last) {
+                        uint32_t ph[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sl2x2, refx2), a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            if (i & 1)
+                                sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+                            else
+                                sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+                            ph[i] = pack_half2(a, b);
+                        }
+                        tmem_st16(s_at + c * 16, ph);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+                float a, b;
+                unpack_f32x2(add_f32x2(sum0, sum1), a, b);
+                l += a + b;
+            }
+            if (!ok) break;
+            if (!warp_wait(&o_full[x], no & 1, ctx)) break;
+            ++no;
+            tc_fence_after();
+            const bool mine = token < w.n;
+            const float inv = 1.f / l;
+            float probe = 0.f;  // stays 0 while every value is finite
+            __half* dst = static_cast<__half*>(p.out) + (int64_t)(w.first + token) * p.out_stride +
+                          (w.h * G + row % G) * kHeadDim;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_at + c * 32, o);
+                tmem_wait_ld();
+                tmem_use32(o);
+                uint32_t y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
+                    probe = fmaf(a, 0.f, fmaf(b, 0.f, probe));
+                    y[i] = pack_half2(a, b);
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4*>(dst)[c * 4 + i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                }
+            }
+            tc_fence_before();  // the reads of O are done before the next tile's first weights are announced
+            unsigned again = __ballot_sync(0xffffffffu, mine && probe != 0.f);
+            while (again) {  // rows that are not finite: from their own keys alone
+                const int r = (row & ~31) + __ffs(again) - 1;
+                again &= again - 1;
+                __syncwarp();
+                row_attention(p, w.first, w.t0 + x * kTokens + r / G, w.h * G + r % G, lane);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// Packed rows [tokens][heads][128] at `stride` elements a token as the 3-D tensor (d, heads, tokens), box (64, heads of
+// the box, tokens of the box), 128-byte swizzle: one box is half of a tile's dims.
+bool encode(CUtensorMap* map, const void* rows, int heads, int64_t tokens, int64_t stride, int box_heads) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)kRowBytes, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)(kRows / box_heads)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(rows), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G>
+int launch(const Params& prm, int num_sms, cudaStream_t stream) {
+    static int configured_mask = 0;  // one bit per device ordinal (< 32)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 32 || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+        cudaFuncAttributes a{};
+        cudaError_t e = cudaFuncGetAttributes(&a, prompt_kernel<G>);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares come out of what the launch gives them
+        if (a.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(prompt_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
+    }
+    // at most this many pairs of tiles: every sequence begins one, and the rest are full
+    const int64_t pairs = ((int64_t)prm.p.total_tokens * G / (2 * kRows) + std::min(prm.p.num_seqs, prm.p.total_tokens)) * prm.p.Hkv;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(pairs, num_sms));
+    prompt_kernel<G><<<grid, kThreads, kSmem, stream>>>(prm);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 int launch_prompt_attention(const PromptParams& p, int num_sms, void* stream) {
-    const dim3 grid(num_sms * 8, std::min(p.num_seqs, 64));
-    prompt_attention_kernel<<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    Params prm;
+    prm.p = p;
+    const int g = p.Hq / p.Hkv;
+    if (!encode(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g) ||
+        !encode(&prm.k, p.k, p.Hkv, p.total_tokens, p.k_stride, 1) ||
+        !encode(&prm.v, p.v, p.Hkv, p.total_tokens, p.v_stride, 1))
+        return cudaErrorInvalidValue;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (g) {
+        case 1: return launch<1>(prm, num_sms, s);
+        case 2: return launch<2>(prm, num_sms, s);
+        case 4: return launch<4>(prm, num_sms, s);
+        case 8: return launch<8>(prm, num_sms, s);
+        case 16: return launch<16>(prm, num_sms, s);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace pkv
