@@ -474,7 +474,7 @@ int pkv_q4_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size_t* 
  * One decode step over 4-bit pages: as pkv_decode_step, with q, block_table, seq_lens and out of the same layouts and
  * attention over the values that the codes stand for (the products take the codes as they are; scales and offsets are
  * applied in fp32). There is no plan: the division of the step's pages over the GPU is worked out on the device from
- * seq_lens, so one captured graph serves every step of a batch. scale may be any finite number. A row of length 0
+ * seq_lens, so one captured graph serves every step of a batch. |scale| <= 1e12. A row of length 0
  * gets 0. Errors the kernels detect: PKV_STATUS_BAD_PAGE (a page outside the pool: its tokens are left out),
  * PKV_STATUS_BAD_LEN (the row counts as empty), PKV_STATUS_TIMEOUT.
  */

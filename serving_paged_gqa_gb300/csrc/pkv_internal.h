@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include <cuda.h>
+#include <vector_types.h>
 
 #include "pkv.h"
 
@@ -105,6 +106,9 @@ struct Q4Params {
     const int32_t* seq_lens;
     void* out;
     pkv_ws_header* hdr;
+    uint32_t* counters;  // arrivals of the pieces of a (row, KV head), by its first piece; zero between steps
+    float2* ml;          // (m, l) per state
+    float* acc;          // float [state][d]
     int32_t B, Hq, Hkv, num_pages, max_pages;
     float scale_log2;
 };

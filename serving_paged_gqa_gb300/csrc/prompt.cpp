@@ -64,7 +64,7 @@ int q4_step(const pkv_problem* pr, const void* q, const void* k_new, const void*
     int rc = pkv_q4_workspace_bytes(pr, num_sms, &need);
     if (rc == PKV_OK) rc = check_ws(ws, ws_bytes, need);
     if (rc != PKV_OK) return rc;
-    if (!std::isfinite(scale)) return PKV_E_INVAL;
+    if (!(std::fabs(scale) <= 1e12f)) return PKV_E_INVAL;  // times a group's scale and 2^24 it stays inside fp32
     if (pr->batch == 0) return PKV_OK;
     if (!q || !pool || !block_table || !seq_lens_dev || !out) return PKV_E_NULLPTR;
     if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
