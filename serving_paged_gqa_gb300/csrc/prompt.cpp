@@ -84,7 +84,9 @@ int q4_step(const pkv_problem* pr, const void* q, const void* k_new, const void*
     p.Hkv = pr->num_kv_heads;
     p.num_pages = pr->num_pages;
     p.max_pages = pr->max_pages_per_seq;
+    // not 0, so that a masked score of -inf stays one (see pkv_prompt_attention)
     p.scale_log2 = scale * 1.4426950408889634f;
+    if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = 1e-30f;
     return cuda_rc(launch_q4_decode(p, num_sms, stream));
 }
 

@@ -6,10 +6,10 @@
 //   q.k_j   = sum_g scale_jg (q.code_jg) + offset_jg (sum of q over the group)
 //   out     = sum_g sum_j (w_j scale_jg) code_jg + sum_j w_j offset_jg
 // so the products (mma.sync m16n8k16, tokens or dims on the 16-row side, the G <= 16 query heads on the 8-column side)
-// take the codes as they lie in memory: one mask makes two codes into two fp16 subnormals (q4.cuh), no conversion. The
-// weights w_j scale_jg are rounded to fp16 once, relative to R_g, the largest V scale that the warp has met in the
-// group (kept like a running maximum), so that V of any magnitude keeps its 11 bits. tcgen05 needs 64 or 128 rows of
-// query heads, of which a KV head has G.
+// take the codes as they lie in memory: one mask makes two codes into two fp16 subnormals (q4.cuh), no conversion.
+// tcgen05 needs 64 or 128 rows of query heads, of which a KV head has G. The weights w_j scale_jg are rounded to fp16
+// once; the exponent that w_j is taken relative to includes V's scale (ref, below), so that V of any magnitude keeps
+// fp16's 11 bits.
 //
 // Bound: HBM; a (token, KV head) is 144 bytes against 512 in fp16. A unit is 4 pages (64 tokens) of one (row, KV head),
 // four bulk copies of 2304 bytes into one ring stage, and goes to one consumer warp.
@@ -37,7 +37,9 @@ namespace {
 constexpr int kUnitPages = 4;
 constexpr int kUnitTokens = kUnitPages * kPageSize;
 constexpr int kStageBytes = kUnitPages * kQ4Block;
+constexpr int kChunk = 32 / kUnitPages;  // units whose block-table entries one warp-wide read brings
 constexpr int kCombRow = kHeadDim + 4;  // floats per partial output row: rows land 4 banks apart
+constexpr uint32_t kAllPages = (1u << kUnitPages) - 1u;
 constexpr int kMinUnits = 4;            // units per CTA below which fewer CTAs take part
 
 // A piece's part of one (row, KV head) pair.
@@ -54,7 +56,7 @@ struct Shape {
     static constexpr int NC = G >= 16 ? 6 : 4;
     static constexpr int NS = 2 * NC;
     static constexpr int NB = G >= 8 ? 1 : 2;
-    static constexpr int kSlots = G >= 16 ? 2 : 4;  // segments published ahead
+    static constexpr int kSlots = G >= 8 ? 2 : 4;  // segments published ahead
     static constexpr int per_sm = G >= 16 ? 1 : 2;
     static constexpr int threads = (NC + 2) * 32;
     static constexpr int off_q = NS * kStageBytes;
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         const uint8_t* pool = static_cast<const uint8_t*>(p.pool);
         const uint64_t pol = policy_evict_first();
         int seq = 0, k = 0;
+        uint32_t issued = 0;  // after a time-out: units behind seq whose copies were issued
         bool ok = true;
         int b = 0, h = 0, u = 0, len = 0, units = 0;
         if (lo < hi) {
@@ -214,40 +217,57 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             __syncwarp();
             const int32_t* bt = p.block_table + (int64_t)b * p.max_pages;
             const int pages = (len + kPageSize - 1) / kPageSize;
-            const int p0 = u * kUnitPages;  // the segment's first page; lanes hold 32 entries (8 units) at a time
-            int ent = p0 + lane < pages ? bt[p0 + lane] : -1, ent_next = -1;
-            for (int i = 0; i < n; ++i) {
-                if ((i & 7) == 0) {
-                    if (i > 0) ent = ent_next;
-                    const int at = p0 + (i + 8) * kUnitPages + lane;
-                    ent_next = i + 8 < n && at < pages ? bt[at] : -1;
+            const int p0 = u * kUnitPages;  // the segment's first page; lanes hold 32 entries (kChunk units) at a time
+            // Sixteen units at a time, a lane each: the warp sleeps on the first stage that is still in use, then every
+            // lane whose stage is free announces its unit and issues its copies (one unit after the other, a loader
+            // needs 600 cycles a unit, which halves the bandwidth).
+            int ent = p0 + lane < pages ? bt[p0 + lane] : -1;
+            for (int c0 = 0; c0 < n && ok; c0 += kChunk) {
+                const int cnt = min(kChunk, n - c0);
+                int page[kUnitPages];
+#pragma unroll
+                for (int i = 0; i < kUnitPages; ++i)
+                    page[i] = __shfl_sync(0xffffffffu, ent, (lane * kUnitPages + i) & 31);
+                const int at = p0 + (c0 + kChunk) * kUnitPages + lane;
+                ent = c0 + kChunk < n && at < pages ? bt[at] : -1;
+                const int unit = u + c0 + lane;  // of the pair
+                const int np = min(kUnitPages, pages - unit * kUnitPages);
+                uint32_t okmask = 0;
+#pragma unroll
+                for (int i = 0; i < kUnitPages; ++i)
+                    if (i < np && page[i] >= 0 && page[i] < p.num_pages) okmask |= 1u << i;
+                const int st = (seq + lane) % NS;
+                const uint32_t parity = (((seq + lane) / NS) & 1) ^ 1;
+                bool pending = lane < cnt;
+                if (pending && okmask != (1u << np) - 1u) raise_status(ctx.status, PKV_STATUS_BAD_PAGE);
+                for (unsigned left; (left = __ballot_sync(0xffffffffu, pending)) != 0;) {
+                    const int first = __ffs(left) - 1;
+                    if (!warp_wait(&empty[(seq + first) % NS], (((seq + first) / NS) & 1) ^ 1, ctx)) {
+                        ok = false;
+                        break;
+                    }
+                    if (pending && mbar_test_wait(&empty[st], parity)) {
+                        pending = false;
+                        const int nv = min(kUnitTokens, len - unit * kUnitTokens);
+                        const bool append = p.k_new && unit == units - 1;
+                        meta[st] = (uint32_t)nv | okmask << 8 | (append ? 1u << 12 : 0u);
+                        if (okmask)
+                            mbar_arrive_expect_tx(&full[st], __popc(okmask) * kQ4Block);
+                        else
+                            mbar_arrive(&full[st]);
+#pragma unroll
+                        for (int i = 0; i < kUnitPages; ++i)
+                            if ((okmask >> i) & 1)
+                                bulk_g2s_hint(smem + st * kStageBytes + i * kQ4Block,
+                                              pool + ((int64_t)page[i] * p.Hkv + h) * kQ4Block, kQ4Block, &full[st], pol);
+                    }
+                    __syncwarp();
                 }
-                const int first = (u + i) * kUnitPages;
-                const int np = min(kUnitPages, pages - first);
-                const int mine_ent = __shfl_sync(0xffffffffu, ent, (i & 7) * kUnitPages + (lane & 3));
-                const bool good = lane < np && mine_ent >= 0 && mine_ent < p.num_pages;
-                const unsigned okmask = __ballot_sync(0xffffffffu, good);
-                const int st = seq % NS;
-                if (!warp_wait(&empty[st], ((seq / NS) & 1) ^ 1, ctx)) {
-                    ok = false;
-                    break;
+                if (ok) {
+                    seq += cnt;
+                } else {  // gave up: these units' copies in flight are waited for, too
+                    issued = __ballot_sync(0xffffffffu, lane < cnt && !pending);
                 }
-                if (lane == 0) {
-                    const int nv = min(kUnitTokens, len - (u + i) * kUnitTokens);
-                    const bool append = p.k_new && u + i == units - 1;
-                    meta[st] = (uint32_t)nv | okmask << 8 | (append ? 1u << 12 : 0u);
-                    if (okmask != (1u << np) - 1u) raise_status(ctx.status, PKV_STATUS_BAD_PAGE);
-                    if (okmask)
-                        mbar_arrive_expect_tx(&full[st], __popc(okmask) * kQ4Block);
-                    else
-                        mbar_arrive(&full[st]);
-                }
-                __syncwarp();
-                if (good)
-                    bulk_g2s_hint(smem + st * kStageBytes + lane * kQ4Block,
-                                  pool + ((int64_t)mine_ent * p.Hkv + h) * kQ4Block, kQ4Block, &full[st], pol);
-                __syncwarp();
-                ++seq;
             }
             pos += n;
             u = 0;
@@ -261,7 +281,10 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             }
         }
         // every copy that this warp issued lands before the CTA may end
-        for (int j = max(0, seq - NS); j < seq; ++j) warp_drain(&full[j % NS], (j / NS) & 1);
+        for (int j = max(0, seq - NS); j < seq + kChunk; ++j) {
+            const bool mine = j < seq ? j + NS >= seq + 32 || !((issued >> (j + NS - seq)) & 1) : (issued >> (j - seq)) & 1;
+            if (mine) warp_drain(&full[j % NS], (j / NS) & 1);
+        }
         for (int j = max(0, k - kSlots); j < k; ++j) warp_drain(&seg_q[j % kSlots], (j / kSlots) & 1);
     } else if (warp == NC + 1) {
         // ---------------------------------------------------------------------------------------- epilogue
@@ -336,7 +359,17 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         // --------------------------------------------------------------------------------------- consumers
         const int g8 = lane >> 2;  // token row of S^T, dim row of O^T, head column of the B operand
         const int t4 = lane & 3;   // head columns 2 t4, 2 t4 + 1 of S^T and O^T
-        const float sl2 = p.scale_log2;
+        // Up to four query heads leave half of the 8 columns empty. The lanes of columns 4-7 then take over the scores of
+        // tokens 8-15 of a page from the lanes of columns 0-3 (kFold): every lane has one token instead of two, half of
+        // the scalar work. Their weights become columns 4-7 of the second product, whose sums are added at the end.
+        constexpr bool kFold = G <= 4;
+        constexpr int kTok = kFold ? 1 : 2;  // tokens of a page that this lane scores: tok0, and tok0 + 8
+        const int tok0 = kFold ? g8 + ((t4 >> 1) << 3) : g8;
+        const int col = kFold ? 2 * (t4 & 1) : 2 * t4;  // this lane's heads: 8 nt + col, + 1
+        constexpr int kFirstLane = kFold ? 2 : 4;       // lanes that differ in bits from here on share their heads
+        // scores are kept in units of 2^-24 / (|scale| * log2(e)): X = sum_g scale_g (q.code_g) 2^-24 + ..., x = X * xk
+        const float xk = fabsf(p.scale_log2) * 16777216.f;
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs
         int seq = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             if (!warp_wait(&seg_q[slot], (k / kSlots) & 1, ctx)) break;
             // Q^T as the B operand: b0 = Q[head][16 ks + 2 t4, + 1], b1 = + 8, + 9; head = 8 nt + g8
             uint32_t qb[kNT][8][2];
-            float qs[kNT][2][2];  // [nt][group][head 2 t4, 2 t4 + 1]: sum of q over the group, times scale * log2(e)
+            float qs[kNT][2][2];  // [nt][group][head]: sum of q over the group, times 2^-24
             const uint8_t* qrow = smem + L::off_q + slot * G * kRowBytes;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
@@ -362,7 +395,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t w = head < G ? *reinterpret_cast<const uint32_t*>(qrow + head * kRowBytes +
-                                                                                         (ks * 16 + 2 * t4 + 8 * i) * 2)
+                                                                                         (ks * 16 + 2 * t4 + 8 * i) * 2) ^ flip
                                                     : 0u;
                         qb[nt][ks][i] = w;
                         const float2 f = half2_of(w);
@@ -375,23 +408,25 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                     s1 += __shfl_xor_sync(0xffffffffu, s1, o);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {  // from the lanes of head 2 t4 + i
-                    qs[nt][0][i] = __shfl_sync(0xffffffffu, s0, (2 * t4 + i) * 4) * sl2;
-                    qs[nt][1][i] = __shfl_sync(0xffffffffu, s1, (2 * t4 + i) * 4) * sl2;
+                for (int i = 0; i < 2; ++i) {  // from the lanes of that head
+                    qs[nt][0][i] = __shfl_sync(0xffffffffu, s0, (col + i) * 4) * 5.9604644775390625e-8f;
+                    qs[nt][1][i] = __shfl_sync(0xffffffffu, s1, (col + i) * 4) * 5.9604644775390625e-8f;
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[slot]);
 
             float o[kNT][8][4];  // O^T: tile dt < 4 dims 16 dt + g8, + 8 of group 0; 4 + dt the same of group 1
-            float osum[kNT][2][2], m[kNT][2], l[kNT][2], R[2] = {0.f, 0.f};
+            // Weights are 2^(x - ref) with ref chosen per head so that weight * V's scale stays below 2^14 and its
+            // largest values above 1; ref is raised only when a unit would go beyond, then by what brings it to 2^7.
+            float osum[kNT][2][2], ref[kNT][2], l[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
                 for (int d = 0; d < 8; ++d) o[nt][d][0] = o[nt][d][1] = o[nt][d][2] = o[nt][d][3] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    m[nt][i] = -INFINITY;
+                    ref[nt][i] = -INFINITY;
                     l[nt][i] = osum[nt][0][i] = osum[nt][1][i] = 0.f;
                 }
             }
@@ -406,7 +441,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 uint8_t* stage = smem + st * kStageBytes;
                 const uint32_t mt = meta[st];
                 const int nv = mt & 0xff;
-                const uint32_t okmask = (mt >> 8) & 0xf;
+                const uint32_t okmask = (mt >> 8) & kAllPages;
                 const bool append = (mt >> 12) & 1;
                 if (append) {
                     const int r = (nv - 1) % kPageSize, pg = (nv - 1) / kPageSize;
@@ -431,151 +466,175 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                         }
                     }
                 }
-                const bool whole = nv == kUnitTokens && okmask == 0xf;
-                // scores of the unit's 64 tokens: this lane holds tokens 16 pg + g8, + 8 of heads 2 t4, 2 t4 + 1
-                float x[kNT][kUnitPages][4];
-                uint32_t vpar[kUnitPages][2][2];  // [page][token g8, + 8][group]: V's (scale, offset)
-                __half2 top = __float2half2_rn(0.f);
-#pragma unroll
-                for (int pg = 0; pg < kUnitPages; ++pg) {
-                    const uint8_t* blk = stage + pg * kQ4Block;
-                    const uint4 ka = *reinterpret_cast<const uint4*>(blk + lane * 16);
-                    const uint4 kb = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
-                    const uint2 pa = *reinterpret_cast<const uint2*>(blk + kQ4Codes + g8 * 8);
-                    const uint2 pb = *reinterpret_cast<const uint2*>(blk + kQ4Codes + 64 + g8 * 8);
-                    uint2 va = *reinterpret_cast<const uint2*>(blk + kQ4Half + kQ4Codes + g8 * 8);
-                    uint2 vb = *reinterpret_cast<const uint2*>(blk + kQ4Half + kQ4Codes + 64 + g8 * 8);
-                    bool oka = true, okb = true;
-                    if (!whole) {
-                        const bool pgok = (okmask >> pg) & 1;
-                        oka = pgok && pg * kPageSize + g8 < nv;
-                        okb = pgok && pg * kPageSize + g8 + 8 < nv;
-                        if (!oka) va = make_uint2(0u, 0u);
-                        if (!okb) vb = make_uint2(0u, 0u);
+                const bool whole = nv == kUnitTokens && okmask == kAllPages;
+                if (!whole) {  // tokens that the row does not have get parameters of 0, and scores of -inf below
+                    for (int tok = lane; tok < kUnitTokens; tok += 32) {
+                        const int pg = tok / kPageSize;
+                        if (!((okmask >> pg) & 1) || tok >= nv) {
+                            uint8_t* blk = stage + pg * kQ4Block + kQ4Codes + (tok % kPageSize) * 8;
+                            *reinterpret_cast<uint2*>(blk) = make_uint2(0u, 0u);
+                            *reinterpret_cast<uint2*>(blk + kQ4Half) = make_uint2(0u, 0u);
+                        }
                     }
-                    vpar[pg][0][0] = va.x;
-                    vpar[pg][0][1] = va.y;
-                    vpar[pg][1][0] = vb.x;
-                    vpar[pg][1][1] = vb.y;
-                    const uint32_t sa = __byte_perm(va.x, va.y, 0x5410), sb2 = __byte_perm(vb.x, vb.y, 0x5410);
-                    top = __hmax2(top, __hmax2(*reinterpret_cast<const __half2*>(&sa), *reinterpret_cast<const __half2*>(&sb2)));
-                    float c0[kNT][4], c1[kNT][4];
+                    __syncwarp();
+                }
+                // scores of the unit's tokens: [page][token][head]
+                float x[kNT][kUnitPages][kTok][2];
+                __half2 top = __float2half2_rn(0.f);  // V's scales of this lane's tokens
+#pragma unroll
+                for (int p0 = 0; p0 < kUnitPages; p0 += 2) {  // two pages at a time: four chains of products in flight
+                    uint32_t wa[2][4], wb[2][4];
+                    float c0[2][kNT][4], c1[2][kNT][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint8_t* blk = stage + (p0 + y) * kQ4Block;
+                        const uint4 ka = *reinterpret_cast<const uint4*>(blk + lane * 16);
+                        const uint4 kb = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
+                        wa[y][0] = ka.x, wa[y][1] = ka.y, wa[y][2] = ka.z, wa[y][3] = ka.w;
+                        wb[y][0] = kb.x, wb[y][1] = kb.y, wb[y][2] = kb.z, wb[y][3] = kb.w;
+#pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                            for (int i2 = 0; i2 < 4; ++i2) c0[y][nt][i2] = c1[y][nt][i2] = 0.f;
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t a8 = wa[y][ks] >> 8, b8 = wb[y][ks] >> 8;
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt) {
+                                mma_16816(c0[y][nt], wa[y][ks] & 0x000F000Fu, wb[y][ks] & 0x000F000Fu, a8 & 0x000F000Fu,
+                                          b8 & 0x000F000Fu, qb[nt][ks][0], qb[nt][ks][1]);
+                                mma_16816(c1[y][nt], wa[y][ks] & 0x00F000F0u, wb[y][ks] & 0x00F000F0u, a8 & 0x00F000F0u,
+                                          b8 & 0x00F000F0u, qb[nt][4 + ks][0], qb[nt][4 + ks][1]);
+                            }
+                        }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int pg = p0 + y;
+#pragma unroll
+                        for (int u2 = 0; u2 < kTok; ++u2) {
+                            const uint8_t* blk = stage + pg * kQ4Block + kQ4Codes + (tok0 + 8 * u2) * 8;
+                            const uint2 pk = *reinterpret_cast<const uint2*>(blk);
+                            const uint2 pv = *reinterpret_cast<const uint2*>(blk + kQ4Half);
+                            const uint32_t sv = __byte_perm(pv.x, pv.y, 0x5410);
+                            top = __hmax2(top, *reinterpret_cast<const __half2*>(&sv));
+                            const float2 a0 = half2_of(pk.x), a1 = half2_of(pk.y);
+                            const float a1s = a1.x * 0.0625f;  // group 1's codes lie 4 bits higher
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                                for (int i2 = 0; i2 < 2; ++i2) {
+                                    float d0 = c0[y][nt][2 * u2 + i2], d1 = c1[y][nt][2 * u2 + i2];
+                                    if (kFold) {
+                                        const float e0 = __shfl_up_sync(0xffffffffu, c0[y][nt][2 + i2], 2);
+                                        const float e1 = __shfl_up_sync(0xffffffffu, c1[y][nt][2 + i2], 2);
+                                        d0 = t4 < 2 ? d0 : e0;
+                                        d1 = t4 < 2 ? d1 : e1;
+                                    }
+                                    x[nt][pg][u2][i2] = fmaf(d0, a0.x, fmaf(d1, a1s, fmaf(a0.y, qs[nt][0][i2], a1.y * qs[nt][1][i2])));
+                                }
+                        }
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int pg = 0; pg < kUnitPages; ++pg)
+#pragma unroll
+                        for (int u2 = 0; u2 < kTok; ++u2)
+                            if (!((okmask >> pg) & 1) || pg * kPageSize + tok0 + 8 * u2 >= nv)
+#pragma unroll
+                                for (int nt = 0; nt < kNT; ++nt) x[nt][pg][u2][0] = x[nt][pg][u2][1] = -INFINITY;
+                }
+                // does a weight * scale of this unit go beyond 2^14? (per lane: its largest score and its largest scale)
+                const __half peak = __hmax(__hmax(__low2half(top), __high2half(top)), __ushort_as_half(1));
+                float need = __log2f(__half2float(peak)) - 7.f;
+                float mx[kNT][2];
+                bool raise = false;
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        float v = -INFINITY;
+#pragma unroll
+                        for (int pg = 0; pg < kUnitPages; ++pg)
+#pragma unroll
+                            for (int u2 = 0; u2 < kTok; ++u2) v = fmaxf(v, x[nt][pg][u2][i2]);
+                        mx[nt][i2] = v;
+                        raise = raise || fmaf(v, xk, need) > ref[nt][i2] + 7.f;
+                    }
+                if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int s = kFirstLane; s < 32; s <<= 1) need = fmaxf(need, __shfl_xor_sync(0xffffffffu, need, s));
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                        for (int i2 = 0; i2 < 4; ++i2) c0[nt][i2] = c1[nt][i2] = 0.f;
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint32_t a8 = wa[ks] >> 8, b8 = wb[ks] >> 8;
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) {
-                            mma_16816(c0[nt], wa[ks] & 0x000F000Fu, wb[ks] & 0x000F000Fu, a8 & 0x000F000Fu,
-                                      b8 & 0x000F000Fu, qb[nt][ks][0], qb[nt][ks][1]);
-                            mma_16816(c1[nt], wa[ks] & 0x00F000F0u, wb[ks] & 0x00F000F0u, a8 & 0x00F000F0u,
-                                      b8 & 0x00F000F0u, qb[nt][4 + ks][0], qb[nt][4 + ks][1]);
-                        }
-                    }
-                    const float2 a0 = half2_of(pa.x), a1 = half2_of(pa.y), b0f = half2_of(pb.x), b1f = half2_of(pb.y);
-                    const float k24 = sl2 * 16777216.f, k20 = sl2 * 1048576.f;
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
                         for (int i2 = 0; i2 < 2; ++i2) {
-                            const float va_ = fmaf(c0[nt][i2], a0.x * k24, fmaf(c1[nt][i2], a1.x * k20,
-                                                   fmaf(a0.y, qs[nt][0][i2], a1.y * qs[nt][1][i2])));
-                            const float vb_ = fmaf(c0[nt][2 + i2], b0f.x * k24, fmaf(c1[nt][2 + i2], b1f.x * k20,
-                                                   fmaf(b0f.y, qs[nt][0][i2], b1f.y * qs[nt][1][i2])));
-                            x[nt][pg][i2] = oka ? va_ : -INFINITY;
-                            x[nt][pg][2 + i2] = okb ? vb_ : -INFINITY;
-                        }
-                    }
-                }
-                // running maxima: scores per head, V's scales per group
+                            float v = mx[nt][i2];
 #pragma unroll
-                for (int s = 4; s < 32; s <<= 1) top = __hmax2(top, __shfl_xor_sync(0xffffffffu, top, s));
-                const float2 tf = __half22float2(top);
-                bool change = tf.x > R[0] || tf.y > R[1];
-                float mx[kNT][2];
+                            for (int s = kFirstLane; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+                            v = fmaf(v, xk, need);
+                            if (v > ref[nt][i2] + 7.f) {
+                                const float f = fast_exp2(ref[nt][i2] - v);
+                                ref[nt][i2] = v;
+                                l[nt][i2] *= f;
+                                osum[nt][0][i2] *= f;
+                                osum[nt][1][i2] *= f;
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        float v = fmaxf(x[nt][0][i2], x[nt][0][2 + i2]);
-#pragma unroll
-                        for (int pg = 1; pg < kUnitPages; ++pg) v = fmaxf(v, fmaxf(x[nt][pg][i2], x[nt][pg][2 + i2]));
-#pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-                        mx[nt][i2] = fmaxf(v, m[nt][i2]);
-                        change = change || mx[nt][i2] != m[nt][i2];
-                    }
-                }
-                if (__any_sync(0xffffffffu, change)) {
-                    float fr[2];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float r = fmaxf(R[g], g ? tf.y : tf.x);
-                        fr[g] = R[g] > 0.f ? R[g] / r : 0.f;
-                        R[g] = r;
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-                        for (int i2 = 0; i2 < 2; ++i2) {
-                            const float f = mx[nt][i2] == -INFINITY ? 1.f : fast_exp2(m[nt][i2] - mx[nt][i2]);
-                            m[nt][i2] = mx[nt][i2];
-                            l[nt][i2] *= f;
-                            osum[nt][0][i2] *= f;
-                            osum[nt][1][i2] *= f;
-#pragma unroll
-                            for (int d = 0; d < 8; ++d) {
-                                o[nt][d][i2] *= f * fr[d >> 2];
-                                o[nt][d][2 + i2] *= f * fr[d >> 2];
+                                for (int d = 0; d < 8; ++d) {
+                                    o[nt][d][i2] *= f;
+                                    o[nt][d][2 + i2] *= f;
+                                }
                             }
                         }
-                    }
                 }
-                const float ir0 = R[0] > 0.f ? 1.f / R[0] : 0.f, ir1 = R[1] > 0.f ? 1.f / R[1] : 0.f;
+                float nref[kNT][2];
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) nref[nt][i2] = ref[nt][i2] == -INFINITY ? 0.f : -ref[nt][i2];
+                uint32_t pb[kUnitPages][kNT][2][kTok];  // [page][nt][group]: weights * scale, tokens 0-7 and 8-15 as the B operand
+#pragma unroll
+                for (int pg = 0; pg < kUnitPages; ++pg)
+#pragma unroll
+                    for (int u2 = 0; u2 < kTok; ++u2) {
+                        const uint2 pv = *reinterpret_cast<const uint2*>(stage + pg * kQ4Block + kQ4Half + kQ4Codes + (tok0 + 8 * u2) * 8);
+                        const float2 a0 = half2_of(pv.x), a1 = half2_of(pv.y);
+#pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt) {
+                            float w[2];
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2) {
+                                w[i2] = fast_exp2(fmaf(x[nt][pg][u2][i2], xk, nref[nt][i2]));
+                                l[nt][i2] += w[i2];
+                                osum[nt][0][i2] = fmaf(w[i2], a0.y, osum[nt][0][i2]);
+                                osum[nt][1][i2] = fmaf(w[i2], a1.y, osum[nt][1][i2]);
+                            }
+                            pb[pg][nt][0][u2] = transpose8x8(pack_half2(w[0] * a0.x, w[1] * a0.x));
+                            pb[pg][nt][1][u2] = transpose8x8(pack_half2(w[0] * a1.x, w[1] * a1.x));
+                        }
+                    }
 #pragma unroll
                 for (int pg = 0; pg < kUnitPages; ++pg) {
                     const uint8_t* blk = stage + pg * kQ4Block + kQ4Half;
                     const uint4 va = *reinterpret_cast<const uint4*>(blk + lane * 16);
                     const uint4 vb = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
-                    const float2 a0 = half2_of(vpar[pg][0][0]), a1 = half2_of(vpar[pg][0][1]);
-                    const float2 b0f = half2_of(vpar[pg][1][0]), b1f = half2_of(vpar[pg][1][1]);
-                    uint32_t pb[kNT][2][2];  // [nt][group]: weights * scale as the B operand
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
-                        float w[4];
-#pragma unroll
-                        for (int i2 = 0; i2 < 2; ++i2) {
-                            const float ref = m[nt][i2] == -INFINITY ? 0.f : m[nt][i2];
-                            w[i2] = fast_exp2(x[nt][pg][i2] - ref);
-                            w[2 + i2] = fast_exp2(x[nt][pg][2 + i2] - ref);
-                            l[nt][i2] += w[i2] + w[2 + i2];
-                            osum[nt][0][i2] = fmaf(w[i2], a0.y, fmaf(w[2 + i2], b0f.y, osum[nt][0][i2]));
-                            osum[nt][1][i2] = fmaf(w[i2], a1.y, fmaf(w[2 + i2], b1f.y, osum[nt][1][i2]));
-                        }
-                        const float s0 = a0.x * ir0, s1 = a1.x * ir1, u0 = b0f.x * ir0, u1 = b1f.x * ir1;
-                        pb[nt][0][0] = transpose8x8(pack_half2(w[0] * s0, w[1] * s0));
-                        pb[nt][0][1] = transpose8x8(pack_half2(w[2] * u0, w[3] * u0));
-                        pb[nt][1][0] = transpose8x8(pack_half2(w[0] * s1, w[1] * s1));
-                        pb[nt][1][1] = transpose8x8(pack_half2(w[2] * u1, w[3] * u1));
-                    }
                     const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
                     for (int dt = 0; dt < 4; ++dt) {
                         const uint32_t a8 = wa[dt] >> 8, b8 = wb[dt] >> 8;
 #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
-                            mma_16816(o[nt][dt], wa[dt] & 0x000F000Fu, a8 & 0x000F000Fu, wb[dt] & 0x000F000Fu,
-                                      b8 & 0x000F000Fu, pb[nt][0][0], pb[nt][0][1]);
-                            mma_16816(o[nt][4 + dt], wa[dt] & 0x00F000F0u, a8 & 0x00F000F0u, wb[dt] & 0x00F000F0u,
-                                      b8 & 0x00F000F0u, pb[nt][1][0], pb[nt][1][1]);
+                            // folded: rows 0-3 of the transpose are tokens 0-7, rows 4-7 are tokens 8-15
+                            const uint32_t p00 = kFold && g8 >= 4 ? 0u : pb[pg][nt][0][0], p10 = kFold && g8 >= 4 ? 0u : pb[pg][nt][1][0];
+                            const uint32_t p01 = kFold && g8 < 4 ? 0u : pb[pg][nt][0][kTok - 1], p11 = kFold && g8 < 4 ? 0u : pb[pg][nt][1][kTok - 1];
+                            mma_16816(o[nt][dt], wa[dt] & 0x000F000Fu, a8 & 0x000F000Fu, wb[dt] & 0x000F000Fu, b8 & 0x000F000Fu, p00, p01);
+                            mma_16816(o[nt][4 + dt], wa[dt] & 0x00F000F0u, a8 & 0x00F000F0u, wb[dt] & 0x00F000F0u, b8 & 0x00F000F0u, p10, p11);
                         }
                     }
                 }
-                if (append) fence_proxy_async_smem();  // our stores into the stage before the next copy into it
+                if (append || !whole) fence_proxy_async_smem();  // our stores into the stage before the next copy into it
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
@@ -585,30 +644,36 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2)
+                for (int i2 = 0; i2 < 2; ++i2) {
+                    if (kFold)
 #pragma unroll
-                    for (int s = 4; s < 32; s <<= 1) {
+                        for (int d = 0; d < 8; ++d) {
+                            o[nt][d][i2] += __shfl_xor_sync(0xffffffffu, o[nt][d][i2], 2);
+                            o[nt][d][2 + i2] += __shfl_xor_sync(0xffffffffu, o[nt][d][2 + i2], 2);
+                        }
+#pragma unroll
+                    for (int s = kFirstLane; s < 32; s <<= 1) {
                         l[nt][i2] += __shfl_xor_sync(0xffffffffu, l[nt][i2], s);
                         osum[nt][0][i2] += __shfl_xor_sync(0xffffffffu, osum[nt][0][i2], s);
                         osum[nt][1][i2] += __shfl_xor_sync(0xffffffffu, osum[nt][1][i2], s);
                     }
+                }
             if (!warp_wait(&part_empty[e], ((k / NB) & 1) ^ 1, ctx)) break;
             float* co = comb + (e * NC + warp) * G * kCombRow;
             float2* cml = comb_ml + (e * NC + warp) * G;
-            const float f0 = R[0] * 16777216.f, f1 = R[1] * 1048576.f;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int i2 = 0; i2 < 2; ++i2) {
-                    const int head = nt * 8 + 2 * t4 + i2;
-                    if (head < G) {
+                    const int head = nt * 8 + col + i2;
+                    if (head < G && (!kFold || t4 < 2)) {
 #pragma unroll
                         for (int d = 0; d < 8; ++d) {
-                            const float f = d < 4 ? f0 : f1;
+                            const float f = d < 4 ? 16777216.f : 1048576.f;
                             co[head * kCombRow + d * 16 + g8] = fmaf(o[nt][d][i2], f, osum[nt][d >> 2][i2]);
                             co[head * kCombRow + d * 16 + g8 + 8] = fmaf(o[nt][d][2 + i2], f, osum[nt][d >> 2][i2]);
                         }
-                        if (g8 == 0) cml[head] = make_float2(m[nt][i2], l[nt][i2]);
+                        if (g8 == 0) cml[head] = make_float2(ref[nt][i2], l[nt][i2]);
                     }
                 }
             __syncwarp();
