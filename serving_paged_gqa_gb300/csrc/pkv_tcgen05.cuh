@@ -86,24 +86,67 @@ __device__ __forceinline__ uint64_t smem_desc_mn_major(uint32_t addr, uint32_t m
 }
 
 // Instruction descriptor: fp16 A and B, fp32 accumulator, M = 128, N columns (a multiple of 16).
-__device__ __forceinline__ uint32_t mma_idesc(uint32_t n, bool b_mn_major) {
+__host__ __device__ constexpr uint32_t mma_idesc(uint32_t n, bool b_mn_major) {
     return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
 }
 
-// D (TMEM) (+)= A (shared) B (shared), 16 elements of the contraction.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// True in one lane of the (converged) warp, always the same one. The branch on it keeps the operands of the matrix
+// instructions in uniform registers, where the hardware takes them from; a branch on the lane's number costs moves
+// into them for every instruction (88 cycles an instruction, more than the 64 it runs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
+// D (TMEM) = A (shared) B (shared) over a contraction of 128: two swizzled boxes of 64 in each operand, `box` apart
+// (in units of 16 bytes), four steps of 32 bytes in a box.
+template <int kBox16>
+__device__ __forceinline__ void mma_ss_128(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .b64 a, b;\n\t.reg .pred t;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, !t;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, %4;\n\tadd.s64 b, %2, %4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, %4 + 2;\n\tadd.s64 b, %2, %4 + 2;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, %4 + 4;\n\tadd.s64 b, %2, %4 + 4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, %4 + 6;\n\tadd.s64 b, %2, %4 + 6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(kBox16)
         : "memory");
 }
 
-// D (TMEM) (+)= A (TMEM, fp16 pairs: 8 columns for 16 elements of the contraction) B (shared).
+// D (TMEM) += A (TMEM, fp16 pairs: 8 columns for 16 elements of the contraction) B (shared, MN-major), one step of 16;
+// accumulate = false: D is overwritten.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// The same, four steps: the contraction's rows of 128 bytes are 16 * 128 bytes further on in B each.
+__device__ __forceinline__ void mma_ts_64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t.reg .pred p, t;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s64 b, %2, 128;\n\tadd.s32 a, %1, 8;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s64 b, %2, 256;\n\tadd.s32 a, %1, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s64 b, %2, 384;\n\tadd.s32 a, %1, 24;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }

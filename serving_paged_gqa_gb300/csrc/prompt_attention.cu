@@ -17,7 +17,7 @@
 //                   only when a row's scores exceed it by more than 8 (in log2): weights then reach 2^8 at most, far
 //                   inside fp16, and the accumulator is rescaled (by these warps) in the first steps only. Finally
 //                   they divide, round and store the output rows.
-//   warp 8          one lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P from
+//   warp 8          one (elected) lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P from
 //                   TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
 //                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
 //   warp 9          one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
@@ -64,7 +64,7 @@ constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
 constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
 constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
 constexpr int off_bars = off_hist + 32 * 4;
-constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 2 + 2 + 1;
+constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 1;
 constexpr int off_misc = off_bars + kBars * 8;  // abort flag, TMEM address
 constexpr int kSmem = off_misc + 16 + 1024;     // slack to align the base to 1024 bytes
 static_assert(off_order % 16 == 0 && off_work % 16 == 0 && off_bars % 8 == 0, "alignment");
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint64_t* q_full = w_empty + kSlots;  // [2], like those below: tile A, tile B
     uint64_t* q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
-    uint64_t* p_full = s_full + 2;        // its weights are
-    uint64_t* o_full = p_full + 2;        // its accumulator is complete
+    uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
+    uint64_t* o_full = p_full + 4;        // its accumulator is complete
     uint64_t* drain = o_full + 2;
     Work* work = reinterpret_cast<Work*>(smem + off_work);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);  // one arrival a warp
+            mbar_init(&p_full[2 * i], 4);  // one arrival a warp
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
         }
         mbar_init(drain, 1);
@@ -357,45 +358,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const int end0 = tile_end(w, 0, kTokens), end1 = tile_end(w, 1, kTokens);
                 const int steps = (max(end0, end1) + kRows - 1) / kRows;
                 // ring positions: K_j at kv + 2j, V_j one behind it
-                auto stage_addr = [&](int pos) { return smem_addr(smem + off_ring + (pos % kStages) * kTileBytes); };
+                const uint32_t ring = smem_addr(smem + off_ring);
+                auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
                 auto wait_stage = [&](int pos) { return warp_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
                 // keys of step j that tile x needs (0: none)
                 auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
                 auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
                     const int n = (keys(x, j) + 15) & ~15;
                     if (n == 0) return;
-                    if (lane == 0) {
-                        const uint32_t idesc = mma_idesc(n, false);
-                        const uint32_t qa = smem_addr(smem + off_q + x * kTileBytes), ka = stage_addr(kv + 2 * j);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t o = (i >> 2) * kBoxBytes + (i & 3) * 32;
-                            mma_ss(tmem + x * 128, smem_desc_k_major(qa + o), smem_desc_k_major(ka + o), idesc, i > 0);
-                        }
+                    const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
+                    const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
+                    const uint32_t idesc = mma_idesc(n, false);
+                    const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
+                    if (elect_one()) {
+                        mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, idesc);
                         mma_commit(&s_full[x]);
-                        if (keys(x, j + 1) == 0) mma_commit(&q_empty[x]);  // the tile's last use of its queries
+                        if (last) mma_commit(&q_empty[x]);
                     }
                     __syncwarp();
                 };
                 auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
                     const int n = (keys(x, j) + 15) >> 4;
                     if (n == 0) return true;
-                    if (!warp_wait(&p_full[x], np[x] & 1, ctx)) return false;
-                    ++np[x];
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t idesc = mma_idesc(kHeadDim, true);
-                        const uint32_t va = stage_addr(kv + 2 * j + 1);
-                        for (int i = 0; i < n; ++i)
-                            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, smem_desc_mn_major(va + i * 2048, kBoxBytes),
-                                   idesc, j > 0 || i > 0);
-                        if (keys(x, j + 1) == 0) mma_commit(&o_full[x]);
+                    constexpr uint32_t idesc = mma_idesc(kHeadDim, true);
+                    const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
+                    const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
+                    const bool last = keys(x, j + 1) == 0;
+                    for (int half = 0; half < 2; ++half) {  // weights of 64 keys each
+                        if (!warp_wait(&p_full[2 * x + half], np[x] & 1, ctx)) return false;
+                        tc_fence_after();
+                        const int c = min(4, n - 4 * half);  // steps of 16 keys
+                        if (elect_one()) {
+                            if (c == 4)
+                                mma_ts_64(o, pw + 32 * half, v + 512 * half, idesc, j > 0 || half > 0);
+                            else
+                                for (int i = 0; i < c; ++i)
+                                    mma_ts(o, pw + 32 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
+                            if (half == 1 && last) mma_commit(&o_full[x]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    ++np[x];
                     return true;
                 };
                 auto release = [&](int pos) {
-                    if (lane == 0) mma_commit(&kv_empty[pos % kStages]);
+                    if (elect_one()) mma_commit(&kv_empty[pos % kStages]);
                     __syncwarp();
                 };
                 ok = wait_stage(kv);
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 kv += 2 * steps;
             }
             // every matrix instruction has completed before the TMEM is freed and the CTA ends
-            if (lane == 0) mma_commit(drain);
+            if (elect_one()) mma_commit(drain);
             __syncwarp();
             warp_drain(drain, 0);
         }
@@ -459,28 +466,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 ++ns;
                 tc_fence_after();
-                float s[kRows];
-                uint32_t* su = reinterpret_cast<uint32_t*>(s);
                 const int last = end - j * kRows;  // keys of this step, at least 1
+                // The step with the diagonal and the sequence's end is masked and cut; the others are whole.
+                const bool tail = j == steps - 1;
+                const int lim = tail ? min(token, end - 1) - j * kRows : kRows;
+                // Two passes over the scores in TMEM, 32 columns at a time with the next ones on their way: the row's
+                // maximum, then the weights. (All 128 in registers need more than a thread has beside the weights, and
+                // this way the first 64 keys' products begin before the last weights exist.)
+                uint32_t r[2][32];
+                float mx = -INFINITY;
+                tmem_ld32(s_at, r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c * 32 < last) tmem_ld32(s_at + c * 32, su + c * 32);
-                tmem_wait_ld();
+                for (int c = 0; c < 4; ++c) {
+                    if (c * 32 < last) {
+                        tmem_wait_ld();
+                        tmem_use32(r[c & 1]);
+                        if (c < 3 && c * 32 + 32 < last) tmem_ld32(s_at + c * 32 + 32, r[(c + 1) & 1]);
+                        float* f = reinterpret_cast<float*>(r[c & 1]);
+                        if (tail) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_use32(su + c * 32);
-                if (j == steps - 1) {  // the step with the diagonal and the sequence's end
-                    const int lim = min(token, end - 1) - j * kRows;
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i > lim) f[i] = -INFINITY;
+                        }
+                        float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kRows; ++i)
-                        if (i > lim) s[i] = -INFINITY;
+                        for (int i = 0; i < 32; i += 4) {
+                            m0 = fmaxf(fmaxf(m0, f[i]), f[i + 1]);
+                            m1 = fmaxf(fmaxf(m1, f[i + 2]), f[i + 3]);
+                        }
+                        mx = fmaxf(mx, fmaxf(m0, m1));
+                    }
                 }
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kRows; i += 4) {
-                    mx0 = fmaxf(fmaxf(mx0, s[i]), s[i + 1]);
-                    mx1 = fmaxf(fmaxf(mx1, s[i + 2]), s[i + 3]);
-                }
-                const float mx = fmaxf(mx0, mx1);
+                tmem_ld32(s_at, r[0]);
                 const bool raise = (mx - m) * sl2 > kRaise || m == -INFINITY;
                 if (__any_sync(0xffffffffu, raise && j > 0)) {
                     float f = 1.f;
@@ -489,25 +506,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * sl2);
                         m = mn;
                     }
-                    if (j > 0) {
-                        l *= f;
-                        const uint64_t ff = pack_f32x2(f, f);
+                    l *= f;
+                    const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + c * 32, o);
+                        tmem_wait_ld();
+                        tmem_use32(o);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(o_at + c * 32, o);
-                            tmem_wait_ld();
-                            tmem_use32(o);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float a, b;
-                                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), ff),
-                                             a, b);
-                                o[i] = __float_as_uint(a);
-                                o[i + 1] = __float_as_uint(b);
-                            }
-                            tmem_st32(o_at + c * 32, o);
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), ff), a, b);
+                            o[i] = __float_as_uint(a);
+                            o[i + 1] = __float_as_uint(b);
                         }
+                        tmem_st32(o_at + c * 32, o);
                     }
                 } else if (raise) {
                     m = fmaxf(m, mx);
@@ -515,29 +529,41 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const float ref = m == -INFINITY ? 0.f : -m * sl2;
                 const uint64_t refx2 = pack_f32x2(ref, ref);
                 uint64_t sum0 = 0, sum1 = 0;
+                uint32_t ph[32];  // weights of 64 keys
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c * 32 < last) {
-                        uint32_t ph[16];
+                        tmem_wait_ld();
+                        tmem_use32(r[c & 1]);
+                        if (c < 3 && c * 32 + 32 < last) tmem_ld32(s_at + c * 32 + 32, r[(c + 1) & 1]);
+                        float* f = reinterpret_cast<float*>(r[c & 1]);
+                        if (tail) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i > lim) f[i] = -INFINITY;
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float a, b;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sl2x2, refx2), a, b);
+                            unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
                             a = fast_exp2(a);
                             b = fast_exp2(b);
                             if (i & 1)
                                 sum1 = add_f32x2(sum1, pack_f32x2(a, b));
                             else
                                 sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-                            ph[i] = pack_half2(a, b);
+                            ph[(c & 1) * 16 + i] = pack_half2(a, b);
                         }
-                        tmem_st16(s_at + c * 16, ph);
+                    }
+                    // The weights of keys 64 h .. + 63 go over the scores of keys 32 h .. + 31, which have been taken.
+                    if (c & 1) {
+                        if ((c - 1) * 32 < last) tmem_st32(s_at + (c >> 1) * 32, ph);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 1)]);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
                 float a, b;
                 unpack_f32x2(add_f32x2(sum0, sum1), a, b);
                 l += a + b;
