@@ -470,34 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 // The step with the diagonal and the sequence's end is masked and cut; the others are whole.
                 const bool tail = j == steps - 1;
                 const int lim = tail ? min(token, end - 1) - j * kRows : kRows;
-                // Two passes over the scores in TMEM, 32 columns at a time with the next ones on their way: the row's
-                // maximum, then the weights. (All 128 in registers need more than a thread has beside the weights, and
-                // this way the first 64 keys' products begin before the last weights exist.)
-                uint32_t r[2][32];
+                uint32_t r[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < last) tmem_ld32(s_at + c * 32, r[c]);
+                tmem_wait_ld();
                 float mx = -INFINITY;
-                tmem_ld32(s_at, r[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (c * 32 < last) {
-                        tmem_wait_ld();
-                        tmem_use32(r[c & 1]);
-                        if (c < 3 && c * 32 + 32 < last) tmem_ld32(s_at + c * 32 + 32, r[(c + 1) & 1]);
-                        float* f = reinterpret_cast<float*>(r[c & 1]);
-                        if (tail) {
+                    tmem_use32(r[c]);
+                    float* f = reinterpret_cast<float*>(r[c]);
+                    if (tail) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i > lim) f[i] = -INFINITY;
-                        }
-                        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            m0 = fmaxf(fmaxf(m0, f[i]), f[i + 1]);
-                            m1 = fmaxf(fmaxf(m1, f[i + 2]), f[i + 3]);
-                        }
-                        mx = fmaxf(mx, fmaxf(m0, m1));
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i > lim) f[i] = -INFINITY;
                     }
+                    float m0 = f[0], m1 = f[1];
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) {
+                        m0 = fmaxf(m0, f[i]);
+                        m1 = fmaxf(m1, f[i + 1]);
+                    }
+                    mx = fmaxf(mx, fmaxf(m0, m1));
                 }
-                tmem_ld32(s_at, r[0]);
                 const bool raise = (mx - m) * sl2 > kRaise || m == -INFINITY;
                 if (__any_sync(0xffffffffu, raise && j > 0)) {
                     float f = 1.f;
@@ -533,15 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c * 32 < last) {
-                        tmem_wait_ld();
-                        tmem_use32(r[c & 1]);
-                        if (c < 3 && c * 32 + 32 < last) tmem_ld32(s_at + c * 32 + 32, r[(c + 1) & 1]);
-                        float* f = reinterpret_cast<float*>(r[c & 1]);
-                        if (tail) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i > lim) f[i] = -INFINITY;
-                        }
+                        const float* f = reinterpret_cast<const float*>(r[c]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float a, b;
