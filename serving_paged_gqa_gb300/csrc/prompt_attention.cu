@@ -13,9 +13,7 @@
 // One CTA per SM, persistent; pairs of tiles are claimed from an atomic counter, longest sequences and latest tokens
 // first. Warp roles:
 //   warps 0-3, 4-7  softmax of tile A, of tile B: thread = row. The row's 128 scores come from TMEM into registers
-//                   (tcgen05.ld), the weights go back to TMEM as fp16 over the scores. The running maximum is raised
-//                   only when a row's scores exceed it by more than 8 (in log2): weights then reach 2^8 at most, far
-//                   inside fp16, and the accumulator is rescaled (by these warps) in the first steps only. Finally
+//                   (tcgen05.ld), the weights go back to TMEM as fp16 over the scores, 64 keys at a time. Finally
 //                   they divide, round and store the output rows.
 //   warp 8          one (elected) lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P from
 //                   TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
@@ -51,7 +49,7 @@ constexpr int kStages = 4;
 constexpr int kSlots = 1;  // a CTA claims its next pair when its softmax begins the current one
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
-constexpr float kRaise = 8.f;                // log2 by which scores may exceed the running maximum before it is raised
+constexpr float kMost = 32768.f;             // sum of 64 weights above which the row's reference is raised
 
 struct Work {
     int32_t first, n, t0, h;  // sequence's first packed row and length; first token of tile A; KV head (-1: no more work)
@@ -64,7 +62,7 @@ constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
 constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
 constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
 constexpr int off_bars = off_hist + 32 * 4;
-constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 1;
+constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 1;
 constexpr int off_misc = off_bars + kBars * 8;  // abort flag, TMEM address
 constexpr int kSmem = off_misc + 16 + 1024;     // slack to align the base to 1024 bytes
 static_assert(off_order % 16 == 0 && off_work % 16 == 0 && off_bars % 8 == 0, "alignment");
@@ -150,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
     uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
     uint64_t* o_full = p_full + 4;        // its accumulator is complete
-    uint64_t* drain = o_full + 2;
+    uint64_t* lo_done = o_full + 2;       // the products of a step's first 64 keys are in the accumulator
+    uint64_t* drain = lo_done + 2;
     Work* work = reinterpret_cast<Work*>(smem + off_work);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
@@ -172,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&p_full[2 * i], 4);  // one arrival a warp
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
+            mbar_init(&lo_done[i], 1);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                             else
                                 for (int i = 0; i < c; ++i)
                                     mma_ts(o, pw + 32 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
+                            if (half == 0) mma_commit(&lo_done[x]);
                             if (half == 1 && last) mma_commit(&o_full[x]);
                         }
                         __syncwarp();
@@ -458,102 +459,149 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (end == 0) continue;
             const int steps = (end + kRows - 1) / kRows;
             const int token = w.t0 + x * kTokens + row / G;
-            float m = -INFINITY, l = 0.f;  // running maximum of the raw scores (scale >= 0 keeps their order)
+            // Weights are 2^(x - ref), ref = m * scale * log2(e), with m the first step's maximum. m stays as it is while
+            // no weight exceeds 2^15, for which 64 keys' sum of weights, needed anyway, is the test: an ordinary step
+            // has no search for a maximum. A step that fails it (its weights are not announced yet) raises m to its own
+            // maximum, scales what has been accumulated, and computes its weights again.
+            float m = -INFINITY, l = 0.f;
             for (int j = 0; j < steps; ++j) {
                 if (!warp_wait(&s_full[x], ns & 1, ctx)) {
                     ok = false;
                     break;
                 }
-                ++ns;
                 tc_fence_after();
                 const int last = end - j * kRows;  // keys of this step, at least 1
                 // The step with the diagonal and the sequence's end is masked and cut; the others are whole.
                 const bool tail = j == steps - 1;
                 const int lim = tail ? min(token, end - 1) - j * kRows : kRows;
-                uint32_t r[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+                uint32_t r[4][32];  // the row's scores
+                auto fetch = [&](int c) {
                     if (c * 32 < last) tmem_ld32(s_at + c * 32, r[c]);
-                tmem_wait_ld();
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                };
+                auto arrived = [&](int c) {  // after tmem_wait_ld
                     tmem_use32(r[c]);
-                    float* f = reinterpret_cast<float*>(r[c]);
                     if (tail) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i > lim) f[i] = -INFINITY;
+                            if (c * 32 + i > lim) r[c][i] = 0xff800000u;  // -inf
                     }
+                };
+                auto greatest = [&](int c) {
+                    const float* f = reinterpret_cast<const float*>(r[c]);
                     float m0 = f[0], m1 = f[1];
 #pragma unroll
                     for (int i = 2; i < 32; i += 2) {
                         m0 = fmaxf(m0, f[i]);
                         m1 = fmaxf(m1, f[i + 1]);
                     }
-                    mx = fmaxf(mx, fmaxf(m0, m1));
-                }
-                const bool raise = (mx - m) * sl2 > kRaise || m == -INFINITY;
-                if (__any_sync(0xffffffffu, raise && j > 0)) {
-                    float f = 1.f;
-                    if (raise) {
-                        const float mn = fmaxf(m, mx);
-                        f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * sl2);
-                        m = mn;
+                    return fmaxf(m0, m1);
+                };
+                uint32_t ph[32];  // the weights of 64 keys, in fp16
+                auto weights = [&](int h) {  // of keys 64 h .. + 63; returns their sum
+                    const float ref = m == -INFINITY ? 0.f : -m * sl2;
+                    const uint64_t refx2 = pack_f32x2(ref, ref);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                    for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                        if (c * 32 < last) {
+                            const float* f = reinterpret_cast<const float*>(r[c]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float a, b;
+                                unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
+                                a = fast_exp2(a);
+                                b = fast_exp2(b);
+                                if (i & 1)
+                                    sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+                                else
+                                    sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+                                ph[(c & 1) * 16 + i] = pack_half2(a, b);
+                            }
+                        }
                     }
-                    l *= f;
-                    const uint64_t ff = pack_f32x2(f, f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + c * 32, o);
+                    float a, b;
+                    unpack_f32x2(add_f32x2(sum0, sum1), a, b);
+                    return a + b;
+                };
+                fetch(0);
+                fetch(1);
+                tmem_wait_ld();
+                arrived(0);
+                arrived(1);
+                fetch(2);
+                fetch(3);
+                if (j == 0) {
+                    m = greatest(0);
+                    if (32 < last) m = fmaxf(m, greatest(1));
+                    tmem_wait_ld();
+                    arrived(2);
+                    arrived(3);
+                    if (64 < last) m = fmaxf(m, greatest(2));
+                    if (96 < last) m = fmaxf(m, greatest(3));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && j > 0) {
                         tmem_wait_ld();
-                        tmem_use32(o);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a, b;
-                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), ff), a, b);
-                            o[i] = __float_as_uint(a);
-                            o[i + 1] = __float_as_uint(b);
+                        arrived(2);
+                        arrived(3);
+                    }
+                    float sum = weights(h);
+                    if (j > 0 && __any_sync(0xffffffffu, sum > kMost || m == -INFINITY)) {
+                        // the products that have been announced must be in the accumulator before it is scaled
+                        if (h == 1 && !warp_wait(&lo_done[x], ns & 1, ctx)) {
+                            ok = false;
+                            break;
                         }
-                        tmem_st32(o_at + c * 32, o);
-                    }
-                } else if (raise) {
-                    m = fmaxf(m, mx);
-                }
-                const float ref = m == -INFINITY ? 0.f : -m * sl2;
-                const uint64_t refx2 = pack_f32x2(ref, ref);
-                uint64_t sum0 = 0, sum1 = 0;
-                uint32_t ph[32];  // weights of 64 keys
+                        tc_fence_after();
+                        tmem_wait_ld();
+                        float mn = m;
+#pragma unroll 1
+                        for (int c = 2 * h; c < 4; ++c) {
+                            if (c * 32 >= last) break;
+                            uint32_t t[32];
+                            tmem_ld32(s_at + c * 32, t);
+                            tmem_wait_ld();
+                            tmem_use32(t);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c * 32 < last) {
-                        const float* f = reinterpret_cast<const float*>(r[c]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                            if (i & 1)
-                                sum1 = add_f32x2(sum1, pack_f32x2(a, b));
-                            else
-                                sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-                            ph[(c & 1) * 16 + i] = pack_half2(a, b);
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i <= lim) mn = fmaxf(mn, __uint_as_float(t[i]));
                         }
+                        const float f = m == -INFINITY || mn == m ? (mn == m ? 1.f : 0.f) : fast_exp2((m - mn) * sl2);
+                        m = mn;
+                        l *= f;
+                        const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t t[32];
+                            tmem_ld32(o_at + c * 32, t);
+                            tmem_wait_ld();
+                            tmem_use32(t);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float a, b;
+                                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
+                                t[i] = __float_as_uint(a);
+                                t[i + 1] = __float_as_uint(b);
+                            }
+                            tmem_st32(o_at + c * 32, t);
+                        }
+                        if (h == 0) {  // its wait above covered these
+                            arrived(2);
+                            arrived(3);
+                        }
+                        sum = weights(h);
                     }
-                    // The weights of keys 64 h .. + 63 go over the scores of keys 32 h .. + 31, which have been taken.
-                    if (c & 1) {
-                        if ((c - 1) * 32 < last) tmem_st32(s_at + (c >> 1) * 32, ph);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 1)]);
-                    }
+                    l += sum;
+                    // They go over the scores of keys 32 h .. + 31, which have been taken.
+                    if (64 * h < last) tmem_st32(s_at + 32 * h, ph);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
                 }
-                float a, b;
-                unpack_f32x2(add_f32x2(sum0, sum1), a, b);
-                l += a + b;
+                if (!ok) break;
+                ++ns;
             }
             if (!ok) break;
             if (!warp_wait(&o_full[x], no & 1, ctx)) break;

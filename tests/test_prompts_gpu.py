@@ -127,6 +127,26 @@ def test_prompt_flat_and_sharp_softmax(factor, scale):
     check_prompt(q, k, v, cu, out, scale=scale)
 
 
+@pytest.mark.parametrize("step", [0.02, 0.2, 1.0])
+@pytest.mark.parametrize("shape", ["up", "down", "second half", "saw"])
+def test_prompt_scores_that_grow_along_the_keys(step, shape):
+    """Scores whose maximum moves by up to 1.4 in log2 from key to key, so that the running reference is raised in
+    every step, in a step's first or second 64 keys, by some rows only, or never after the first."""
+    n, g = 700, gen(77)
+    q, k, v, cu = packed(g, [n], 8, 2)
+    at = torch.arange(n, device="cuda", dtype=torch.float32)
+    along = {"up": at, "down": -at, "second half": torch.where(at % 128 >= 64, at, at * 0), "saw": (at * 37) % 300}[shape]
+    unit = torch.zeros(D, device="cuda")
+    unit[5] = 8.0
+    k = (k.float() * 0.1 + (along * step * math.sqrt(D) / 8.0)[:, None, None] * (unit / 8.0)).half()
+    turn = torch.tensor([1.0, 1.0, 0.5, 0.0], device="cuda").repeat(2)  # rows of one tile that grow at different rates
+    q = (q.float() * 0.1 + turn[None, :, None] * unit).half()
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("which", ["k", "v", "kv"])
 def test_prompt_masked_tokens_never_reach_a_row(bad, which):
