@@ -12,16 +12,27 @@
 //
 // One CTA per SM, persistent; pairs of tiles are claimed from an atomic counter, longest sequences and latest tokens
 // first. Warp roles:
-//   warps 0-3, 4-7  softmax of tile A, of tile B: thread = row. The row's 128 scores come from TMEM into registers
-//                   (tcgen05.ld), the weights go back to TMEM as fp16 over the scores, 64 keys at a time. Finally
-//                   they divide, round and store the output rows.
-//   warp 8          one (elected) lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P from
-//                   TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
+//   warps 0-15      softmax: warps 0-3 and 4-7 the first and second 64 keys of every step of tile A, 8-15 those of tile
+//                   B; thread = row. The scores come from TMEM into registers (tcgen05.ld), the weights go back as fp16
+//                   over them. (With one thread for all 128 keys of a row the softmax of a step took 2000 cycles, and
+//                   the tensor core, which has 1024 cycles of the other tile's work meanwhile, waited.) Finally they
+//                   divide, round and store the output rows, 64 dims each.
+//   warp 16         one (elected) lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P
+//                   from TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
 //                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
-//   warp 9          one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
-//   warp 10         claims work, one pair ahead, and publishes it.
-// TMEM (512 columns): S_A, S_B (P in the first 64 columns of each), O_A, O_B. Instructions of one thread run in order,
-// so S(j+1) may be issued over P(j) right after PV(j).
+//   warp 17         one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
+//   warp 18         claims work, one pair ahead, and publishes it.
+// TMEM (512 columns): S_A, S_B (P over columns 0-31 and 64-95 of each), O_A, O_B. Instructions of one thread run in
+// order, so S(j+1) may be issued over P(j) right after PV(j).
+//
+// Weights are 2^(x - ref), one ref a row. It is the maximum of the row's first 64 keys, and stays as it is while no weight
+// exceeds 2^15, for which 64 keys' sum of weights, needed anyway, is the test: an ordinary step has no search for a
+// maximum. A thread whose keys fail the test (before their weights are announced) raises ref by a whole number to its
+// keys' maximum, scales what has been accumulated, and computes its weights again. The two threads of a row do not wait
+// for each other in ordinary steps (that cost 450 cycles a step): products of a step's second half never begin before
+// those of its first, so where the first half raises, it scales the second half's weights in TMEM as well (by a power
+// of two: exactly), and where the second half does, it first waits for the first half's products. Each sees what the
+// other has raised at the next step.
 //
 // A value that a row does not attend to is multiplied by a weight of 0, which does not remove an infinity or a NaN of
 // V. Output rows that are not finite are therefore computed again by a warp that reads the row's own keys alone
@@ -47,8 +58,9 @@ constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two boxes of 64 dims
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kStages = 4;
 constexpr int kSlots = 1;  // a CTA claims its next pair when its softmax begins the current one
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
+constexpr int kSoftmax = 512;                // threads of the softmax
+constexpr int kThreads = kSoftmax + 128;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96
 constexpr float kMost = 32768.f;             // sum of 64 weights above which the row's reference is raised
 
 struct Work {
@@ -62,10 +74,13 @@ constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
 constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
 constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
 constexpr int off_bars = off_hist + 32 * 4;
-constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 1;
-constexpr int off_misc = off_bars + kBars * 8;  // abort flag, TMEM address
+constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 1;
+constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
+constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
+constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
+constexpr int off_misc = off_late + 8 * 4;  // abort flag, TMEM address
 constexpr int kSmem = off_misc + 16 + 1024;     // slack to align the base to 1024 bytes
-static_assert(off_order % 16 == 0 && off_work % 16 == 0 && off_bars % 8 == 0, "alignment");
+static_assert(off_order % 16 == 0 && off_work % 16 == 0 && off_bars % 8 == 0 && off_parts % 8 == 0, "alignment");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Params {
@@ -85,8 +100,9 @@ __device__ __forceinline__ Row4 load4(const __half* p) {
     return Row4{{a.x, a.y, b.x, b.y}};
 }
 
-// One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, lane l holds dims 4l..4l+3.
-__device__ __noinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int lane) {
+// One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, lane l holds dims 4l..4l+3. Stores
+// dims 64 half .. + 63.
+__device__ __noinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int half, int lane) {
     const int h = hq / (p.Hq / p.Hkv);
     const __half* k = static_cast<const __half*>(p.k) + first * p.k_stride + h * kHeadDim + lane * 4;
     const __half* v = static_cast<const __half*>(p.v) + first * p.v_stride + h * kHeadDim + lane * 4;
@@ -111,7 +127,8 @@ __device__ __noinline__ void row_attention(const PromptParams& p, int64_t first,
     uint2 u;
     u.x = pack_half2(o[0] * inv, o[1] * inv);
     u.y = pack_half2(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (first + pos) * p.out_stride + hq * kHeadDim + lane * 4) = u;
+    if (lane >> 4 == half)
+        *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (first + pos) * p.out_stride + hq * kHeadDim + lane * 4) = u;
 }
 
 // ---- the tensor-core kernel ---------------------------------------------------------------------------------------
@@ -149,7 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
     uint64_t* o_full = p_full + 4;        // its accumulator is complete
     uint64_t* lo_done = o_full + 2;       // the products of a step's first 64 keys are in the accumulator
-    uint64_t* drain = lo_done + 2;
+    uint64_t* o_free = lo_done + 2;       // the accumulator has been read
+    uint64_t* first_ref = o_free + 2;     // [tile][warp of the half]: the tile's first references are in shared memory
+    uint64_t* half_done = first_ref + 8;  // [tile][warp of the half]: the second half has settled its weights of the step
+    uint64_t* drain = half_done + 8;
     Work* work = reinterpret_cast<Work*>(smem + off_work);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
@@ -162,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], 10);  // 8 softmax warps, the MMA warp, the loader
+            mbar_init(&w_empty[i], kSoftmax / 32 + 2);  // and the MMA warp, the loader
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -172,20 +192,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&lo_done[i], 1);
+            mbar_init(&o_free[i], 8);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&first_ref[i], 1);
+            mbar_init(&half_done[i], 1);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 8) tmem_alloc(tmem_at, 512);
+    if (warp == 16) tmem_alloc(tmem_at, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
-    if (warp >= 8) {
+    if (warp >= kSoftmax / 32) {
         regs_shrink<kOtherRegs>();
-        if (warp == 10) {
+        if (warp == 18) {
             // ---------------------------------------------------------------------------------- work claims
             // Sequences in descending order of the power of two of their tile pairs; within one, the last tokens
             // (most keys) first.
@@ -288,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     atomicExch(&p.hdr->ctas_done, 0u);
                 }
             }
-        } else if (warp == 9) {
+        } else if (warp == 17) {
             // ------------------------------------------------------------------------------------- copies
             if (lane == 0) {
                 prefetch_tensormap(&prm.q);
@@ -343,10 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int j = max(0, seq - kStages); j < seq; ++j) warp_drain(&kv_full[j % kStages], (j / kStages) & 1);
             for (int x = 0; x < 2; ++x)
                 if (nq[x] > 0) warp_drain(&q_full[x], (nq[x] - 1) & 1);
-        } else if (warp == 8) {
+        } else if (warp == 16) {
             // ------------------------------------------------------------------------- matrix instructions
+            // (The votes of the waits keep the warp together; a __syncwarp after every elected block costs 6 %.)
             int kv = 0;                        // ring position of the next K tile of the current work
-            int nq[2] = {0, 0}, np[2] = {0, 0};  // tiles begun, steps of softmax taken
+            int nq[2] = {0, 0}, no[2] = {0, 0};  // tiles begun; accumulators begun
+            int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int slot = k % kSlots;
@@ -375,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         mma_commit(&s_full[x]);
                         if (last) mma_commit(&q_empty[x]);
                     }
-                    __syncwarp();
                 };
                 auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
                     const int n = (keys(x, j) + 15) >> 4;
@@ -384,27 +410,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
                     const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
                     const bool last = keys(x, j + 1) == 0;
-                    for (int half = 0; half < 2; ++half) {  // weights of 64 keys each
-                        if (!warp_wait(&p_full[2 * x + half], np[x] & 1, ctx)) return false;
-                        tc_fence_after();
+                    if (j == 0) {  // the previous tile's rows have been read
+                        if (!warp_wait(&o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
+                        ++no[x];
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {  // 64 keys each
                         const int c = min(4, n - 4 * half);  // steps of 16 keys
+                        if (c <= 0) break;
+                        if (!warp_wait(&p_full[2 * x + half], np[x][half] & 1, ctx)) return false;
+                        ++np[x][half];
+                        tc_fence_after();
                         if (elect_one()) {
                             if (c == 4)
-                                mma_ts_64(o, pw + 32 * half, v + 512 * half, idesc, j > 0 || half > 0);
+                                mma_ts_64(o, pw + 64 * half, v + 512 * half, idesc, j > 0 || half > 0);
                             else
                                 for (int i = 0; i < c; ++i)
-                                    mma_ts(o, pw + 32 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
+                                    mma_ts(o, pw + 64 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
                             if (half == 0) mma_commit(&lo_done[x]);
-                            if (half == 1 && last) mma_commit(&o_full[x]);
+                            if (last && n - 4 * half <= 4) mma_commit(&o_full[x]);
                         }
-                        __syncwarp();
                     }
-                    ++np[x];
                     return true;
                 };
                 auto release = [&](int pos) {
                     if (elect_one()) mma_commit(&kv_empty[pos % kStages]);
-                    __syncwarp();
                 };
                 ok = wait_stage(kv);
                 for (int x = 0; x < 2 && ok; ++x) {
@@ -440,13 +470,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     } else {
         // ---------------------------------------------------------------------------- softmax and output rows
         regs_grow<kSoftmaxRegs>();
-        const int x = warp >> 2;
+        const int x = warp >> 3, h = (warp >> 2) & 1;  // tile, half of the keys (and of the output's dims)
         const int row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + x * 128, o_at = tmem + lanes + 256 + x * 128;
+        const uint32_t s_at = tmem + lanes + x * 128 + h * 64;  // this half's scores, and its weights over the first 32
+        const uint32_t o_at = tmem + lanes + 256 + x * 128;
+        volatile float* ref_at = reinterpret_cast<volatile float*>(smem + off_ref) + x * kRows + row;
+        float2* parts = reinterpret_cast<float2*>(smem + off_parts) + x * 2 * kRows + row;  // + buffer * 4 kRows + half * kRows
+        uint64_t* settled = &first_ref[x * 4 + (warp & 3)];
+        uint64_t* second = &half_done[x * 4 + (warp & 3)];
+        volatile int* late_at = reinterpret_cast<volatile int*>(smem + off_late) + x * 4 + (warp & 3);
         const float sl2 = p.scale_log2;
         const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
         int ns = 0, no = 0;  // steps, tiles taken
+        int step2 = 0;       // steps with keys in the second half, as the first half counts them
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int slot = k % kSlots;
@@ -459,52 +496,56 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (end == 0) continue;
             const int steps = (end + kRows - 1) / kRows;
             const int token = w.t0 + x * kTokens + row / G;
-            // Weights are 2^(x - ref), ref = m * scale * log2(e), with m the first step's maximum. m stays as it is while
-            // no weight exceeds 2^15, for which 64 keys' sum of weights, needed anyway, is the test: an ordinary step
-            // has no search for a maximum. A step that fails it (its weights are not announced yet) raises m to its own
-            // maximum, scales what has been accumulated, and computes its weights again.
-            float m = -INFINITY, l = 0.f;
+            float ref = -INFINITY, l = 0.f;
             for (int j = 0; j < steps; ++j) {
                 if (!warp_wait(&s_full[x], ns & 1, ctx)) {
                     ok = false;
                     break;
                 }
+                const int step = ns++;
+                const int last = end - j * kRows - h * 64;  // keys of this half, counted from its first
+                if (last <= 0) continue;                    // the tile's last step ends in the first half
                 tc_fence_after();
-                const int last = end - j * kRows;  // keys of this step, at least 1
-                // The step with the diagonal and the sequence's end is masked and cut; the others are whole.
+                // The step with the diagonal and the sequence's end is masked; the others are whole.
                 const bool tail = j == steps - 1;
-                const int lim = tail ? min(token, end - 1) - j * kRows : kRows;
-                uint32_t r[4][32];  // the row's scores
-                auto fetch = [&](int c) {
-                    if (c * 32 < last) tmem_ld32(s_at + c * 32, r[c]);
-                };
-                auto arrived = [&](int c) {  // after tmem_wait_ld
-                    tmem_use32(r[c]);
+                const int lim = tail ? min(token, end - 1) - j * kRows - h * 64 : 64;
+                auto fetch = [&](int c, uint32_t* r) {  // 32 of the row's scores
+                    tmem_ld32(s_at + c * 32, r);
+                    tmem_wait_ld();
+                    tmem_use32(r);
                     if (tail) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i > lim) r[c][i] = 0xff800000u;  // -inf
+                            if (c * 32 + i > lim) r[i] = 0xff800000u;  // -inf
                     }
                 };
-                auto greatest = [&](int c) {
-                    const float* f = reinterpret_cast<const float*>(r[c]);
-                    float m0 = f[0], m1 = f[1];
+                auto greatest = [&]() {
+                    float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int i = 2; i < 32; i += 2) {
-                        m0 = fmaxf(m0, f[i]);
-                        m1 = fmaxf(m1, f[i + 1]);
+                    for (int c = 0; c < 2; ++c) {
+                        if (c * 32 < last) {
+                            uint32_t r[32];
+                            fetch(c, r);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                m0 = fmaxf(m0, __uint_as_float(r[i]));
+                                m1 = fmaxf(m1, __uint_as_float(r[i + 1]));
+                            }
+                        }
                     }
                     return fmaxf(m0, m1);
                 };
-                uint32_t ph[32];  // the weights of 64 keys, in fp16
-                auto weights = [&](int h) {  // of keys 64 h .. + 63; returns their sum
-                    const float ref = m == -INFINITY ? 0.f : -m * sl2;
-                    const uint64_t refx2 = pack_f32x2(ref, ref);
+                uint32_t ph[32];  // the weights, in fp16
+                auto weights = [&]() {  // returns their sum
+                    const float nref = ref == -INFINITY ? 0.f : -ref;
+                    const uint64_t refx2 = pack_f32x2(nref, nref);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                    for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         if (c * 32 < last) {
-                            const float* f = reinterpret_cast<const float*>(r[c]);
+                            uint32_t r[32];
+                            fetch(c, r);
+                            const float* f = reinterpret_cast<const float*>(r);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 float a, b;
@@ -515,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                                     sum1 = add_f32x2(sum1, pack_f32x2(a, b));
                                 else
                                     sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-                                ph[(c & 1) * 16 + i] = pack_half2(a, b);
+                                ph[c * 16 + i] = pack_half2(a, b);
                             }
                         }
                     }
@@ -523,102 +564,145 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     unpack_f32x2(add_f32x2(sum0, sum1), a, b);
                     return a + b;
                 };
-                fetch(0);
-                fetch(1);
-                tmem_wait_ld();
-                arrived(0);
-                arrived(1);
-                fetch(2);
-                fetch(3);
-                if (j == 0) {
-                    m = greatest(0);
-                    if (32 < last) m = fmaxf(m, greatest(1));
-                    tmem_wait_ld();
-                    arrived(2);
-                    arrived(3);
-                    if (64 < last) m = fmaxf(m, greatest(2));
-                    if (96 < last) m = fmaxf(m, greatest(3));
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && j > 0) {
+                // Scales what has been accumulated up to now (this thread's sum; the row's accumulator).
+                auto scale_sum = [&](float to) {
+                    if (to != ref) l *= ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                };
+                auto scale_acc = [&](float f) {
+                    const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t t[32];
+                        tmem_ld32(o_at + c * 32, t);
                         tmem_wait_ld();
-                        arrived(2);
-                        arrived(3);
+                        tmem_use32(t);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
+                            t[i] = __float_as_uint(a);
+                            t[i + 1] = __float_as_uint(b);
+                        }
+                        tmem_st32(o_at + c * 32, t);
                     }
-                    float sum = weights(h);
-                    if (j > 0 && __any_sync(0xffffffffu, sum > kMost || m == -INFINITY)) {
-                        // the products that have been announced must be in the accumulator before it is scaled
-                        if (h == 1 && !warp_wait(&lo_done[x], ns & 1, ctx)) {
+                };
+                // The reference that this half's keys ask for: above the present one by a whole number.
+                auto raised = [&]() {
+                    const float top = greatest() * sl2;
+                    return ref == -INFINITY ? top : top > ref ? ref + ceilf(top - ref) : ref;
+                };
+                if (j > 0) {  // the other half may have raised it in the step before
+                    const float r = *ref_at;
+                    scale_sum(r);
+                    ref = r;
+                } else if (h == 0) {
+                    ref = greatest() * sl2;
+                    *ref_at = ref;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(settled);
+                } else {
+                    if (!warp_wait(settled, no & 1, ctx)) {
+                        ok = false;
+                        break;
+                    }
+                    ref = *ref_at;
+                }
+                float sum = weights();
+                const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, sum > kMost || ref == -INFINITY);
+                if (h == 0 && raise) {
+                    // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
+                    float f2 = 1.f;
+                    const float to = raised();
+                    const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                    if (last > 64) {
+                        if (!warp_wait(second, step2 & 1, ctx)) {
+                            ok = false;
+                            break;
+                        }
+                        if (*late_at == 0) f2 = f;
+                    }
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, f2 != 1.f)) {
+                        uint32_t t[32];
+                        tmem_ld32(s_at + 64, t);
+                        tmem_wait_ld();
+                        tmem_use32(t);
+                        const __half2 hf = __float2half2_rn(f2);  // a power of two: exact
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&t[i]), hf);
+                            t[i] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        tmem_st32(s_at + 64, t);
+                    }
+                    scale_sum(to);
+                    ref = to;
+                    *ref_at = ref;
+                    scale_acc(f);
+                    sum = weights();
+                } else if (h == 1) {
+                    if (raise) {
+                        if (lane == 0) *late_at = 1;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(second);
+                        // the first half's products must be in the accumulator before it is scaled
+                        if (!warp_wait(&lo_done[x], step & 1, ctx)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        tmem_wait_ld();
-                        float mn = m;
-#pragma unroll 1
-                        for (int c = 2 * h; c < 4; ++c) {
-                            if (c * 32 >= last) break;
-                            uint32_t t[32];
-                            tmem_ld32(s_at + c * 32, t);
-                            tmem_wait_ld();
-                            tmem_use32(t);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i <= lim) mn = fmaxf(mn, __uint_as_float(t[i]));
-                        }
-                        const float f = m == -INFINITY || mn == m ? (mn == m ? 1.f : 0.f) : fast_exp2((m - mn) * sl2);
-                        m = mn;
-                        l *= f;
-                        const uint64_t ff = pack_f32x2(f, f);
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t t[32];
-                            tmem_ld32(o_at + c * 32, t);
-                            tmem_wait_ld();
-                            tmem_use32(t);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float a, b;
-                                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
-                                t[i] = __float_as_uint(a);
-                                t[i + 1] = __float_as_uint(b);
-                            }
-                            tmem_st32(o_at + c * 32, t);
-                        }
-                        if (h == 0) {  // its wait above covered these
-                            arrived(2);
-                            arrived(3);
-                        }
-                        sum = weights(h);
+                        const float r = *ref_at;  // the first half may have raised it in this step
+                        scale_sum(r);
+                        ref = r;
+                        const float to = raised();
+                        const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                        scale_sum(to);
+                        ref = to;
+                        *ref_at = ref;
+                        scale_acc(f);
+                        sum = weights();
+                    } else if (lane == 0) {
+                        *late_at = 0;
                     }
-                    l += sum;
-                    // They go over the scores of keys 32 h .. + 31, which have been taken.
-                    if (64 * h < last) tmem_st32(s_at + 32 * h, ph);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
                 }
-                if (!ok) break;
-                ++ns;
+                if (last > 64) ++step2;
+                l += sum;
+                parts[(no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
+                tmem_st32(s_at, ph);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (h == 1 && !raise) mbar_arrive(second);  // before the one that lets the first half's next step begin
+                    mbar_arrive(&p_full[2 * x + h]);
+                }
             }
             if (!ok) break;
             if (!warp_wait(&o_full[x], no & 1, ctx)) break;
-            ++no;
             tc_fence_after();
+            // the row's sum: both halves', relative to the last reference (they only rise)
+            const float2 lo = parts[(no & 1) * 4 * kRows], hi = parts[(no & 1) * 4 * kRows + kRows];
+            float total = lo.y;
+            if (end > 64) {
+                const float top = fmaxf(lo.x, hi.x);
+                total = lo.y * (lo.x == top ? 1.f : fast_exp2(lo.x - top)) + hi.y * (hi.x == top ? 1.f : fast_exp2(hi.x - top));
+            }
             const bool mine = token < w.n;
-            const float inv = 1.f / l;
+            const float inv = 1.f / total;
             float probe = 0.f;  // stays 0 while every value is finite
             __half* dst = static_cast<__half*>(p.out) + (int64_t)(w.first + token) * p.out_stride +
-                          (w.h * G + row % G) * kHeadDim;
+                          (w.h * G + row % G) * kHeadDim + h * 64;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_at + c * 32, o);
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[32], y[16];
+                tmem_ld32(o_at + h * 64 + c * 32, o);
                 tmem_wait_ld();
                 tmem_use32(o);
-                uint32_t y[16];
+                if (c == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[x]);  // the next tile's products may overwrite it
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
@@ -631,19 +715,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         reinterpret_cast<uint4*>(dst)[c * 4 + i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 }
             }
-            tc_fence_before();  // the reads of O are done before the next tile's first weights are announced
+            ++no;
             unsigned again = __ballot_sync(0xffffffffu, mine && probe != 0.f);
             while (again) {  // rows that are not finite: from their own keys alone
                 const int r = (row & ~31) + __ffs(again) - 1;
                 again &= again - 1;
                 __syncwarp();
-                row_attention(p, w.first, w.t0 + x * kTokens + r / G, w.h * G + r % G, lane);
+                row_attention(p, w.first, w.t0 + x * kTokens + r / G, w.h * G + r % G, h, lane);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }
@@ -685,7 +769,7 @@ int launch(const Params& prm, int num_sms, cudaStream_t stream) {
         cudaError_t e = cudaFuncGetAttributes(&a, prompt_kernel<G>);
         if (e != cudaSuccess) return e;
         // the warpgroups' register shares come out of what the launch gives them
-        if (a.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+        if (a.numRegs * kThreads < kSoftmax * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(prompt_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
