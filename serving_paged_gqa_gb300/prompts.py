@@ -7,14 +7,13 @@ marshalling only: the work runs in the library's CUDA kernels, on the device of 
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
 import torch
 
 from ._lib import PKV_PROMPT_WS_BYTES, PKV_Q4_BLOCK_BYTES, Problem, Prompt, check, load
-from .binding import _ptr, _stream, alloc_workspace, make_problem
+from .binding import alloc_workspace, make_problem
 
 __all__ = [
     "make_prompt", "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append",
@@ -22,47 +21,72 @@ __all__ = [
     "prompt_attention", "prompt_append", "q4_problem", "q4_prompt_append", "q4_read", "q4_decode",
 ]
 
+# The marshalling of a call is on the path of every small step, so it stays with integers: pointers and streams are
+# passed as numbers, devices are compared by their index.
+_byref = ctypes.byref
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _sms: dict[int, int] = {}
 
 
-def _num_sms(device: torch.device) -> int:
-    i = device.index if device.index is not None else torch.cuda.current_device()
-    n = _sms.get(i)
+def _num_sms(device: int) -> int:
+    n = _sms.get(device)
     if n is None:
-        n = _sms[i] = torch.cuda.get_device_properties(i).multi_processor_count
+        n = _sms[device] = torch.cuda.get_device_properties(device).multi_processor_count
     return n
 
 
-def _on(device: torch.device):
-    """The library launches on the current device: makes the tensors' device current where it is not."""
-    if device.type != "cuda":
+def _device(first: torch.Tensor, *others) -> int:
+    """The index of the device that all tensors are on."""
+    i = first.get_device()
+    if i < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    for t in others:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"the tensors must be on one device: {t.device} and {first.device}")
+    return i
 
 
-def _same_device(device: torch.device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"the tensors must be on one device: {t.device} and {device}")
+def _handle(stream, device: int) -> int:
+    """The stream's handle; None: the device's current stream."""
+    if stream is None:
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _call(device: int, name: str, *args) -> None:
+    """Calls the library with `device` current (it launches on the current device)."""
+    fn = getattr(load(), name)
+    if device == torch.cuda.current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != 0:
+        check(rc, name)
+
+
+def _addr(t: torch.Tensor | None, dtype, name: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, heads: int | None = None, rows: int | None = None, d: int | None = None) -> int:
     """Checks a packed [tokens, heads, d] tensor whose tokens may be strided; returns the distance between tokens."""
-    if t.dim() != 3 or t.dtype != torch.float16:
+    shape = t.shape
+    if len(shape) != 3 or t.dtype != torch.float16:
         raise ValueError(f"{name} must be a float16 tensor [tokens, heads, d]")
-    n, h, dim = t.shape
+    n, h, dim = shape
     if (heads is not None and h != heads) or (rows is not None and n != rows) or (d is not None and dim != d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {heads}, {d}]")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows}, {heads}, {d}]")
     s0, s1, s2 = t.stride()
-    if (dim > 1 and s2 != 1) or (h > 1 and s1 != dim):
+    if (s2 != 1 and dim > 1) or (s1 != dim and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return s0 if n > 1 else h * dim
-
-
-def _rows_ptr(t: torch.Tensor) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr())
 
 
 def make_prompt(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, q_stride=None, k_stride=None,
@@ -75,115 +99,134 @@ def make_prompt(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, q_s
 
 
 def pkv_check_prompt(prompt: Prompt) -> int:
-    return load().pkv_check_prompt(ctypes.byref(prompt))
+    return load().pkv_check_prompt(_byref(prompt))
 
 
-def _seqs(cu_seqlens: torch.Tensor, num_seqs: int) -> ctypes.c_void_p:
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() != num_seqs + 1:
+def _fits(t: torch.Tensor, name: str, prompt: Prompt, heads: int, stride: int) -> int:
+    """Checks that a packed tensor is the one that the prompt describes; its address."""
+    s = _rows(t, name, heads, prompt.total_tokens, prompt.head_dim)
+    if s != stride and prompt.total_tokens > 1:
+        raise ValueError(f"{name}: its tokens are {s} elements apart, the prompt says {stride}")
+    return t.data_ptr()
+
+
+def _seqs(cu_seqlens: torch.Tensor, num_seqs: int) -> int:
+    if cu_seqlens.numel() != num_seqs + 1:
         raise ValueError(f"cu_seqlens must have {num_seqs + 1} entries")
-    return _ptr(cu_seqlens, torch.int32, "cu_seqlens")
+    return _addr(cu_seqlens, torch.int32, "cu_seqlens")
+
+
+def _start(start, num_seqs: int) -> int | None:
+    if start is not None and start.numel() != num_seqs:
+        raise ValueError(f"start must have {num_seqs} entries")
+    return _addr(start, torch.int32, "start")
+
+
+def _table(block_table: torch.Tensor, problem: Problem) -> int:
+    if tuple(block_table.shape) != (problem.batch, problem.max_pages_per_seq):
+        raise ValueError(f"block_table must have shape ({problem.batch}, {problem.max_pages_per_seq})")
+    return _addr(block_table, torch.int32, "block_table")
+
+
+def _attention(dev, prompt, q, k, v, cu_seqlens, scale, ws, out, stream) -> None:
+    _call(dev, "pkv_prompt_attention", _byref(prompt), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _seqs(cu_seqlens, prompt.num_seqs), scale, _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(),
+          out.data_ptr(), _handle(stream, dev))
 
 
 def pkv_prompt_attention(prompt: Prompt, q, k, v, cu_seqlens, scale, ws, out, stream=None) -> None:
-    dev = q.device
-    _same_device(dev, k, v, cu_seqlens, ws, out)
-    with _on(dev):
-        check(load().pkv_prompt_attention(
-            ctypes.byref(prompt), _rows_ptr(q), _rows_ptr(k), _rows_ptr(v), _seqs(cu_seqlens, prompt.num_seqs), scale,
-            _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(), _rows_ptr(out), _stream(stream)),
-            "pkv_prompt_attention")
-
-
-def _start(start, num_seqs: int) -> ctypes.c_void_p:
-    if start is not None and start.numel() != num_seqs:
-        raise ValueError(f"start must have {num_seqs} entries")
-    return _ptr(start, torch.int32, "start")
-
-
-def _table(block_table: torch.Tensor, problem: Problem) -> ctypes.c_void_p:
-    if tuple(block_table.shape) != (problem.batch, problem.max_pages_per_seq):
-        raise ValueError(f"block_table must have shape ({problem.batch}, {problem.max_pages_per_seq})")
-    return _ptr(block_table, torch.int32, "block_table")
+    dev = _device(q, k, v, cu_seqlens, ws, out)
+    _fits(q, "q", prompt, prompt.num_q_heads, prompt.q_stride)
+    _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride)
+    _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _fits(out, "out", prompt, prompt.num_q_heads, prompt.out_stride)
+    _attention(dev, prompt, q, k, v, cu_seqlens, scale, ws, out, stream)
 
 
 def pkv_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws,
                       stream=None) -> None:
-    dev = k.device
-    _same_device(dev, v, cu_seqlens, start, k_pool, v_pool, block_table, ws)
-    with _on(dev):
-        check(load().pkv_prompt_append(
-            ctypes.byref(problem), ctypes.byref(prompt), _rows_ptr(k), _rows_ptr(v),
-            _seqs(cu_seqlens, prompt.num_seqs), _start(start, prompt.num_seqs), _ptr(k_pool, torch.float16, "k_pool"),
-            _ptr(v_pool, torch.float16, "v_pool"), _table(block_table, problem), _num_sms(dev),
-            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "pkv_prompt_append")
+    dev = _device(k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws)
+    _call(dev, "pkv_prompt_append", _byref(problem), _byref(prompt),
+          _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride),
+          _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride), _seqs(cu_seqlens, prompt.num_seqs),
+          _start(start, prompt.num_seqs), _addr(k_pool, torch.float16, "k_pool"),
+          _addr(v_pool, torch.float16, "v_pool"), _table(block_table, problem), _num_sms(dev),
+          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
 
 
 def pkv_q4_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, pool, block_table, ws,
                          stream=None) -> None:
-    dev = k.device
-    _same_device(dev, v, cu_seqlens, start, pool, block_table, ws)
-    with _on(dev):
-        check(load().pkv_q4_prompt_append(
-            ctypes.byref(problem), ctypes.byref(prompt), _rows_ptr(k), _rows_ptr(v),
-            _seqs(cu_seqlens, prompt.num_seqs), _start(start, prompt.num_seqs), _ptr(pool, torch.uint8, "pool"),
-            _table(block_table, problem), _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)),
-            "pkv_q4_prompt_append")
+    dev = _device(k, v, cu_seqlens, start, pool, block_table, ws)
+    _call(dev, "pkv_q4_prompt_append", _byref(problem), _byref(prompt),
+          _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride),
+          _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride), _seqs(cu_seqlens, prompt.num_seqs),
+          _start(start, prompt.num_seqs), _addr(pool, torch.uint8, "pool"), _table(block_table, problem),
+          _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
 
 
 def pkv_q4_read(problem: Problem, prompt: Prompt, cu_seqlens, start, pool, block_table, k_out, v_out, ws,
                 stream=None) -> None:
-    dev = pool.device
-    _same_device(dev, k_out, v_out, cu_seqlens, start, block_table, ws)
-    with _on(dev):
-        check(load().pkv_q4_read(
-            ctypes.byref(problem), ctypes.byref(prompt), _seqs(cu_seqlens, prompt.num_seqs),
-            _start(start, prompt.num_seqs), _ptr(pool, torch.uint8, "pool"), _table(block_table, problem),
-            _rows_ptr(k_out), _rows_ptr(v_out), _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(),
-            _stream(stream)), "pkv_q4_read")
+    dev = _device(pool, k_out, v_out, cu_seqlens, start, block_table, ws)
+    _call(dev, "pkv_q4_read", _byref(problem), _byref(prompt), _seqs(cu_seqlens, prompt.num_seqs),
+          _start(start, prompt.num_seqs), _addr(pool, torch.uint8, "pool"), _table(block_table, problem),
+          _fits(k_out, "k_out", prompt, prompt.num_kv_heads, prompt.k_stride),
+          _fits(v_out, "v_out", prompt, prompt.num_kv_heads, prompt.v_stride), _num_sms(dev),
+          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
 
 
 def pkv_q4_pool_bytes(problem: Problem) -> int:
     n = ctypes.c_size_t(0)
-    check(load().pkv_q4_pool_bytes(ctypes.byref(problem), ctypes.byref(n)), "pkv_q4_pool_bytes")
+    check(load().pkv_q4_pool_bytes(_byref(problem), _byref(n)), "pkv_q4_pool_bytes")
     return int(n.value)
 
 
 def pkv_q4_workspace_bytes(problem: Problem, num_sms: int | None = None) -> int:
     """Bytes of the workspace of a 4-bit decode step (num_sms None: that of the current device)."""
     if num_sms is None:
-        num_sms = _num_sms(torch.device("cuda", torch.cuda.current_device()))
+        num_sms = _num_sms(torch.cuda.current_device())
     n = ctypes.c_size_t(0)
-    check(load().pkv_q4_workspace_bytes(ctypes.byref(problem), int(num_sms), ctypes.byref(n)),
-          "pkv_q4_workspace_bytes")
+    check(load().pkv_q4_workspace_bytes(_byref(problem), int(num_sms), _byref(n)), "pkv_q4_workspace_bytes")
     return int(n.value)
 
 
+def _step_tensors(problem: Problem, q, pool, block_table, seq_lens, out, k_new=None, v_new=None) -> None:
+    b, hq, hkv, d = problem.batch, problem.num_q_heads, problem.num_kv_heads, problem.head_dim
+    for t, name, want in ((q, "q", (b, hq, d)), (out, "out", (b, hq, d)), (k_new, "k_new", (b, hkv, d)),
+                          (v_new, "v_new", (b, hkv, d)), (pool, "pool", (problem.num_pages, hkv, PKV_Q4_BLOCK_BYTES))):
+        if t is not None and t.shape != want:
+            raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    if seq_lens.numel() != b:
+        raise ValueError(f"seq_lens must have {b} entries")
+
+
+def _step(problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out, stream) -> None:
+    dev = _device(q, k_new, v_new, pool, block_table, seq_lens, ws, out)
+    _step_tensors(problem, q, pool, block_table, seq_lens, out, k_new, v_new)
+    f16 = torch.float16
+    head = (_byref(problem), _addr(q, f16, "q"))
+    tail = (_addr(pool, torch.uint8, "pool"), _table(block_table, problem), _addr(seq_lens, torch.int32, "seq_lens"),
+            scale, _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _addr(out, f16, "out"),
+            _handle(stream, dev))
+    if k_new is None and v_new is None:
+        _call(dev, "pkv_q4_decode_step", *head, *tail)
+    else:
+        _call(dev, "pkv_q4_decode_step_append", *head, _addr(k_new, f16, "k_new"), _addr(v_new, f16, "v_new"), *tail)
+
+
 def pkv_q4_decode_step(problem: Problem, q, pool, block_table, seq_lens, scale, ws, out, stream=None) -> None:
-    dev = q.device
-    _same_device(dev, pool, block_table, seq_lens, ws, out)
-    with _on(dev):
-        check(load().pkv_q4_decode_step(
-            ctypes.byref(problem), _ptr(q, torch.float16, "q"), _ptr(pool, torch.uint8, "pool"),
-            _table(block_table, problem), _ptr(seq_lens, torch.int32, "seq_lens"), scale, _num_sms(dev),
-            _ptr(ws, torch.uint8, "ws"), ws.numel(), _ptr(out, torch.float16, "out"), _stream(stream)),
-            "pkv_q4_decode_step")
+    _step(problem, q, None, None, pool, block_table, seq_lens, scale, ws, out, stream)
 
 
 def pkv_q4_decode_step_append(problem: Problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out,
                               stream=None) -> None:
-    dev = q.device
-    _same_device(dev, k_new, v_new, pool, block_table, seq_lens, ws, out)
-    with _on(dev):
-        check(load().pkv_q4_decode_step_append(
-            ctypes.byref(problem), _ptr(q, torch.float16, "q"), _ptr(k_new, torch.float16, "k_new"),
-            _ptr(v_new, torch.float16, "v_new"), _ptr(pool, torch.uint8, "pool"), _table(block_table, problem),
-            _ptr(seq_lens, torch.int32, "seq_lens"), scale, _num_sms(dev), _ptr(ws, torch.uint8, "ws"), ws.numel(),
-            _ptr(out, torch.float16, "out"), _stream(stream)), "pkv_q4_decode_step_append")
+    if k_new is None or v_new is None:
+        raise ValueError("k_new and v_new are required")
+    _step(problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out, stream)
 
 
 # ------------------------------------------------------------------------------- the same, described by the tensors
-def _torch_stream(stream, device) -> torch.cuda.Stream | None:
-    """`stream` as a torch stream where it is not the current one (what the call allocates is recorded on it)."""
+def _other(stream, device: int) -> torch.cuda.Stream | None:
+    """`stream` as a torch stream where it is not the device's current one."""
     if stream is None:
         return None
     if not isinstance(stream, torch.cuda.Stream):
@@ -191,20 +234,21 @@ def _torch_stream(stream, device) -> torch.cuda.Stream | None:
     return None if stream == torch.cuda.current_stream(device) else stream
 
 
-def _scratch(nbytes: int, ws, device, stream):
+def _scratch(nbytes: int, ws, device: int, stream):
     """The caller's workspace, or one for this call alone."""
     if ws is not None:
         return ws
-    other = _torch_stream(stream, device)
-    if other is None:
-        return alloc_workspace(nbytes, device)
-    with torch.cuda.stream(other):
-        return alloc_workspace(nbytes, device)
+    other = _other(stream, device)
+    with torch.cuda.device(device):
+        if other is None:
+            return alloc_workspace(nbytes, device)
+        with torch.cuda.stream(other):
+            return alloc_workspace(nbytes, device)
 
 
-def _new(shape, device, stream) -> torch.Tensor:
+def _new(shape, device: int, stream) -> torch.Tensor:
     out = torch.empty(shape, dtype=torch.float16, device=device)
-    other = _torch_stream(stream, device)
+    other = _other(stream, device)
     if other is not None:
         other.wait_stream(torch.cuda.current_stream(device))  # the memory may still be read on the current stream
         out.record_stream(other)
@@ -225,13 +269,15 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     ks = _rows(k, "k", None, t, d)
     hkv = k.shape[1]
     vs = _rows(v, "v", hkv, t, d)
-    dev = q.device
-    with _on(dev):
-        if out is None:
-            out = _new((t, hq, d), dev, stream)
-        prompt = Prompt(cu_seqlens.numel() - 1, t, hq, hkv, d, 0, qs, ks, vs, _rows(out, "out", hq, t, d))
-        pkv_prompt_attention(prompt, q, k, v, cu_seqlens, 1.0 / math.sqrt(d) if scale is None else scale,
-                             _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), out, stream)
+    dev = _device(q, k, v, cu_seqlens, ws, out)
+    if out is None:
+        out = _new((t, hq, d), dev, stream)
+        os = hq * d
+    else:
+        os = _rows(out, "out", hq, t, d)
+    prompt = Prompt(cu_seqlens.numel() - 1, t, hq, hkv, d, 0, qs, ks, vs, os)
+    _attention(dev, prompt, q, k, v, cu_seqlens, 1.0 / math.sqrt(d) if scale is None else scale,
+               _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), out, stream)
     return out
 
 
@@ -251,9 +297,8 @@ def prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, k_
     b, pages = block_table.shape
     problem = make_problem(b, hkv, hkv, d, k_pool.shape[1], k_pool.shape[0], pages)
     prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
-    with _on(k.device):
-        pkv_prompt_append(problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table,
-                          _scratch(PKV_PROMPT_WS_BYTES, ws, k.device, stream), stream)
+    pkv_prompt_append(problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table,
+                      _scratch(PKV_PROMPT_WS_BYTES, ws, _device(k), stream), stream)
 
 
 def _check_pool(pool: torch.Tensor) -> int:
@@ -282,9 +327,8 @@ def q4_prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
     b, pages = block_table.shape
     problem = make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages)
     prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
-    with _on(k.device):
-        pkv_q4_prompt_append(problem, prompt, k, v, cu_seqlens, start, pool, block_table,
-                             _scratch(PKV_PROMPT_WS_BYTES, ws, k.device, stream), stream)
+    pkv_q4_prompt_append(problem, prompt, k, v, cu_seqlens, start, pool, block_table,
+                         _scratch(PKV_PROMPT_WS_BYTES, ws, _device(k), stream), stream)
 
 
 def q4_read(cu_seqlens: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor,
@@ -293,23 +337,21 @@ def q4_read(cu_seqlens: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     """Tokens of 4-bit pages as packed fp16 rows (include/pkv.h, pkv_q4_read). Returns k_out, v_out
     [total_tokens, Hkv, d]; give either both of them or total_tokens."""
     hkv, d = _check_pool(pool), 128
-    dev = pool.device
     b, pages = block_table.shape
-    with _on(dev):
-        if k_out is None and v_out is None:
-            if total_tokens is None:
-                raise ValueError("give k_out and v_out, or total_tokens")
-            k_out = _new((int(total_tokens), hkv, d), dev, stream)
-            v_out = _new((int(total_tokens), hkv, d), dev, stream)
-        elif k_out is None or v_out is None:
-            raise ValueError("give both of k_out and v_out, or neither")
-        t = k_out.shape[0]
-        if total_tokens is not None and total_tokens != t:
-            raise ValueError(f"k_out has {t} rows, total_tokens is {total_tokens}")
-        prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, _rows(k_out, "k_out", hkv, t, d),
-                        _rows(v_out, "v_out", hkv, t, d), hkv * d)
-        pkv_q4_read(make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages), prompt, cu_seqlens, start, pool,
-                    block_table, k_out, v_out, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both of k_out and v_out, or neither")
+    if k_out is None:
+        if total_tokens is None:
+            raise ValueError("give k_out and v_out, or total_tokens")
+        dev = _device(pool)
+        k_out, v_out = (_new((int(total_tokens), hkv, d), dev, stream) for _ in range(2))
+    t = k_out.shape[0]
+    if total_tokens is not None and total_tokens != t:
+        raise ValueError(f"k_out has {t} rows, total_tokens is {total_tokens}")
+    prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, _rows(k_out, "k_out", hkv, t, d),
+                    _rows(v_out, "v_out", hkv, t, d), hkv * d)
+    pkv_q4_read(make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages), prompt, cu_seqlens, start, pool, block_table,
+                k_out, v_out, _scratch(PKV_PROMPT_WS_BYTES, ws, _device(pool), stream), stream)
     return k_out, v_out
 
 
@@ -323,24 +365,13 @@ def q4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, se
     int32 on the device. Keep ws (pkv_q4_workspace_bytes, alloc_workspace) over the steps of a loop.
     """
     problem = q4_problem(q, pool, block_table)
-    b, hq, d = q.shape
-    if seq_lens.numel() != b:
-        raise ValueError(f"seq_lens must have {b} entries")
     if (k_new is None) != (v_new is None):
         raise ValueError("give both of k_new and v_new, or neither")
-    dev = q.device
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(dev):
-        if out is None:
-            out = _new((b, hq, d), dev, stream)
-        elif out.shape != q.shape:
-            raise ValueError(f"out must have shape {tuple(q.shape)}")
-        if ws is None:
-            ws = _scratch(pkv_q4_workspace_bytes(problem, _num_sms(dev)), None, dev, stream)
-        if k_new is None:
-            pkv_q4_decode_step(problem, q, pool, block_table, seq_lens, scale, ws, out, stream)
-        else:
-            if k_new.shape != (b, pool.shape[1], d) or v_new.shape != k_new.shape:
-                raise ValueError(f"k_new and v_new must have shape {(b, pool.shape[1], d)}")
-            pkv_q4_decode_step_append(problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out, stream)
+    dev = _device(q)
+    if out is None:
+        out = _new(tuple(q.shape), dev, stream)
+    if ws is None:
+        ws = _scratch(pkv_q4_workspace_bytes(problem, _num_sms(dev)), None, dev, stream)
+    scale = 1.0 / math.sqrt(q.shape[2]) if scale is None else scale
+    _step(problem, q, k_new, v_new, pool, block_table, seq_lens, scale, ws, out, stream)
     return out
