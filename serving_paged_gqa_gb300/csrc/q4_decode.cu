@@ -40,14 +40,15 @@ constexpr int kStageBytes = kUnitPages * kQ4Block;
 constexpr int kChunk = 32 / kUnitPages;  // units whose block-table entries one warp-wide read brings
 constexpr int kCombRow = kHeadDim + 4;  // floats per partial output row: rows land 4 banks apart
 constexpr uint32_t kAllPages = (1u << kUnitPages) - 1u;
-constexpr int kMinUnits = 4;            // units per CTA below which fewer CTAs take part
+constexpr int kMinUnits = 8;            // units per CTA below which fewer CTAs take part
 
 // A piece's part of one (row, KV head) pair.
 struct Segment {
     int32_t b, h, units;  // units < 0: no more segments
     int32_t out;          // -1: the whole pair, written to out; else the state that it leaves
     int32_t first_cta, ctas;  // the pair's pieces
-    int32_t pad[2];
+    int32_t len;              // tokens of the row
+    int32_t append;           // 1: the new token is in this piece
 };
 
 // consumers, stages, partial-result buffers, resident CTAs
@@ -65,10 +66,12 @@ struct Shape {
     static constexpr int off_seg = off_comb_ml + NB * NC * G * 8;
     static constexpr int off_meta = off_seg + (kSlots + 2) * (int)sizeof(Segment);  // and two pairs to merge
     static constexpr int off_bars = off_meta + NS * 4;
-    static constexpr int nbars = 2 * NS + 3 * kSlots + 2 * NB;
+    static constexpr int nbars = 2 * NS + 3 * kSlots + 2 * NB + 2;
     static constexpr int off_misc = off_bars + nbars * 8;
-    static constexpr int smem = off_misc + 64;
+    static constexpr int off_new = (off_misc + 64 + 15) / 16 * 16;  // a block with the new token in its slot
+    static constexpr int smem = off_new + kQ4Block;
     static_assert(off_bars % 8 == 0 && off_comb % 16 == 0 && smem <= 227 * 1024, "layout");
+    static constexpr int kFactors = NB * NC * kCombRow;  // pieces of a pair whose factors fit (the grid is smaller)
 };
 
 __device__ __forceinline__ int row_length(const Q4Params& p, int b) {
@@ -87,6 +90,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
+}
+
+// The bytes of one token of a block, K and V: 64 code bytes and 8 of parameters each.
+__device__ __forceinline__ void copy_token(uint8_t* dst, const uint8_t* src, int r, int lane) {
+#pragma unroll
+    for (int d = lane; d < 64; d += 32) {
+        const int kb = q4_k_byte(r, d), vb = kQ4Half + q4_v_byte(r, d);
+        dst[kb] = src[kb];
+        dst[vb] = src[vb];
+    }
+    if (lane < 4) {
+        const int at = (lane >> 1) * kQ4Half + kQ4Codes + r * 8 + (lane & 1) * 4;
+        *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(src + at);
+    }
 }
 
 __device__ __forceinline__ float2 half2_of(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
@@ -108,6 +125,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
     uint64_t* seg_empty = seg_q + kSlots;
     uint64_t* part_full = seg_empty + kSlots;
     uint64_t* part_empty = part_full + NB;
+    uint64_t* merged = part_empty + NB;
+    uint64_t* new_full = merged + 1;
+    uint8_t* new_blk = smem + L::off_new;
     Segment* segs = reinterpret_cast<Segment*>(smem + L::off_seg);
     Segment* merges = segs + kSlots;
     uint32_t* meta = reinterpret_cast<uint32_t*>(smem + L::off_meta);
@@ -131,6 +151,8 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             mbar_init(&part_full[i], NC);
             mbar_init(&part_empty[i], 1);
         }
+        mbar_init(merged, 1);
+        mbar_init(new_full, 1);
         *abort_flag = 0;
         *n_merges = 0;
         mbar_fence_init();
@@ -207,7 +229,8 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 s.out = n == units ? -1 : 2 * cta + (u == 0 ? 1 : 0);
                 s.first_cta = cta_of(pos - u, total, ctas);
                 s.ctas = cta_of(pos - u + units - 1, total, ctas) - s.first_cta + 1;
-                s.pad[0] = s.pad[1] = 0;
+                s.len = len;
+                s.append = p.k_new && u + n == units ? 1 : 0;
                 segs[slot] = s;
                 mbar_arrive(&seg_full[slot]);
                 mbar_arrive_expect_tx(&seg_q[slot], G * kRowBytes);
@@ -295,6 +318,19 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[slot]);
             if (s.units < 0) break;
+            if (s.append) {
+                // The new token, quantised while the pages are on their way: into the pool, and into a block that the
+                // consumer of the pair's last unit takes it from (what the page's copy brings of its slot is not used).
+                const int r = (s.len - 1) % kPageSize;
+                const int32_t phys = p.block_table[(int64_t)s.b * p.max_pages + (s.len - 1) / kPageSize];
+                const int64_t src = ((int64_t)s.b * p.Hkv + s.h) * kHeadDim;
+                q4_quantise_row(static_cast<const __half*>(p.k_new) + src, new_blk, r, false, lane);
+                q4_quantise_row(static_cast<const __half*>(p.v_new) + src, new_blk + kQ4Half, r, true, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(new_full);
+                if (phys >= 0 && phys < p.num_pages)
+                    copy_token(static_cast<uint8_t*>(p.pool) + ((int64_t)phys * p.Hkv + s.h) * kQ4Block, new_blk, r, lane);
+            }
             if (!warp_wait(&part_full[e], (k / NB) & 1, ctx)) break;
             const float* co = comb + e * NC * G * kCombRow;
             const float2* cml = comb_ml + e * NC * G;
@@ -370,12 +406,12 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         // scores are kept in units of 2^-24 / (|scale| * log2(e)): X = sum_g scale_g (q.code_g) 2^-24 + ..., x = X * xk
         const float xk = fabsf(p.scale_log2) * 16777216.f;
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs
-        int seq = 0;
+        int seq = 0, new_seen = 0;  // units, new tokens of the segments before
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int slot = k % kSlots, e = k % NB;
             if (!warp_wait(&seg_full[slot], (k / kSlots) & 1, ctx)) break;
-            const int n = segs[slot].units, sb = segs[slot].b, sh = segs[slot].h;
+            const int n = segs[slot].units, seg_append = segs[slot].append;
             if (n < 0) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&seg_empty[slot]);
@@ -444,27 +480,13 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 const uint32_t okmask = (mt >> 8) & kAllPages;
                 const bool append = (mt >> 12) & 1;
                 if (append) {
-                    const int r = (nv - 1) % kPageSize, pg = (nv - 1) / kPageSize;
-                    if ((okmask >> pg) & 1) {
-                        uint8_t* blk = stage + pg * kQ4Block;
-                        const int64_t src = ((int64_t)sb * p.Hkv + sh) * kHeadDim;
-                        q4_quantise_row(static_cast<const __half*>(p.k_new) + src, blk, r, false, lane);
-                        q4_quantise_row(static_cast<const __half*>(p.v_new) + src, blk + kQ4Half, r, true, lane);
-                        __syncwarp();
-                        // the token's bytes into the pool: 64 code bytes and 8 parameter bytes of K and of V
-                        const int32_t phys = p.block_table[(int64_t)sb * p.max_pages + (row_length(p, sb) - 1) / kPageSize];
-                        uint8_t* dst = static_cast<uint8_t*>(p.pool) + ((int64_t)phys * p.Hkv + sh) * kQ4Block;
-#pragma unroll
-                        for (int d = lane; d < 64; d += 32) {
-                            const int kb = q4_k_byte(r, d), vb = kQ4Half + q4_v_byte(r, d);
-                            dst[kb] = blk[kb];
-                            dst[vb] = blk[vb];
-                        }
-                        if (lane < 4) {
-                            const int at = (lane >> 1) * kQ4Half + kQ4Codes + r * 8 + (lane & 1) * 4;
-                            *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(blk + at);
-                        }
+                    if (!warp_wait(new_full, new_seen & 1, ctx)) {
+                        ok = false;
+                        break;
                     }
+                    const int pg = (nv - 1) / kPageSize;
+                    if ((okmask >> pg) & 1) copy_token(stage + pg * kQ4Block, new_blk, (nv - 1) % kPageSize, lane);
+                    __syncwarp();
                 }
                 const bool whole = nv == kUnitTokens && okmask == kAllPages;
                 if (!whole) {  // tokens that the row does not have get parameters of 0, and scores of -inf below
@@ -640,6 +662,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             }
             if (!ok) break;
             seq += n;
+            // every consumer sees every phase of this barrier (a parity two phases on would pass at once)
+            if (seg_append && !warp_wait(new_full, new_seen & 1, ctx)) break;
+            new_seen += seg_append;
             // hand this warp's partial result of the segment to the epilogue warp
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
@@ -681,76 +706,91 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         }
     }
 
-    // The pairs whose last piece arrived here: warps take their states in turn, eight loads of one head in flight.
+    // The pairs whose last piece arrived here. The states of a pair come through the ring's memory by bulk copies, all in
+    // flight together (read with loads, 8 a warp at a time, 38 states of 4 heads took 8 us); meanwhile a warp per head
+    // takes the maximum of the references and turns them into factors.
     __syncthreads();
     const int nm = *abort_flag ? 0 : *n_merges;
+    constexpr int kStateBytes = G * kHeadDim * 4;
+    constexpr int kHeld = NS * kStageBytes / kStateBytes;  // states that the ring's memory holds
+    float* factor = comb;                                  // [state][head]
+    float* sums = reinterpret_cast<float*>(comb_ml);       // [head]
+    uint32_t phase = 0;
     for (int i = 0; i < nm; ++i) {
         const Segment s = merges[i];
-        if (warp < NC) {
-            for (int g = 0; g < G; ++g) {
-                float M = -INFINITY, l = 0.f;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c0 = warp; c0 < s.ctas; c0 += 8 * NC) {
-                    float2 ml[8];
-                    float4 v[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int at = c0 + c * NC;
-                        const int64_t state = (int64_t)(2 * (s.first_cta + at) + (at == 0 ? 1 : 0)) * G + g;
-                        ml[c] = at < s.ctas ? __ldcg(p.ml + state) : make_float2(-INFINITY, 0.f);
-                        v[c] = at < s.ctas ? __ldcg(reinterpret_cast<const float4*>(p.acc + state * kHeadDim) + lane)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    float mn = M;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) mn = fmaxf(mn, ml[c].x);
-                    const float ref = mn == -INFINITY ? 0.f : mn;
-                    const float f = fast_exp2(M - ref);
-                    M = mn;
-                    l *= f;
-                    a.x *= f;
-                    a.y *= f;
-                    a.z *= f;
-                    a.w *= f;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float e = fast_exp2(ml[c].x - ref);
-                        l += e * ml[c].y;
-                        a.x += e * v[c].x;
-                        a.y += e * v[c].y;
-                        a.z += e * v[c].z;
-                        a.w += e * v[c].w;
-                    }
-                }
-                *reinterpret_cast<float4*>(comb + (warp * G + g) * kCombRow + lane * 4) = a;
-                if (lane == 0) comb_ml[warp * G + g] = make_float2(M, l);
-            }
+        const int64_t first = 2 * (int64_t)s.first_cta;  // state c of the pair: 2 (first_cta + c), + 1 for c = 0
+        auto fetch = [&](int c0) {                       // warp 0: states c0 .. + kHeld - 1
+            const int n = min(kHeld, s.ctas - c0);
+            if (lane == 0) mbar_arrive_expect_tx(merged, n * kStateBytes);
+            __syncwarp();
+            for (int c = c0 + lane; c < c0 + n; c += 32)
+                bulk_g2s(smem + (c - c0) * kStateBytes, p.acc + (first + 2 * c + (c == 0)) * (G * kHeadDim), kStateBytes, merged);
+        };
+        if (warp == 0) {
+            fence_proxy_async_global();
+            fetch(0);
         }
-        __syncthreads();
         for (int g = warp; g < G; g += NC + 2) {
             float M = -INFINITY, l = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = lane; c < s.ctas; c += 32) M = fmaxf(M, __ldcg(p.ml + (first + 2 * c + (c == 0)) * G + g).x);
 #pragma unroll
-            for (int w = 0; w < NC; ++w) M = fmaxf(M, comb_ml[w * G + g].x);
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int w = 0; w < NC; ++w) {
-                const float2 ml = comb_ml[w * G + g];
+            for (int c = lane; c < s.ctas; c += 32) {
+                const float2 ml = __ldcg(p.ml + (first + 2 * c + (c == 0)) * G + g);
                 const float f = fast_exp2(ml.x - ref);
-                const float4 v = *reinterpret_cast<const float4*>(comb + (w * G + g) * kCombRow + lane * 4);
+                factor[c * G + g] = f;
                 l += f * ml.y;
-                a.x += f * v.x;
-                a.y += f * v.y;
-                a.z += f * v.z;
-                a.w += f * v.w;
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint2 y;
-            y.x = pack_half2(a.x * inv, a.y * inv);
-            y.y = pack_half2(a.z * inv, a.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + ((int64_t)s.b * p.Hq + s.h * G + g) * kHeadDim + lane * 4) = y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) sums[g] = l;
+        }
+        constexpr int kPer = (G + NC + 1) / (NC + 2);  // heads a warp
+        float4 acc[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool here = true;
+        for (int c0 = 0; c0 < s.ctas && here; c0 += kHeld) {
+            __syncthreads();  // the factors are there; the states before have been used
+            if (c0 > 0 && warp == 0) {
+                fence_proxy_async_smem();
+                fetch(c0);
+            }
+            here = warp_wait(merged, phase, ctx);
+            phase ^= 1;
+            const int n = here ? min(kHeld, s.ctas - c0) : 0;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int g = warp + j * (NC + 2);
+                if (g < G) {
+#pragma unroll 4
+                    for (int c = 0; c < n; ++c) {
+                        const float f = factor[(c0 + c) * G + g];
+                        const float4 v = reinterpret_cast<const float4*>(smem + c * kStateBytes + g * kHeadDim * 4)[lane];
+                        acc[j].x += f * v.x;
+                        acc[j].y += f * v.y;
+                        acc[j].z += f * v.z;
+                        acc[j].w += f * v.w;
+                    }
+                }
+            }
+            here = __syncthreads_and(here);  // all leave together after a time-out
+        }
+        if (!here) break;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int g = warp + j * (NC + 2);
+            if (g < G) {
+                const float l = sums[g], inv = l == 0.f ? 0.f : 1.f / l;
+                uint2 y;
+                y.x = pack_half2(acc[j].x * inv, acc[j].y * inv);
+                y.y = pack_half2(acc[j].z * inv, acc[j].w * inv);
+                *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + ((int64_t)s.b * p.Hq + s.h * G + g) * kHeadDim + lane * 4) = y;
+            }
         }
         __syncthreads();
+        if (warp == 0) fence_proxy_async_smem();
     }
 }
 
@@ -769,7 +809,7 @@ int launch(Q4Params p, int num_sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    const int ctas = L::per_sm * num_sms;
+    const int ctas = std::min(L::per_sm * num_sms, L::kFactors);
     char* ws = reinterpret_cast<char*>(p.hdr);
     int64_t off = sizeof(pkv_ws_header);
     p.counters = reinterpret_cast<uint32_t*>(ws + off);
