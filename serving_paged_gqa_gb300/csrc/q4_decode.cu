@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         const int t4 = lane & 3;   // head columns 2 t4, 2 t4 + 1 of S^T and O^T
         // Up to four query heads leave half of the 8 columns empty. The lanes of columns 4-7 then take over the scores of
         // tokens 8-15 of a page from the lanes of columns 0-3 (kFold): every lane has one token instead of two, half of
-        // the scalar work. Their weights become columns 4-7 of the second product, whose sums are added at the end.
+        // the scalar work; the second product's columns 4-7 carry the weights' second part.
         constexpr bool kFold = G <= 4;
         constexpr int kTok = kFold ? 1 : 2;  // tokens of a page that this lane scores: tok0, and tok0 + 8
         const int tok0 = kFold ? g8 + ((t4 >> 1) << 3) : g8;
@@ -616,13 +616,17 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                     for (int i2 = 0; i2 < 2; ++i2) nref[nt][i2] = ref[nt][i2] == -INFINITY ? 0.f : -ref[nt][i2];
-                uint32_t pb[kUnitPages][kNT][2][kTok];  // [page][nt][group]: weights * scale, tokens 0-7 and 8-15 as the B operand
+                // Weights * scale as the B operand, in two fp16 parts, the second what the first's rounding left: the codes
+                // are all positive, so a rounding of the weights would meet their common offset of 7.5 steps and cost three
+                // times the output's own rounding. Folded, the two parts share the columns (0-3, 4-7) and take no
+                // more products than one.
+                uint32_t pb[kUnitPages][kNT][2][kFold ? 1 : 2][2];  // [page][nt][group][part][tokens 0-7, 8-15]
 #pragma unroll
                 for (int pg = 0; pg < kUnitPages; ++pg)
 #pragma unroll
                     for (int u2 = 0; u2 < kTok; ++u2) {
                         const uint2 pv = *reinterpret_cast<const uint2*>(stage + pg * kQ4Block + kQ4Half + kQ4Codes + (tok0 + 8 * u2) * 8);
-                        const float2 a0 = half2_of(pv.x), a1 = half2_of(pv.y);
+                        const float2 par[2] = {half2_of(pv.x), half2_of(pv.y)};
 #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
                             float w[2];
@@ -630,11 +634,26 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             for (int i2 = 0; i2 < 2; ++i2) {
                                 w[i2] = fast_exp2(fmaf(x[nt][pg][u2][i2], xk, nref[nt][i2]));
                                 l[nt][i2] += w[i2];
-                                osum[nt][0][i2] = fmaf(w[i2], a0.y, osum[nt][0][i2]);
-                                osum[nt][1][i2] = fmaf(w[i2], a1.y, osum[nt][1][i2]);
+                                osum[nt][0][i2] = fmaf(w[i2], par[0].y, osum[nt][0][i2]);
+                                osum[nt][1][i2] = fmaf(w[i2], par[1].y, osum[nt][1][i2]);
                             }
-                            pb[pg][nt][0][u2] = transpose8x8(pack_half2(w[0] * a0.x, w[1] * a0.x));
-                            pb[pg][nt][1][u2] = transpose8x8(pack_half2(w[0] * a1.x, w[1] * a1.x));
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float v0 = w[0] * par[g].x, v1 = w[1] * par[g].x;
+                                const uint32_t hi = pack_half2(v0, v1);
+                                const float2 hf = half2_of(hi);
+                                const uint32_t th = transpose8x8(hi), tl = transpose8x8(pack_half2(v0 - hf.x, v1 - hf.y));
+                                if (kFold) {
+                                    // rows 0-3 of the transposes are tokens 0-7, rows 4-7 tokens 8-15 of the same heads;
+                                    // columns 0-3 take the first part of all 16 tokens, columns 4-7 the second
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, g8 < 4 ? tl : th, 16);
+                                    pb[pg][nt][g][0][0] = g8 < 4 ? th : got;
+                                    pb[pg][nt][g][0][1] = g8 < 4 ? got : tl;
+                                } else {
+                                    pb[pg][nt][g][0][u2] = th;
+                                    pb[pg][nt][g][kFold ? 0 : 1][u2] = tl;
+                                }
+                            }
                         }
                     }
 #pragma unroll
@@ -647,13 +666,14 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                     for (int dt = 0; dt < 4; ++dt) {
                         const uint32_t a8 = wa[dt] >> 8, b8 = wb[dt] >> 8;
 #pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) {
-                            // folded: rows 0-3 of the transpose are tokens 0-7, rows 4-7 are tokens 8-15
-                            const uint32_t p00 = kFold && g8 >= 4 ? 0u : pb[pg][nt][0][0], p10 = kFold && g8 >= 4 ? 0u : pb[pg][nt][1][0];
-                            const uint32_t p01 = kFold && g8 < 4 ? 0u : pb[pg][nt][0][kTok - 1], p11 = kFold && g8 < 4 ? 0u : pb[pg][nt][1][kTok - 1];
-                            mma_16816(o[nt][dt], wa[dt] & 0x000F000Fu, a8 & 0x000F000Fu, wb[dt] & 0x000F000Fu, b8 & 0x000F000Fu, p00, p01);
-                            mma_16816(o[nt][4 + dt], wa[dt] & 0x00F000F0u, a8 & 0x00F000F0u, wb[dt] & 0x00F000F0u, b8 & 0x00F000F0u, p10, p11);
-                        }
+                        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                            for (int part = 0; part < (kFold ? 1 : 2); ++part) {
+                                mma_16816(o[nt][dt], wa[dt] & 0x000F000Fu, a8 & 0x000F000Fu, wb[dt] & 0x000F000Fu,
+                                          b8 & 0x000F000Fu, pb[pg][nt][0][part][0], pb[pg][nt][0][part][1]);
+                                mma_16816(o[nt][4 + dt], wa[dt] & 0x00F000F0u, a8 & 0x00F000F0u, wb[dt] & 0x00F000F0u,
+                                          b8 & 0x00F000F0u, pb[pg][nt][1][part][0], pb[pg][nt][1][part][1]);
+                            }
                     }
                 }
                 if (append || !whole) fence_proxy_async_smem();  // our stores into the stage before the next copy into it
