@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         // --------------------------------------------------------------------------------------- consumers
         const int g8 = lane >> 2;  // token row of S^T, dim row of O^T, head column of the B operand
         const int t4 = lane & 3;   // head columns 2 t4, 2 t4 + 1 of S^T and O^T
-        // Up to four query heads leave half of the 8 columns empty. The lanes of columns 4-7 then take over the scores of
-        // tokens 8-15 of a page from the lanes of columns 0-3 (kFold): every lane has one token instead of two, half of
-        // the scalar work; the second product's columns 4-7 carry the weights' second part.
+        // Up to four query heads leave half of the 8 columns empty. They get the heads a second time (kFold), and their lanes
+        // take over the scores of tokens 8-15 of a page: every lane has one token instead of two, half of the scalar work.
+        // In the second product those columns carry the weights' second part.
         constexpr bool kFold = G <= 4;
         constexpr int kTok = kFold ? 1 : 2;  // tokens of a page that this lane scores: tok0, and tok0 + 8
         const int tok0 = kFold ? g8 + ((t4 >> 1) << 3) : g8;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             const uint8_t* qrow = smem + L::off_q + slot * G * kRowBytes;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
-                const int head = nt * 8 + g8;
+                const int head = kFold ? g8 & 3 : nt * 8 + g8;
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                     uint32_t wa[2][4], wb[2][4];
                     float c0[2][kNT][4], c1[2][kNT][4];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < (kUnitPages - p0 < 2 ? 1 : 2); ++y) {
                         const uint8_t* blk = stage + (p0 + y) * kQ4Block;
                         const uint4 ka = *reinterpret_cast<const uint4*>(blk + lane * 16);
                         const uint4 kb = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
+                        for (int y = 0; y < (kUnitPages - p0 < 2 ? 1 : 2); ++y) {
                             const uint32_t a8 = wa[y][ks] >> 8, b8 = wb[y][ks] >> 8;
 #pragma unroll
                             for (int nt = 0; nt < kNT; ++nt) {
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             }
                         }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < (kUnitPages - p0 < 2 ? 1 : 2); ++y) {
                         const int pg = p0 + y;
 #pragma unroll
                         for (int u2 = 0; u2 < kTok; ++u2) {
@@ -549,11 +549,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                                 for (int i2 = 0; i2 < 2; ++i2) {
                                     float d0 = c0[y][nt][2 * u2 + i2], d1 = c1[y][nt][2 * u2 + i2];
-                                    if (kFold) {
-                                        const float e0 = __shfl_up_sync(0xffffffffu, c0[y][nt][2 + i2], 2);
-                                        const float e1 = __shfl_up_sync(0xffffffffu, c1[y][nt][2 + i2], 2);
-                                        d0 = t4 < 2 ? d0 : e0;
-                                        d1 = t4 < 2 ? d1 : e1;
+                                    if (kFold && t4 >= 2) {  // tokens 8-15
+                                        d0 = c0[y][nt][2 + i2];
+                                        d1 = c1[y][nt][2 + i2];
                                     }
                                     x[nt][pg][u2][i2] = fmaf(d0, a0.x, fmaf(d1, a1s, fmaf(a0.y, qs[nt][0][i2], a1.y * qs[nt][1][i2])));
                                 }
