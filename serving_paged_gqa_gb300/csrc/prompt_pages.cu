@@ -169,8 +169,8 @@ __device__ __forceinline__ Group group_of(__half2 extremes) {  // (min, -max)
 // two values, lies in [128, 256), where an fp32 has 16 fraction bits: byte 2 holds the code (192 is 0 modulo 16, and
 // 0.5 makes the truncation a rounding), and the low 16 bits are the quotient's distance above the last tie, plus 2.
 // The reciprocal, the constant and the sum are off by less than 2 of those units together (|offset / scale| <= 60), so
-// where the distance is below 4 the true quotient could round the other way, and the definition's division decides.
-__device__ __forceinline__ uint2 codes8(const uint4& x, const Group& g) {
+// where the distance is below 4 the true quotient could round the other way (doubt): the definition's division decides.
+__device__ __forceinline__ uint2 codes8(const uint4& x, const Group& g, bool& doubt) {
     const __half2* h = reinterpret_cast<const __half2*>(&x);
     const uint64_t inv2 = pack_f32x2(g.inv, g.inv), add2 = pack_f32x2(g.add, g.add);
     uint32_t k[8], least = 0xffffffffu;
@@ -183,8 +183,7 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, const Group& g) {
         k[2 * i + 1] = __float_as_uint(b);
         least = __vminu2(least, __byte_perm(k[2 * i], k[2 * i + 1], 0x5410));
     }
-    if (g.exact || (least & 0xffffu) < 4u || least < 0x40000u)
-        return codes8_exact(x, __low2float(g.par), __high2float(g.par));
+    doubt = g.exact || (least & 0xffffu) < 4u || least < 0x40000u;
     uint2 y;
     y.x = __byte_perm(__byte_perm(k[0], k[1], 0x0062), __byte_perm(k[2], k[3], 0x0062), 0x5410) & 0x0f0f0f0fu;
     y.y = __byte_perm(__byte_perm(k[4], k[5], 0x0062), __byte_perm(k[6], k[7], 0x0062), 0x5410) & 0x0f0f0f0fu;
@@ -199,9 +198,10 @@ struct Quant {
     Group groups[32];
 };
 
-// The staged rows of K (v = 0) or V (v = 1) into their half block. Rolled over the tokens: unrolled, the code of
-// one page is 24 KB, and a call of a few pages spends 8 us of its 12 on fetching instructions.
-__device__ __forceinline__ void quantise_page(Quant& w, int v, int lane) {
+// The staged rows of K or V into their half block. Rolled over the tokens: unrolled, the code of one page is 24 KB, and
+// a call of a few pages spends most of its time on fetching instructions.
+template <bool kV>
+__device__ __forceinline__ void quantise_page(Quant& w, int lane) {
     const int c = lane & 15, odd = lane >> 4, c7 = c & 7, hi = c >> 3;
     // The extremes of the 8 tokens, reduced over the group's 8 lanes so that lane c7 ends with token i = c7; it works out
     // that token's parameters and the reciprocal of its scale for all of them.
@@ -218,21 +218,18 @@ __device__ __forceinline__ void quantise_page(Quant& w, int v, int lane) {
         w.groups[at] = g;
     }
     __syncwarp();
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-        const int r = 2 * i + odd;
-        const uint2 code = codes8(w.rows[i][lane], w.groups[2 * r + hi]);
-        // Group 1's codes go into the high 4 bits of group 0's bytes. The lane of group 0 keeps dims 8 c7 .. + 3, that
-        // of group 1 dims + 4 .. + 7: four bytes each, e = 4 hi + byte.
+    // Group 1's codes go into the high 4 bits of group 0's bytes. The lane of group 0 keeps dims 8 c7 .. + 3, that of group
+    // 1 dims + 4 .. + 7: four bytes each, e = 4 hi + byte.
+    auto put = [&](int i, uint2 code) {
         const uint32_t got = __shfl_xor_sync(kAll, hi ? code.x : code.y, 8);
         const uint32_t own = hi ? got | code.y << 4 : code.x | got << 4;
         uint32_t word;
         int at;
-        if (v == 0) {
+        if (!kV) {
             // word (r, t, ks): bytes dim 2t of lane c7 even, of c7 odd, dim 2t + 1 of even, of odd
             const uint32_t far = __shfl_xor_sync(kAll, c7 & 1 ? own : own >> 16, 1);
             word = c7 & 1 ? __byte_perm(far, own, 0x7160) : __byte_perm(own, far, 0x5140);
-            at = r * 64 + (2 * hi + (c7 & 1)) * 16 + (c7 >> 1) * 4;
+            at = i * 128 + odd * 64 + (2 * hi + (c7 & 1)) * 16 + (c7 >> 1) * 4;
         } else {
             // word (i, e, ks): bytes token 2i of lane c7 even, of odd, token 2i + 1 of even, of odd. Four lanes with four
             // e each transpose their 4 x 4 bytes in two exchanges; lane (odd, c7 & 1) keeps e = 4 hi + 2 odd + (c7 & 1).
@@ -243,6 +240,23 @@ __device__ __forceinline__ void quantise_page(Quant& w, int v, int lane) {
             at = (i >> 2) * 512 + (4 * hi + 2 * odd + (c7 & 1)) * 64 + (i & 3) * 16 + (c7 >> 1) * 4;
         }
         *reinterpret_cast<uint32_t*>(w.half + at) = word;
+    };
+    uint32_t doubts = 0;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        bool doubt;
+        put(i, codes8(w.rows[i][lane], w.groups[2 * (2 * i + odd) + hi], doubt));
+        doubts |= (doubt ? 1u : 0u) << i;
+    }
+    // tokens with a quotient in doubt again, after the others (a branch for each token would cost all of them)
+    for (uint32_t left = __reduce_or_sync(kAll, doubts); left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        const Group g = w.groups[2 * (2 * i + odd) + hi];
+        bool doubt;
+        uint2 code = codes8(w.rows[i][lane], g, doubt);
+        if (doubt) code = codes8_exact(w.rows[i][lane], __low2float(g.par), __high2float(g.par));
+        __syncwarp();
+        put(i, code);
     }
 }
 
@@ -270,16 +284,25 @@ __global__ void __launch_bounds__(kThreads, 4) q4_append_kernel(const PagesParam
             const int lo = (int)max((int64_t)0, -row), hi = (int)min((int64_t)kPageSize, q.n - row);
             const __half* x = static_cast<const __half*>(v ? p.v : p.k) + h * kHeadDim + c * 8;
             const int64_t stride = v ? p.v_stride : p.k_stride;
+            const bool whole = lo == 0 && hi == kPageSize;
+            if (whole) {
+                const __half* at = x + (q.first + row + odd) * stride;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 2 * i + odd;
-                const bool in = r >= lo && r < hi;
-                copy16(&w.rows[i][lane], x + (q.first + (in ? row + r : 0)) * stride, in);
+                for (int i = 0; i < 8; ++i, at += 2 * stride) copy16(&w.rows[i][lane], at, true);
+            } else {
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 2 * i + odd;
+                    const bool in = r >= lo && r < hi;
+                    copy16(&w.rows[i][lane], x + (q.first + (in ? row + r : 0)) * stride, in);
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            quantise_page(w, v, lane);
+            if (v == 0)
+                quantise_page<false>(w, lane);
+            else
+                quantise_page<true>(w, lane);
             __syncwarp();
-            if (lo == 0 && hi == kPageSize) {
+            if (whole) {
                 for (int j = lane; j < kQ4Half / 16; j += 32)
                     reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(blk)[j];
             } else {  // a page that the sequence fills in part: its tokens' bytes, the other slots keep theirs
