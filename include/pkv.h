@@ -405,8 +405,12 @@ int pkv_decode_step_static(const pkv_plan_t* plan, const pkv_problem* problem, c
  *   K codes, slot r:  byte r * 64 + (d / 2 % 4) * 16 + (d / 16) * 4 + 2 * (d % 2) + d / 8 % 2
  *   V codes, slot r:  byte (r / 8) * 512 + (d % 8) * 64 + (r / 2 % 4) * 16 + (d / 16) * 4 + 2 * (r % 2) + d / 8 % 2
  * (the order in which the decode's matrix instructions take them). A (token, KV head) takes 144 bytes, 512 in FP16.
- * num_sms below is the SM count of the current GPU.
+ * num_sms below is the SM count of the current GPU, at most PKV_MAX_SMS.
+ *
+ * A workspace serves one call at a time: calls (and replays of captured ones) that share one are ordered on a stream. It
+ * is zeroed once (pkv_workspace_init), and again after a call that raised PKV_STATUS_TIMEOUT.
  */
+#define PKV_MAX_SMS 4096
 #define PKV_Q4_BLOCK_BYTES 2304
 #define PKV_PROMPT_WS_BYTES 256 /* workspace of the prompt calls and of pkv_q4_read: the header */
 
@@ -428,10 +432,10 @@ int pkv_check_prompt(const pkv_prompt* prompt);
 
 /*
  * Causal grouped-query attention over whole packed prompts: for token i of a sequence and query head hq (KV head
- * hq / G), out = softmax(scale * q_i . k_j over the sequence's tokens j <= i) V. scale must be finite and >= 0.
+ * hq / G), out = softmax(scale * q_i . k_j over the sequence's tokens j <= i) V. 0 <= scale <= 1e12.
  * A value in k or v of a token that a row does not attend to (a later token, another sequence) never reaches that
- * row, infinities and NaN included. ws: PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once (pkv_workspace_init). out
- * must not overlap q, k or v.
+ * row, infinities and NaN included (rows that come out non-finite are computed again key by key, which is slow). ws:
+ * PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once. out must not overlap q, k or v.
  */
 int pkv_prompt_attention(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
                          const int32_t* cu_seqlens, float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out,

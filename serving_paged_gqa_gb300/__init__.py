@@ -7,7 +7,8 @@ causal attention over packed sequences, their K/V into the FP16 pages or quantis
 step over 4-bit pages.
 """
 
-from ._lib import (EXPORTS, LIB_PATH, PKV_MAX_BATCH, PKV_MAX_ROWS_IN_DECODE, PKV_PLAN_INPUTS_AFTER_PREV,  # noqa: F401
+from ._lib import (EXPORTS, LIB_PATH, PKV_MAX_BATCH, PKV_MAX_ROWS_IN_DECODE, PKV_MAX_SMS,  # noqa: F401
+                   PKV_PLAN_INPUTS_AFTER_PREV,
                    PKV_PLAN_OVERLAP_PREV, PKV_PROMPT_WS_BYTES, PKV_Q4_BLOCK_BYTES, Prompt,
                    PKV_SESSION_GRAPHS, PKV_STATIC_SCRATCH_BYTES,
                    PKV_STATUS_BAD_LEN, PKV_STATUS_BAD_PAGE, PKV_STATUS_TASKS, PKV_STATUS_TIMEOUT, PKV_VARIANT_SINGLE,

@@ -52,6 +52,7 @@ PKV_STATIC_SCRATCH_BYTES = 16 << 20
 
 PKV_Q4_BLOCK_BYTES = 2304
 PKV_PROMPT_WS_BYTES = 256
+PKV_MAX_SMS = 4096
 
 
 class Problem(ctypes.Structure):

@@ -19,6 +19,12 @@ int check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return ws_bytes < need ? PKV_E_WS_TOO_SMALL : PKV_OK;
 }
 
+// A GPU's SM count: the workspace's size and the grids are multiples of it.
+bool good_sms(int32_t num_sms) { return num_sms > 0 && num_sms <= PKV_MAX_SMS; }
+
+// Times a score of fp16 rows (at most 128 * 65504^2), or a 4-bit group's scale and 2^24, it stays inside fp32.
+bool good_scale(float scale) { return std::fabs(scale) <= 1e12f; }
+
 bool good_stride(int64_t stride, int64_t heads, int64_t rows) {
     return stride >= heads * kHeadDim && stride % 8 == 0 && stride < (int64_t(1) << 32) &&
            (rows <= 1 || stride <= INT64_MAX / 4 / rows);
@@ -31,7 +37,7 @@ int check_pages(const pkv_problem* pr, const pkv_prompt* pm, const int32_t* cu_s
     int rc = pkv_check_problem(pr);
     if (rc == PKV_OK) rc = pkv_check_prompt(pm);
     if (rc != PKV_OK) return rc;
-    if (pr->batch != pm->num_seqs || pr->num_kv_heads != pm->num_kv_heads || num_sms <= 0) return PKV_E_INVAL;
+    if (pr->batch != pm->num_seqs || pr->num_kv_heads != pm->num_kv_heads || !good_sms(num_sms)) return PKV_E_INVAL;
     rc = check_ws(ws, ws_bytes, PKV_PROMPT_WS_BYTES);
     if (rc != PKV_OK) return rc;
     if (!aligned(cu_seqlens, 4) || !aligned(start, 4) || !aligned(block_table, 4)) return PKV_E_ALIGN;
@@ -64,7 +70,7 @@ int q4_step(const pkv_problem* pr, const void* q, const void* k_new, const void*
     int rc = pkv_q4_workspace_bytes(pr, num_sms, &need);
     if (rc == PKV_OK) rc = check_ws(ws, ws_bytes, need);
     if (rc != PKV_OK) return rc;
-    if (!(std::fabs(scale) <= 1e12f)) return PKV_E_INVAL;  // times a group's scale and 2^24 it stays inside fp32
+    if (!good_scale(scale)) return PKV_E_INVAL;
     if (pr->batch == 0) return PKV_OK;
     if (!q || !pool || !block_table || !seq_lens_dev || !out) return PKV_E_NULLPTR;
     if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
@@ -114,7 +120,7 @@ extern "C" int pkv_prompt_attention(const pkv_prompt* pm, const void* q, const v
     int rc = pkv_check_prompt(pm);
     if (rc == PKV_OK) rc = check_ws(ws, ws_bytes, PKV_PROMPT_WS_BYTES);
     if (rc != PKV_OK) return rc;
-    if (!std::isfinite(scale) || scale < 0.f || num_sms <= 0) return PKV_E_INVAL;
+    if (!good_scale(scale) || scale < 0.f || !good_sms(num_sms)) return PKV_E_INVAL;
     if (nothing(pm)) return PKV_OK;
     if (!q || !k || !v || !cu_seqlens || !out) return PKV_E_NULLPTR;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 4))
@@ -198,7 +204,7 @@ extern "C" int pkv_q4_workspace_bytes(const pkv_problem* pr, int32_t num_sms, si
     if (!pr || !bytes) return PKV_E_NULLPTR;
     int rc = pkv_check_problem(pr);
     if (rc != PKV_OK) return rc;
-    if (num_sms <= 0) return PKV_E_INVAL;
+    if (!good_sms(num_sms)) return PKV_E_INVAL;
     *bytes = q4_workspace_bytes(*pr, num_sms);
     return PKV_OK;
 }

@@ -47,6 +47,7 @@
 #include <algorithm>
 
 #include "pkv_internal.h"
+#include "pkv_launch.h"
 #include "pkv_tcgen05.cuh"
 #include "pkv_wait.cuh"
 
@@ -121,7 +122,9 @@ __device__ __noinline__ void row_attention(const PromptParams& p, int64_t first,
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * b.x[i];
         m = mn;
-        if (isnan(l)) break;  // the row's result is NaN whatever follows
+        // NaN whatever follows: the row's sum, or every output value
+        if (isnan(l)) break;
+        if ((j & 31) == 31 && __all_sync(0xffffffffu, isnan(o[0]) && isnan(o[1]) && isnan(o[2]) && isnan(o[3]))) break;
     }
     const float inv = isnan(l) ? l : 1.f / l;
     uint2 u;
@@ -837,8 +840,7 @@ int launch(const Params& prm, int num_sms, cudaStream_t stream) {
     // at most this many pairs of tiles: every sequence begins one, and the rest are full
     const int64_t pairs = ((int64_t)prm.p.total_tokens * G / (2 * kRows) + std::min(prm.p.num_seqs, prm.p.total_tokens)) * prm.p.Hkv;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(pairs, num_sms));
-    prompt_kernel<G><<<grid, kThreads, kSmem, stream>>>(prm);
-    return cudaGetLastError();
+    return launch_kernel(prompt_kernel<G>, grid, kThreads, kSmem, stream, prm);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "pkv_internal.h"
+#include "pkv_launch.h"
 #include "pkv_tcgen05.cuh"
 #include "q4.cuh"
 
@@ -397,8 +398,7 @@ int64_t page_items(const PagesParams& p) { return ((int64_t)p.total_tokens / kPa
 }  // namespace
 
 int launch_prompt_append(const PagesParams& p, int num_sms, void* stream) {
-    append_kernel<<<grid_for(num_sms, p.total_tokens), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(append_kernel, grid_for(num_sms, p.total_tokens), kThreads, 0, static_cast<cudaStream_t>(stream), p);
 }
 
 int launch_q4_append(const PagesParams& p, int num_sms, void* stream) {
@@ -411,13 +411,11 @@ int launch_q4_append(const PagesParams& p, int num_sms, void* stream) {
         if (e != cudaSuccess) return e;
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    q4_append_kernel<<<grid_for(num_sms, 2 * page_items(p)), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(q4_append_kernel, grid_for(num_sms, 2 * page_items(p)), kThreads, smem, static_cast<cudaStream_t>(stream), p);
 }
 
 int launch_q4_read(const PagesParams& p, int num_sms, void* stream) {
-    q4_read_kernel<<<grid_for(num_sms, page_items(p)), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(q4_read_kernel, grid_for(num_sms, page_items(p)), kThreads, 0, static_cast<cudaStream_t>(stream), p);
 }
 
 }  // namespace pkv

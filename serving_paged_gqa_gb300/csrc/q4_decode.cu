@@ -27,6 +27,7 @@
 #include <algorithm>
 
 #include "pkv_internal.h"
+#include "pkv_launch.h"
 #include "pkv_ptx.cuh"
 #include "pkv_wait.cuh"
 #include "q4.cuh"
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
     constexpr int NC = L::NC, NS = L::NS, NB = L::NB, kSlots = L::kSlots, kNT = (G + 7) / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[L::threads / 32];
-    __shared__ int32_t s_row;   // where the piece begins: row,
+    __shared__ int32_t s_row, s_len;  // where the piece begins: row, its length,
     __shared__ int64_t s_unit;  // unit of the row's Hkv * units
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -137,6 +138,11 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
     volatile int* n_merges = abort_flag + 1;
     const WaitCtx ctx{abort_flag, &p.hdr->status};
 
+    // The line of units: every thread sums a run of rows (the first row's length is on its way while the barriers are set
+    // up), the CTA scans the sums, and the thread whose run holds the piece's first unit finds its row.
+    const int per = (p.B + L::threads - 1) / L::threads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    const int len0 = b0 < b1 ? row_length(p, b0) : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
@@ -157,12 +163,8 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         *n_merges = 0;
         mbar_fence_init();
     }
-    // The line of units: every thread sums a run of rows, the CTA scans the sums, and the thread whose run holds the
-    // piece's first unit finds its row.
-    const int per = (p.B + L::threads - 1) / L::threads;
-    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += row_units(row_length(p, b));
+    int64_t mine = row_units(len0);
+    for (int b = b0 + 1; b < b1; ++b) mine += row_units(row_length(p, b));
     mine *= p.Hkv;
     int64_t incl = mine;
 #pragma unroll
@@ -183,9 +185,11 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
     if (lo < hi && before <= lo && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = (int64_t)row_units(row_length(p, b)) * p.Hkv;
+            const int len = b == b0 ? len0 : row_length(p, b);
+            const int64_t n = (int64_t)row_units(len) * p.Hkv;
             if (lo < at + n) {
                 s_row = b;
+                s_len = len;
                 s_unit = lo - at;
                 break;
             }
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         int b = 0, h = 0, u = 0, len = 0, units = 0;
         if (lo < hi) {
             b = s_row;
-            len = row_length(p, b);
+            len = s_len;
             units = row_units(len);
             h = (int)(s_unit / units);
             u = (int)(s_unit - (int64_t)h * units);
@@ -221,6 +225,10 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 break;
             }
             const int n = (int)min((int64_t)(units - u), hi - pos);
+            const int32_t* bt = p.block_table + (int64_t)b * p.max_pages;
+            const int pages = (len + kPageSize - 1) / kPageSize;
+            const int p0 = u * kUnitPages;  // the segment's first page; lanes hold 32 entries (kChunk units) at a time
+            int ent = p0 + lane < pages ? bt[p0 + lane] : -1;  // on its way while the segment is published
             if (lane == 0) {
                 Segment s;
                 s.b = b;
@@ -238,13 +246,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                          G * kRowBytes, &seg_q[slot]);
             }
             __syncwarp();
-            const int32_t* bt = p.block_table + (int64_t)b * p.max_pages;
-            const int pages = (len + kPageSize - 1) / kPageSize;
-            const int p0 = u * kUnitPages;  // the segment's first page; lanes hold 32 entries (kChunk units) at a time
             // Sixteen units at a time, a lane each: the warp sleeps on the first stage that is still in use, then every
             // lane whose stage is free announces its unit and issues its copies (one unit after the other, a loader
             // needs 600 cycles a unit, which halves the bandwidth).
-            int ent = p0 + lane < pages ? bt[p0 + lane] : -1;
             for (int c0 = 0; c0 < n && ok; c0 += kChunk) {
                 const int cnt = min(kChunk, n - c0);
                 int page[kUnitPages];
@@ -838,8 +842,7 @@ int launch(Q4Params p, int num_sms, cudaStream_t stream) {
     // no more CTAs than the block table can feed
     const int64_t most = ((int64_t)p.B * p.Hkv * ((p.max_pages + kUnitPages - 1) / kUnitPages) + kMinUnits - 1) / kMinUnits;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, most));
-    q4_decode_kernel<G><<<grid, L::threads, L::smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(q4_decode_kernel<G>, grid, L::threads, L::smem, stream, p);
 }
 
 }  // namespace

@@ -104,14 +104,15 @@ def q4_row(q, pool, bt_row, n, scale):
     k, v = values(kc, ks, ko), values(vc, vs, vo)
     out, _ = attend(q[None], k, v, scale, n - 1)
     # Scores: scale * code products and offset * sum(q), each summed in fp32: 2^-24 for each of at most 140 steps of the
-    # sum of magnitudes. Weights times scale are rounded to fp16 relative to the largest scale of the group; the
-    # offsets' part stays in fp32.
+    # sum of magnitudes. Weights times scale are two fp16 parts (2^-21, or half the least subnormal next to a largest of
+    # 1); their products with the codes are added by the matrix instructions, 16 tokens a time, which may cut each sum
+    # to 24 bits: 2^-23 of the running sum a time, at most n / 16 times; the offsets' part stays in fp32.
     parts = values(kc, ks, torch.zeros_like(ko)).abs() + ko.double().abs().repeat_interleave(64, -1)
     ds = 2 * 140 * 2.0 ** -24 * abs(scale) * float((q.double().abs().sum(-1)).max() * parts.max())
     _, coded = attend(q[None], k, values(vc, vs, torch.zeros_like(vo)), scale, n - 1)
     _, offs = attend(q[None], k, vo.double().repeat_interleave(64, -1), scale, n - 1)
-    bound = HALF_STEP * out.abs() + (HALF_STEP + ds + 2.0 ** -15) * coded + (ds + 2.0 ** -15) * offs
-    return out[0], (bound + 15 * n * TINY * float(vs.double().max()) + TINY)[0]
+    bound = HALF_STEP * out.abs() + (2.0 ** -15 + ds + (n // 16 + 1) * 2.0 ** -23) * (coded + offs)
+    return out[0], (bound + 15 * n * TINY * float(vs.double().max()) * 2.0 ** -7 + TINY)[0]
 
 
 def check(got, want, bound, what=""):

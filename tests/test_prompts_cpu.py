@@ -58,7 +58,7 @@ def attention(p=None, q=A, k=A, v=A, cu=A, scale=0.1, sms=152, ws=A, n=256, out=
     (dict(q=None), NULLPTR), (dict(k=None), NULLPTR), (dict(v=None), NULLPTR), (dict(cu=None), NULLPTR), (dict(out=None), NULLPTR),
     (dict(ws=None), NULLPTR), (dict(q=ODD), ALIGN), (dict(k=ODD), ALIGN), (dict(v=ODD), ALIGN), (dict(out=ODD), ALIGN),
     (dict(cu=vp((1 << 20) + 2)), ALIGN), (dict(ws=ODD), ALIGN), (dict(n=255), SMALL), (dict(scale=math.nan), INVAL),
-    (dict(scale=math.inf), INVAL), (dict(scale=-0.1), INVAL), (dict(sms=0), INVAL), (dict(p=prompt(head_dim=64)), UNSUPPORTED),
+    (dict(scale=math.inf), INVAL), (dict(scale=-0.1), INVAL), (dict(scale=2e12), INVAL), (dict(sms=0), INVAL), (dict(sms=4097), INVAL), (dict(p=prompt(head_dim=64)), UNSUPPORTED),
     (dict(p=prompt(num_seqs=0), q=None), OK), (dict(p=prompt(total_tokens=0), q=None), OK),
 ])
 def test_prompt_attention_refuses_before_any_work(change, code):
@@ -79,7 +79,7 @@ def pages(call, pr=None, p=None, k=A, v=A, cu=A, start=None, pool=A, pool2=A, bt
 @pytest.mark.parametrize("change,code", [
     (dict(k=None), NULLPTR), (dict(v=None), NULLPTR), (dict(cu=None), NULLPTR), (dict(pool=None), NULLPTR), (dict(bt=None), NULLPTR),
     (dict(ws=None), NULLPTR), (dict(k=ODD), ALIGN), (dict(v=ODD), ALIGN), (dict(pool=ODD), ALIGN), (dict(ws=ODD), ALIGN),
-    (dict(start=vp((1 << 20) + 1)), ALIGN), (dict(bt=vp((1 << 20) + 1)), ALIGN), (dict(n=0), SMALL), (dict(sms=-1), INVAL),
+    (dict(start=vp((1 << 20) + 1)), ALIGN), (dict(bt=vp((1 << 20) + 1)), ALIGN), (dict(n=0), SMALL), (dict(sms=-1), INVAL), (dict(sms=1 << 30), INVAL),
     (dict(pr=problem(batch=3)), INVAL), (dict(p=prompt(num_kv_heads=4, num_q_heads=16)), INVAL), (dict(pr=problem(page_size=32)), UNSUPPORTED),
     (dict(p=prompt(k_stride=1000)), INVAL), (dict(p=prompt(total_tokens=0), k=None), OK),
     (dict(p=prompt(num_seqs=0), pr=problem(batch=0), k=None), OK),
@@ -101,7 +101,7 @@ def decode(append, pr=None, q=A, kn=A, vn=A, pool=A, bt=A, lens=A, scale=0.1, sm
     (dict(q=None), NULLPTR), (dict(pool=None), NULLPTR), (dict(bt=None), NULLPTR), (dict(lens=None), NULLPTR), (dict(out=None), NULLPTR),
     (dict(ws=None), NULLPTR), (dict(q=ODD), ALIGN), (dict(pool=ODD), ALIGN), (dict(out=ODD), ALIGN), (dict(ws=ODD), ALIGN),
     (dict(bt=vp(3)), ALIGN), (dict(lens=vp(3)), ALIGN), (dict(n=16), SMALL), (dict(scale=math.nan), INVAL), (dict(scale=-math.inf), INVAL),
-    (dict(sms=0), INVAL), (dict(pr=problem(head_dim=64)), UNSUPPORTED), (dict(pr=problem(num_q_heads=48)), UNSUPPORTED),
+    (dict(scale=-2e12), INVAL), (dict(sms=0), INVAL), (dict(sms=4097), INVAL), (dict(pr=problem(head_dim=64)), UNSUPPORTED), (dict(pr=problem(num_q_heads=48)), UNSUPPORTED),
     (dict(pr=problem(batch=0), q=None), OK),
 ])
 def test_q4_decode_refuses_before_any_work(append, change, code):

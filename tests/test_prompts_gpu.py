@@ -172,6 +172,66 @@ def test_prompt_masked_tokens_never_reach_a_row(bad, which):
     assert (got[torch.isinf(want)] == want[torch.isinf(want)]).all()
 
 
+def test_prompt_rows_of_no_sequence_may_hold_anything():
+    """Packed rows behind and between the sequences: infinities and NaN there reach nothing (a tile's keys run past its
+    sequence's end), and a NaN in a whole sequence's V leaves its neighbours as they are."""
+    g = gen(91)
+    lens, gap = [300, 1000, 5], 40
+    at, rows = [], 0
+    for n in lens:
+        at.append((rows, rows + n))
+        rows += n + gap
+    x = normal(g, rows, 12, D)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    keep = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for a, b in at:
+        keep[a:b] = True
+    x[~keep] = math.inf
+    v[at[1][0]:at[1][1]] = math.nan
+    # the gaps are sequences of their own for cu_seqlens, whose rows are not looked at
+    cu = ints([y for pair in at for y in pair] + [rows])
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    for a, b in (at[0], at[2]):
+        w, mag = ref.attend(q[a:b], k[a:b], v[a:b], SCALE, 0)
+        ref.check(out[a:b], w, ref.prompt_bound(w, mag, b - a, q[a:b], k[a:b], v[a:b], SCALE), "beside a sequence of NaN")
+    assert torch.isnan(out[at[1][0]:at[1][1]]).all()
+
+
+@pytest.mark.parametrize("num_sms", [1, 3, 1000])
+def test_grids_of_any_size(num_sms):
+    """The SM count sets the grids alone: results are right for one CTA that does everything and for more than fit."""
+    g = gen(92)
+    q, k, v, cu = packed(g, [333, 20, 129], 8, 2, fused=False)
+    out = torch.full_like(q, math.nan)
+    ws = new_ws()
+    lib, p = pkv.load(), pkv.make_prompt(3, 482, 8, 2, D)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.pkv_prompt_attention(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), SCALE, num_sms, ws.data_ptr(), 256,
+                                    out.data_ptr(), stream) == 0
+    assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
+    lens = [333, 20, 129]
+    bt, pages = table(g, lens)
+    pool = torch.zeros((pages, 2, ref.BLOCK), dtype=torch.uint8, device="cuda")
+    want = pool.clone()
+    for b in range(3):
+        ref.put_tokens(want, bt[b], torch.arange(lens[b], device="cuda"), k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]])
+    pr = pkv.make_problem(3, 8, 2, D, PS, pages, bt.shape[1])
+    assert lib.pkv_q4_prompt_append(pr, p, k.data_ptr(), v.data_ptr(), cu.data_ptr(), None, pool.data_ptr(), bt.data_ptr(), num_sms,
+                                    ws.data_ptr(), 256, stream) == 0
+    assert status(ws) == 0 and torch.equal(pool, want)
+    qd, n = normal(g, 3, 8, D), ints(lens)
+    for call in range(2):
+        out = torch.full_like(qd, math.nan)
+        wd = new_ws(pkv.pkv_q4_workspace_bytes(pr, num_sms))
+        assert lib.pkv_q4_decode_step(pr, qd.data_ptr(), pool.data_ptr(), bt.data_ptr(), n.data_ptr(), SCALE, num_sms, wd.data_ptr(),
+                                      wd.numel(), out.data_ptr(), stream) == 0
+        assert status(wd) == 0
+        check_q4(qd, pool, bt, lens, out)
+
+
 def test_prompt_query_of_nan_reaches_its_own_row_alone():
     q, k, v, cu = packed(gen(10), [90], 8, 2)
     qb = q.clone()
