@@ -13,7 +13,7 @@ import math
 import torch
 
 from ._lib import PKV_PROMPT_WS_BYTES, PKV_Q4_BLOCK_BYTES, Problem, Prompt, check, load
-from .binding import alloc_workspace, make_problem
+from .binding import alloc_workspace
 
 __all__ = [
     "make_prompt", "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append",
@@ -25,6 +25,8 @@ __all__ = [
 # passed as numbers, devices are compared by their index.
 _byref = ctypes.byref
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = torch.cuda.current_device
+_functions: dict[str, object] = {}
 _sms: dict[int, int] = {}
 
 
@@ -55,8 +57,10 @@ def _handle(stream, device: int) -> int:
 
 def _call(device: int, name: str, *args) -> None:
     """Calls the library with `device` current (it launches on the current device)."""
-    fn = getattr(load(), name)
-    if device == torch.cuda.current_device():
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    if device == _current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -143,35 +147,49 @@ def pkv_prompt_attention(prompt: Prompt, q, k, v, cu_seqlens, scale, ws, out, st
     _attention(dev, prompt, q, k, v, cu_seqlens, scale, ws, out, stream)
 
 
+def _append(dev, problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws, stream) -> None:
+    n = prompt.num_seqs
+    _call(dev, "pkv_prompt_append", _byref(problem), _byref(prompt), k.data_ptr(), v.data_ptr(), _seqs(cu_seqlens, n),
+          _start(start, n), _addr(k_pool, torch.float16, "k_pool"), _addr(v_pool, torch.float16, "v_pool"),
+          _table(block_table, problem), _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
+def _q4_append(dev, problem, prompt, k, v, cu_seqlens, start, pool, block_table, ws, stream) -> None:
+    n = prompt.num_seqs
+    _call(dev, "pkv_q4_prompt_append", _byref(problem), _byref(prompt), k.data_ptr(), v.data_ptr(),
+          _seqs(cu_seqlens, n), _start(start, n), _addr(pool, torch.uint8, "pool"), _table(block_table, problem),
+          _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
+def _q4_read(dev, problem, prompt, cu_seqlens, start, pool, block_table, k_out, v_out, ws, stream) -> None:
+    n = prompt.num_seqs
+    _call(dev, "pkv_q4_read", _byref(problem), _byref(prompt), _seqs(cu_seqlens, n), _start(start, n),
+          _addr(pool, torch.uint8, "pool"), _table(block_table, problem), k_out.data_ptr(), v_out.data_ptr(),
+          _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
 def pkv_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws,
                       stream=None) -> None:
-    dev = _device(k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws)
-    _call(dev, "pkv_prompt_append", _byref(problem), _byref(prompt),
-          _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride),
-          _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride), _seqs(cu_seqlens, prompt.num_seqs),
-          _start(start, prompt.num_seqs), _addr(k_pool, torch.float16, "k_pool"),
-          _addr(v_pool, torch.float16, "v_pool"), _table(block_table, problem), _num_sms(dev),
-          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride)
+    _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _append(_device(k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws), problem, prompt, k, v, cu_seqlens, start,
+            k_pool, v_pool, block_table, ws, stream)
 
 
 def pkv_q4_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start, pool, block_table, ws,
                          stream=None) -> None:
-    dev = _device(k, v, cu_seqlens, start, pool, block_table, ws)
-    _call(dev, "pkv_q4_prompt_append", _byref(problem), _byref(prompt),
-          _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride),
-          _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride), _seqs(cu_seqlens, prompt.num_seqs),
-          _start(start, prompt.num_seqs), _addr(pool, torch.uint8, "pool"), _table(block_table, problem),
-          _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride)
+    _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _q4_append(_device(k, v, cu_seqlens, start, pool, block_table, ws), problem, prompt, k, v, cu_seqlens, start, pool,
+               block_table, ws, stream)
 
 
 def pkv_q4_read(problem: Problem, prompt: Prompt, cu_seqlens, start, pool, block_table, k_out, v_out, ws,
                 stream=None) -> None:
-    dev = _device(pool, k_out, v_out, cu_seqlens, start, block_table, ws)
-    _call(dev, "pkv_q4_read", _byref(problem), _byref(prompt), _seqs(cu_seqlens, prompt.num_seqs),
-          _start(start, prompt.num_seqs), _addr(pool, torch.uint8, "pool"), _table(block_table, problem),
-          _fits(k_out, "k_out", prompt, prompt.num_kv_heads, prompt.k_stride),
-          _fits(v_out, "v_out", prompt, prompt.num_kv_heads, prompt.v_stride), _num_sms(dev),
-          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    _fits(k_out, "k_out", prompt, prompt.num_kv_heads, prompt.k_stride)
+    _fits(v_out, "v_out", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _q4_read(_device(pool, k_out, v_out, cu_seqlens, start, block_table, ws), problem, prompt, cu_seqlens, start, pool,
+             block_table, k_out, v_out, ws, stream)
 
 
 def pkv_q4_pool_bytes(problem: Problem) -> int:
@@ -295,10 +313,11 @@ def prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, k_
     if k_pool.dim() != 4 or k_pool.shape[2:] != (hkv, d) or v_pool.shape != k_pool.shape:
         raise ValueError(f"k_pool and v_pool must be [num_pages, page_size, {hkv}, {d}]")
     b, pages = block_table.shape
-    problem = make_problem(b, hkv, hkv, d, k_pool.shape[1], k_pool.shape[0], pages)
+    problem = Problem(b, hkv, hkv, d, k_pool.shape[1], k_pool.shape[0], pages)
     prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
-    pkv_prompt_append(problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table,
-                      _scratch(PKV_PROMPT_WS_BYTES, ws, _device(k), stream), stream)
+    dev = _device(k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws)
+    _append(dev, problem, prompt, k, v, cu_seqlens, start, k_pool, v_pool, block_table,
+            _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
 
 
 def _check_pool(pool: torch.Tensor) -> int:
@@ -311,7 +330,7 @@ def q4_problem(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor) -
     """The problem of a decode step over 4-bit pages: q [B, Hq, d], pool [num_pages, Hkv, block], block_table."""
     hkv = _check_pool(pool)
     b, hq, d = q.shape
-    return make_problem(b, hq, hkv, d, 16, pool.shape[0], block_table.shape[1])
+    return Problem(b, hq, hkv, d, 16, pool.shape[0], block_table.shape[1])
 
 
 def q4_prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
@@ -325,10 +344,11 @@ def q4_prompt_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
     if _check_pool(pool) != hkv:
         raise ValueError(f"pool has {pool.shape[1]} KV heads, k has {hkv}")
     b, pages = block_table.shape
-    problem = make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages)
+    problem = Problem(b, hkv, hkv, d, 16, pool.shape[0], pages)
     prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, ks, vs, hkv * d)
-    pkv_q4_prompt_append(problem, prompt, k, v, cu_seqlens, start, pool, block_table,
-                         _scratch(PKV_PROMPT_WS_BYTES, ws, _device(k), stream), stream)
+    dev = _device(k, v, cu_seqlens, start, pool, block_table, ws)
+    _q4_append(dev, problem, prompt, k, v, cu_seqlens, start, pool, block_table,
+               _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
 
 
 def q4_read(cu_seqlens: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor,
@@ -340,18 +360,18 @@ def q4_read(cu_seqlens: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     b, pages = block_table.shape
     if (k_out is None) != (v_out is None):
         raise ValueError("give both of k_out and v_out, or neither")
+    dev = _device(pool, k_out, v_out, cu_seqlens, start, block_table, ws)
     if k_out is None:
         if total_tokens is None:
             raise ValueError("give k_out and v_out, or total_tokens")
-        dev = _device(pool)
         k_out, v_out = (_new((int(total_tokens), hkv, d), dev, stream) for _ in range(2))
     t = k_out.shape[0]
     if total_tokens is not None and total_tokens != t:
         raise ValueError(f"k_out has {t} rows, total_tokens is {total_tokens}")
     prompt = Prompt(cu_seqlens.numel() - 1, t, hkv, hkv, d, 0, hkv * d, _rows(k_out, "k_out", hkv, t, d),
                     _rows(v_out, "v_out", hkv, t, d), hkv * d)
-    pkv_q4_read(make_problem(b, hkv, hkv, d, 16, pool.shape[0], pages), prompt, cu_seqlens, start, pool, block_table,
-                k_out, v_out, _scratch(PKV_PROMPT_WS_BYTES, ws, _device(pool), stream), stream)
+    _q4_read(dev, Problem(b, hkv, hkv, d, 16, pool.shape[0], pages), prompt, cu_seqlens, start, pool, block_table,
+             k_out, v_out, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
     return k_out, v_out
 
 
