@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             float o[kNT][8][4];  // O^T: tile dt < 4 dims 16 dt + g8, + 8 of group 0; 4 + dt the same of group 1
             // Weights are 2^(x - ref) with ref chosen per head so that weight * V's scale stays below 2^14 and its
             // largest values above 1; ref is raised only when a unit would go beyond, then by what brings it to 2^7.
-            float osum[kNT][2][2], ref[kNT][2], l[kNT][2];
+            float osum[kNT][2][2], taken[kNT][2][2], ref[kNT][2], l[kNT][2], l_taken[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     ref[nt][i] = -INFINITY;
-                    l[nt][i] = osum[nt][0][i] = osum[nt][1][i] = 0.f;
+                    l[nt][i] = osum[nt][0][i] = osum[nt][1][i] = taken[nt][0][i] = taken[nt][1][i] = l_taken[nt][i] = 0.f;
                 }
             }
             // Unit j of the piece lives in stage j % NS and goes to warp j % NC; NS is a multiple of NC, so a stage
@@ -605,6 +605,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                                 l[nt][i2] *= f;
                                 osum[nt][0][i2] *= f;
                                 osum[nt][1][i2] *= f;
+                                l_taken[nt][i2] *= f;
+                                taken[nt][0][i2] *= f;
+                                taken[nt][1][i2] *= f;
 #pragma unroll
                                 for (int d = 0; d < 8; ++d) {
                                     o[nt][d][i2] *= f;
@@ -658,6 +661,33 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             }
                         }
                     }
+                // The matrix instructions cut their sums to fp32 towards zero, which over a long row of codes of one sign adds
+                // up (48 rows, 54 units a warp: 5.2e-4 of the output, its own rounding is 2.1e-4). So every unit
+                // takes the codes' common offset out of the accumulators in advance, and the end puts it back: about 8
+                // times the weights * scale, which this lane estimates from its own tokens (any amount would be right).
+                {
+                    const uint2 pv = *reinterpret_cast<const uint2*>(stage + kQ4Half + kQ4Codes + tok0 * 8);
+                    const bool mine = !kFold || t4 < 2;  // the columns of the weights' second part need none
+                    constexpr float k = 8.f * 16.f / kTok * 5.9604644775390625e-8f;  // of 16 tokens it has kTok
+                    const float k0 = mine ? half2_of(pv.x).x * k : 0.f, k1 = mine ? half2_of(pv.y).x * (16.f * k) : 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                        for (int i2 = 0; i2 < 2; ++i2) {
+                            const float dl = l[nt][i2] - l_taken[nt][i2];  // of this unit
+                            const float t0 = dl * k0, t1 = dl * k1;
+                            l_taken[nt][i2] = l[nt][i2];
+                            taken[nt][0][i2] += t0;
+                            taken[nt][1][i2] += t1;
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) {
+                                o[nt][d][i2] -= t0;
+                                o[nt][d][2 + i2] -= t0;
+                                o[nt][4 + d][i2] -= t1;
+                                o[nt][4 + d][2 + i2] -= t1;
+                            }
+                        }
+                }
 #pragma unroll
                 for (int pg = 0; pg < kUnitPages; ++pg) {
                     const uint8_t* blk = stage + pg * kQ4Block + kQ4Half;
@@ -692,6 +722,11 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int i2 = 0; i2 < 2; ++i2) {
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        o[nt][d][i2] += taken[nt][d >> 2][i2];
+                        o[nt][d][2 + i2] += taken[nt][d >> 2][i2];
+                    }
                     if (kFold)
 #pragma unroll
                         for (int d = 0; d < 8; ++d) {
