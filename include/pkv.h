@@ -46,7 +46,8 @@
 extern "C" {
 #endif
 
-/* 3: serving session (pkv_session_*) and PKV_PLAN_INPUTS_AFTER_PREV; the structs are unchanged from 2. */
+/* 3: serving session (pkv_session_*) and PKV_PLAN_INPUTS_AFTER_PREV; the structs are unchanged from 2. The prompt and
+ * 4-bit-cache calls came later; they change nothing that was there. */
 #define PKV_VERSION 3
 
 #define PKV_OK 0
