@@ -435,7 +435,8 @@ int pkv_check_prompt(const pkv_prompt* prompt);
  * Causal grouped-query attention over whole packed prompts: for token i of a sequence and query head hq (KV head
  * hq / G), out = softmax(scale * q_i . k_j over the sequence's tokens j <= i) V. 0 <= scale <= 1e12.
  * A value in k or v of a token that a row does not attend to (a later token, another sequence) never reaches that
- * row, infinities and NaN included (rows that come out non-finite are computed again key by key, which is slow). ws:
+ * row, infinities and NaN included (the rows just before a token whose v is not finite are computed again key by key,
+ * which is slow). An attended infinity of v makes its dim infinite, of both signs NaN, whatever the weights. ws:
  * PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once. out must not overlap q, k or v.
  */
 int pkv_prompt_attention(const pkv_prompt* prompt, const void* q, const void* k, const void* v,

@@ -22,6 +22,8 @@
 //                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
 //   warp 17         one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
 //   warp 18         claims work, one pair ahead, and publishes it.
+//   warp 19         clears the rows behind a sequence's end in its last tile of V, before the tile counts as loaded (in
+//                   the other warps it costs 2-4 %).
 // TMEM (512 columns): S_A, S_B (P over columns 0-31 and 64-95 of each), O_A, O_B. Instructions of one thread run in
 // order, so S(j+1) may be issued over P(j) right after PV(j).
 //
@@ -35,8 +37,12 @@
 // other has raised at the next step.
 //
 // A value that a row does not attend to is multiplied by a weight of 0, which does not remove an infinity or a NaN of
-// V. Output rows that are not finite are therefore computed again by a warp that reads the row's own keys alone
-// (row_attention): exact in every case, and costs nothing where the data are finite.
+// V. Rows behind the sequence's end are therefore cleared in V's last tile (they may hold anything, and most tiles that
+// end a sequence have some). What is left are infinities and NaN among the tile's own tokens, and scores beyond 2^27, of
+// which the fp32 reference is off by more than the weights' range: an output row that is not finite, or whose weights
+// add up to less than any reference allows, is finished by its warp (finish_rows): dimensions in which V's attended
+// values are not finite get what those add up to, and if others are left, the row is computed again from its own
+// keys alone (row_attention). A row whose weights' sum is NaN has a NaN score that it attends to: it stays NaN.
 //
 // Bound: the tensor core and the paths of its operands. Measured on a GB300 (32 query heads, 8 KV heads): 16384 tokens
 // 1.55 ms, 1420 TFLOP/s (0.74 of the measured cuBLAS burst), the tensor pipe active 62 % of the time at 4096 tokens; the
@@ -80,7 +86,7 @@ constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
 constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
 constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
 constexpr int off_bars = off_hist + 32 * 4;
-constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 1;
+constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 2 + 1;
 constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
 constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
 constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
@@ -99,44 +105,112 @@ struct Row4 {
     float x[4];
 };
 
-__device__ __forceinline__ Row4 load4(const __half* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ uint2 load4(const __half* p) { return *reinterpret_cast<const uint2*>(p); }
+
+__device__ __forceinline__ Row4 floats4(const uint2& u) {
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
     return Row4{{a.x, a.y, b.x, b.y}};
 }
 
-// One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, lane l holds dims 4l..4l+3. Stores
-// dims 64 half .. + 63.
-__device__ __noinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int half, int lane) {
+// One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, 4 at a time; lane l holds dims
+// 4l..4l+3. Stores dims 64 half .. + 63. (With 8 at a time the kernel's ordinary steps spill registers.)
+__device__ __forceinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int half, int lane) {
+    constexpr int kKeys = 4;
     const int h = hq / (p.Hq / p.Hkv);
     const __half* k = static_cast<const __half*>(p.k) + first * p.k_stride + h * kHeadDim + lane * 4;
     const __half* v = static_cast<const __half*>(p.v) + first * p.v_stride + h * kHeadDim + lane * 4;
-    const Row4 q = load4(static_cast<const __half*>(p.q) + (first + pos) * p.q_stride + hq * kHeadDim + lane * 4);
+    const Row4 q = floats4(load4(static_cast<const __half*>(p.q) + (first + pos) * p.q_stride + hq * kHeadDim + lane * 4));
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j <= pos; ++j) {
-        const Row4 a = load4(k + j * p.k_stride);
-        float s = q.x[0] * a.x[0] + q.x[1] * a.x[1] + q.x[2] * a.x[2] + q.x[3] * a.x[3];
+    for (int j = 0; j <= pos; j += kKeys) {
+        uint2 a[kKeys], b[kKeys];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - ref), e = exp2f(s - ref);
-        const Row4 b = load4(v + j * p.v_stride);
-        l = l * f + e;
+        for (int i = 0; i < kKeys; ++i) {
+            a[i] = load4(k + min(j + i, pos) * p.k_stride);
+            b[i] = load4(v + min(j + i, pos) * p.v_stride);
+        }
+        float s[kKeys];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * b.x[i];
+        for (int i = 0; i < kKeys; ++i) {
+            const Row4 x = floats4(a[i]);
+            s[i] = q.x[0] * x.x[0] + q.x[1] * x.x[1] + q.x[2] * x.x[2] + q.x[3] * x.x[3];
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            s[i] = j + i <= pos ? s[i] * p.scale_log2 : -INFINITY;
+            mn = fmaxf(mn, s[i]);
+        }
+        const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref);
+        l *= f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] *= f;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+            if (j + i <= pos) {
+                const float e = exp2f(s[i] - ref);
+                const Row4 x = floats4(b[i]);
+                l += e;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[y] += e * x.x[y];
+            }
         m = mn;
-        // NaN whatever follows: the row's sum, or every output value
-        if (isnan(l)) break;
-        if ((j & 31) == 31 && __all_sync(0xffffffffu, isnan(o[0]) && isnan(o[1]) && isnan(o[2]) && isnan(o[3]))) break;
     }
-    const float inv = isnan(l) ? l : 1.f / l;
+    const float inv = 1.f / l;
     uint2 u;
     u.x = pack_half2(o[0] * inv, o[1] * inv);
     u.y = pack_half2(o[2] * inv, o[3] * inv);
     if (lane >> 4 == half)
         *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (first + pos) * p.out_stride + hq * kHeadDim + lane * 4) = u;
+}
+
+// One warp; rows: a bit for each of its 32 rows (row r is head h * G + r % G of token t0 + r / G of the sequence that
+// begins at row `first`) whose tensor-core result, dims 64 half .. + 63 of it in out, is not finite, redo: those among them
+// that are wrong for certain. Lane l looks at dims 2l, 2l + 1. Infinities of V that the row attends to add up to an
+// infinity, of both signs (or with a NaN) to a NaN, whatever their weights; a row that has other dims that are not
+// finite is computed again.
+template <int G>
+__device__ __noinline__ void finish_rows(const PromptParams& p, int first, int t0, int h, int half, uint32_t rows, uint32_t redo) {
+    const int lane = threadIdx.x & 31;
+    const __half* v = static_cast<const __half*>(p.v) + (int64_t)first * p.v_stride + h * kHeadDim + half * 64 + lane * 2;
+    __half2 top = __float2half2_rn(0.f), low = top, nan = top;  // of the values of the keys before `keys`
+    int64_t keys = 0;
+    for (; rows; rows &= rows - 1) {  // in the order of their tokens
+        const int r = __ffs(rows) - 1, pos = t0 + r / G;
+        if ((redo >> r) & 1) continue;
+#pragma unroll 16
+        for (; keys <= pos; ++keys) {
+            const __half2 x = *reinterpret_cast<const __half2*>(v + keys * p.v_stride);
+            top = __hmax2(top, x);
+            low = __hmin2(low, x);
+            nan = __hmax2_nan(nan, x);
+        }
+        const uint32_t t = *reinterpret_cast<const uint32_t*>(&top), w = *reinterpret_cast<const uint32_t*>(&low),
+                       n = *reinterpret_cast<const uint32_t*>(&nan);
+        uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<__half*>(p.out) + (int64_t)(first + pos) * p.out_stride +
+                                                   (h * G + r % G) * kHeadDim + half * 64 + lane * 2);
+        uint32_t y = *at;
+        bool other = false;
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+            const bool up = ((t >> i) & 0xffffu) == 0x7c00u, down = ((w >> i) & 0xffffu) == 0xfc00u;
+            const bool any = ((n >> i) & 0x7fffu) > 0x7c00u;
+            if (any || up || down)
+                y = (y & ~(0xffffu << i)) | (any || (up && down) ? 0x7fffu : up ? 0x7c00u : 0xfc00u) << i;
+            else
+                other = other || ((y >> i) & 0x7c00u) == 0x7c00u;
+        }
+        *at = y;
+        if (__any_sync(0xffffffffu, other)) redo |= 1u << r;
+    }
+    for (; redo; redo &= redo - 1) {
+        const int r = __ffs(redo) - 1;
+        row_attention(p, first, t0 + r / G, h * G + r % G, half, lane);
+    }
 }
 
 // ---- the tensor-core kernel ---------------------------------------------------------------------------------------
@@ -177,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint64_t* o_free = lo_done + 2;       // the accumulator has been read
     uint64_t* first_ref = o_free + 2;     // [tile][warp of the half]: the tile's first references are in shared memory
     uint64_t* half_done = first_ref + 8;  // [tile][warp of the half]: the second half has settled its weights of the step
-    uint64_t* drain = half_done + 8;
+    uint64_t* tail_full = half_done + 8;  // [2]: a tile of V with rows behind the sequence's end has come
+    uint64_t* drain = tail_full + 2;
     Work* work = reinterpret_cast<Work*>(smem + off_work);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
@@ -190,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kSoftmax / 32 + 2);  // and the MMA warp, the loader
+            mbar_init(&w_empty[i], kSoftmax / 32 + 3);  // and warps 16, 17, 19
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -201,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&o_full[i], 1);
             mbar_init(&lo_done[i], 1);
             mbar_init(&o_free[i], 8);
+            mbar_init(&tail_full[i], 1);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&first_ref[i], 1);
@@ -373,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             uint64_t keep, stream;
             asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
             asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream));
-            int seq = 0, nq[2] = {0, 0};
+            int seq = 0, nq[2] = {0, 0}, nc = 0;
             bool stop = false;
             for (int k = 0; !stop; ++k) {
                 const int slot = k % kSlots;
@@ -398,26 +474,58 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     ++nq[x];
                     return true;
                 };
-                auto load_kv = [&](const CUtensorMap* map, int j) {
+                auto load_kv = [&](const CUtensorMap* map, int j, bool tail = false) {  // tail: comes by way of warp 19
                     const int st = seq % kStages;
+                    uint64_t* bar = tail ? &tail_full[nc & 1] : &kv_full[st];
                     if (!warp_wait(&kv_empty[st], ((seq / kStages) & 1) ^ 1, ctx)) return false;
                     if (lane == 0) {
                         uint8_t* dst = smem + off_ring + st * kTileBytes;
-                        mbar_arrive_expect_tx(&kv_full[st], kTileBytes);
+                        mbar_arrive_expect_tx(bar, kTileBytes);
                         for (int b = 0; b < 2; ++b)
-                            tma_load_3d(dst + b * kBoxBytes, map, b * 64, w.h, w.first + j * kRows, &kv_full[st], keep);
+                            tma_load_3d(dst + b * kBoxBytes, map, b * 64, w.h, w.first + j * kRows, bar, keep);
                     }
                     __syncwarp();
                     ++seq;
+                    nc += tail;
                     return true;
                 };
-                stop = !load_q(0) || !load_kv(&prm.k, 0) || !load_q(1) || !load_kv(&prm.v, 0);
-                for (int j = 1; j < steps && !stop; ++j) stop = !load_kv(&prm.k, j) || !load_kv(&prm.v, j);
+                auto load_v = [&](int j) { return load_kv(&prm.v, j, j == steps - 1 && (end & 15)); };
+                stop = !load_q(0) || !load_kv(&prm.k, 0) || !load_q(1) || !load_v(0);
+                for (int j = 1; j < steps && !stop; ++j) stop = !load_kv(&prm.k, j) || !load_v(j);
             }
             // every copy that this warp issued lands before the CTA may end
+            for (int j = max(0, nc - 2); j < nc; ++j) warp_drain(&tail_full[j & 1], (j >> 1) & 1);
             for (int j = max(0, seq - kStages); j < seq; ++j) warp_drain(&kv_full[j % kStages], (j / kStages) & 1);
             for (int x = 0; x < 2; ++x)
                 if (nq[x] > 0) warp_drain(&q_full[x], (nq[x] - 1) & 1);
+        } else if (warp == 19) {
+            // --------------------------------------------------------------------- rows behind the sequence's end
+            // The products' last step of 16 keys reads them (a pair of tiles ends at a multiple of 16 tokens elsewhere).
+            int kv = 0, nc = 0;
+            for (int k = 0;; ++k) {
+                const int slot = k % kSlots;
+                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
+                const Work w = work[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                if (w.h < 0) break;
+                const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
+                const int steps = (end + kRows - 1) / kRows;
+                kv += 2 * steps;
+                if ((end & 15) == 0) continue;
+                const int pos = kv - 1;
+                // (Two barriers: the loader may be one such tile ahead, but not two, as it gets a work when every warp has
+                // taken the one before.)
+                if (!warp_wait(&tail_full[nc & 1], (nc >> 1) & 1, ctx)) break;
+                ++nc;
+                uint8_t* v = smem + off_ring + (pos % kStages) * kTileBytes;
+                const int first = end - (steps - 1) * kRows, last = (first + 15) & ~15;
+                for (int i = first * 16 + lane; i < last * 16; i += 32)
+                    *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[pos % kStages]);
+            }
         } else if (warp == 16) {
             // ------------------------------------------------------------------------- matrix instructions
             // (The votes of the waits keep the warp together; a __syncwarp after every elected block costs 6 %.)
@@ -616,7 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 };
                 // Scales what has been accumulated up to now (this thread's sum; the row's accumulator).
                 auto scale_sum = [&](float to) {
-                    if (to != ref) l *= ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                    if (to != ref) {
+                        const float f = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                        l = l == INFINITY && f == 0.f ? 0.f : l * f;  // NaN only where a score is
+                    }
                 };
                 auto scale_acc = [&](float f) {
                     const uint64_t ff = pack_f32x2(f, f);
@@ -735,11 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             float total = lo.y;
             if (end > 64) {
                 const float top = fmaxf(lo.x, hi.x);
-                total = lo.y * (lo.x == top ? 1.f : fast_exp2(lo.x - top)) + hi.y * (hi.x == top ? 1.f : fast_exp2(hi.x - top));
+                auto part = [&](const float2& x) {
+                    const float f = x.x == top ? 1.f : fast_exp2(x.x - top);
+                    return x.y == INFINITY && f == 0.f ? 0.f : x.y * f;
+                };
+                total = part(lo) + part(hi);
             }
             const bool mine = token < w.n;
             const float inv = 1.f / total;
-            float probe = 0.f;  // stays 0 while every value is finite
+            __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
+            const __half2 zero = probe;
             // Four lanes exchange 16-byte pieces of their rows, so that they store 64 consecutive bytes of one row at a time
             // (16 bytes of 32 rows an instruction took 1.7 us a tile).
             const int q4 = lane & 3;
@@ -766,8 +882,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
-                    probe = fmaf(a, 0.f, fmaf(b, 0.f, probe));
-                    y[i >> 2][i & 3] = pack_half2(a, b);
+                    const uint32_t u = pack_half2(a, b);
+                    probe = __hfma2(*reinterpret_cast<const __half2*>(&u), zero, probe);
+                    y[i >> 2][i & 3] = u;
                 }
 #pragma unroll
                 for (int s = 1; s < 4; s <<= 1)
@@ -784,12 +901,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
             }
             ++no;
-            unsigned again = __ballot_sync(0xffffffffu, mine && probe != 0.f);
-            while (again) {  // rows that are not finite: from their own keys alone
-                const int r = (row & ~31) + __ffs(again) - 1;
-                again &= again - 1;
-                __syncwarp();
-                row_attention(p, w.first, w.t0 + x * kTokens + r / G, w.h * G + r % G, h, lane);
+            // The largest weight is 1 next to the row's reference, or above 1/2 where it was raised.
+            const bool low_sum = !(total >= 0.25f);
+            const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
+            const unsigned again = __ballot_sync(0xffffffffu, mine && odd && !isnan(total));
+            if (again) {
+                const unsigned redo = __ballot_sync(0xffffffffu, low_sum) & again;
+                __syncwarp();  // the rows were stored by other lanes
+                finish_rows<G>(p, w.first, w.t0 + x * kTokens + (row & ~31) / G, w.h, h, again, redo);
             }
         }
     }

@@ -83,17 +83,4 @@ __device__ __forceinline__ void q4_quantise_row(const __half* x, uint8_t* half_b
     if ((lane & 15) == 0) reinterpret_cast<__half2*>(half_block + kQ4Codes)[2 * r + grp] = par;
 }
 
-// Dims 4 * lane .. + 3 of token r of a block half, as the values that the codes stand for.
-__device__ __forceinline__ void q4_dequantise4(const uint8_t* half_block, int r, bool is_v, int lane, float (&f)[4]) {
-    const int grp = lane >> 4;
-    const __half2 par = reinterpret_cast<const __half2*>(half_block + kQ4Codes)[2 * r + grp];
-    const float sc = __low2float(par), off = __high2float(par);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (4 * lane + i) & 63;
-        const uint32_t b = half_block[is_v ? q4_v_byte(r, d) : q4_k_byte(r, d)];
-        f[i] = __fadd_rn(__fmul_rn((float)((b >> (4 * grp)) & 15u), sc), off);
-    }
-}
-
 }  // namespace pkv

@@ -147,6 +147,76 @@ def test_prompt_scores_that_grow_along_the_keys(step, shape):
     check_prompt(q, k, v, cu, out)
 
 
+def one_hot_levels(g, order, sign, n):
+    """Levels between 16384 and 2^15 in steps of 64 (exact in fp16), and for each row the key of the greatest up to it."""
+    at = torch.randperm(n, generator=g, device="cuda") if order == "random" else torch.arange(n, device="cuda")
+    level = sign * (16384 + 64 * (at if order != "down" else n - 1 - at)).double()
+    return level, torch.tensor([int(level[:i + 1].argmax()) for i in range(n)], device="cuda")
+
+
+@pytest.mark.parametrize("size", [512.0, 4096.0, 32768.0])
+@pytest.mark.parametrize("order,sign", [("up", 1), ("down", 1), ("random", 1), ("random", -1)])
+def test_prompt_scores_of_which_fp32_has_no_fractions(size, order, sign):
+    """Scores from 2^24 to 2^30 (in log2), exact in fp32 and thousands apart: all weights but the greatest key's are 0,
+    and the output is its V (one rounding of the weight, one of the output)."""
+    n, g = 250, gen(93)
+    q, k, v, cu = packed(g, [n], 8, 2, fused=False)
+    level, best = one_hot_levels(g, order, sign, n)
+    q.zero_()
+    q[:, :, 3:19] = size
+    k.zero_()
+    k[:, :, 3:19] = level.half()[:, None, None]
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    want = v[best].repeat_interleave(4, 1).double()
+    ref.check(out, want, (2 * ref.HALF_STEP + 2.0 ** -16) * want.abs() + ref.TINY)
+
+
+def test_prompt_values_of_the_largest_magnitude():
+    """All V at fp16's largest value, and weights that fp16 rounds up by most of half a step (2^-0.99922 = 0.50027 next to
+    the first key's 1): the mean is that value, which a rounding of the numerator alone carries to infinity."""
+    n, g = 200, gen(94)
+    q, k, v, cu = packed(g, [n], 8, 2, fused=False)
+    q.zero_()
+    k.zero_()
+    q[:, :, 0] = 1.0
+    k[0, :, 0] = 7.8359375
+    v.fill_(65504.0)
+    v[:, :, 64:] = -65504.0
+    for scale in (SCALE, 2 * SCALE, -0.0):
+        ws = new_ws()
+        out = pkv.prompt_attention(q, k, v, cu, scale=scale, ws=ws)
+        assert status(ws) == 0
+        # the row's rounding to fp16 steps of 32, and a step for the weights' rounding
+        assert ((out.double() - v.double().repeat_interleave(4, 1)).abs() <= 65504 * 2.0 ** -10).all()
+
+
+def test_prompt_infinities_of_values_add_up():
+    """V's infinities reach every later row of their dim, however small their weights in fp16 are, and meet as a NaN; the
+    rows' other dims and the rows before are as they are without them."""
+    n, g = 400, gen(95)
+    q, k, v, cu = packed(g, [n], 8, 2)
+    k[300:] += 3.0 * (q[300:, :1] > 0)  # sharper towards the end
+    vb = v.clone()
+    vb[5, 0, 10], vb[130, 0, 10] = math.inf, -math.inf
+    vb[131, 1, 70], vb[390, 1, 70] = -math.inf, -math.inf
+    vb[256, 0, 127] = math.nan
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, vb, cu, ws=ws)
+    assert status(ws) == 0
+    w, mag = ref.attend(q, k, v, SCALE, 0)
+    bound = ref.prompt_bound(w, mag, n, q, k, v, SCALE)
+    want = w.clone()
+    want[5:130, :4, 10], want[130:, :4, 10] = math.inf, math.nan
+    want[131:, 4:, 70] = -math.inf
+    want[256:, :4, 127] = math.nan
+    fin = torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert (out.double()[torch.isinf(want)] == want[torch.isinf(want)]).all()
+    ref.check(torch.where(fin, out.double(), 0.0), torch.where(fin, want, 0.0), bound)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("which", ["k", "v", "kv"])
 def test_prompt_masked_tokens_never_reach_a_row(bad, which):
