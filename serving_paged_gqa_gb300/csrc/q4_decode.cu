@@ -13,8 +13,8 @@
 //
 // Bound: HBM; a (token, KV head) is 144 bytes against 512 in fp16. A unit is 4 pages (64 tokens) of one (row, KV head),
 // four bulk copies of 2304 bytes into one ring stage, and goes to one consumer warp. Measured on a GB300 (G = 4): 48 rows
-// of 900-32768 tokens, 765 MB, 138 us without the read-back of the appended tokens: 5.5 TB/s, 0.83 of the copy
-// bandwidth; copies alone 125 us, arithmetic alone 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.4 us.
+// of 900-32768 tokens, 765 MB, 143 us: 5.4 TB/s, 0.80 of the copy bandwidth;
+// copies alone 125 us, arithmetic alone 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.4 us.
 // Division: the units of all (row, KV head) pairs form one line, and each CTA takes an equal piece of it, whatever the
 // rows' lengths; every CTA finds its piece itself from a scan of seq_lens, so there is no plan. A pair that lies in one
 // piece is written out at once. The others leave a state (m, l, accumulator) per piece, and the last of a pair's
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
         const int tok0 = kFold ? g8 + ((t4 >> 1) << 3) : g8;
         const int col = kFold ? 2 * (t4 & 1) : 2 * t4;  // this lane's heads: 8 nt + col, + 1
         constexpr int kFirstLane = kFold ? 2 : 4;       // lanes that differ in bits from here on share their heads
-        // scores are kept in units of 2^-24 / (|scale| * log2(e)): X = sum_g scale_g (q.code_g) 2^-24 + ..., x = X * xk
+        // of a score: sum_g scale_g (q.code_g) 2^-24 + offset_g (sum of q over g) 2^-24
         const float xk = fabsf(p.scale_log2) * 16777216.f;
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs
         int seq = 0, new_seen = 0;  // units, new tokens of the segments before
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             if (!warp_wait(&seg_q[slot], (k / kSlots) & 1, ctx)) break;
             // Q^T as the B operand: b0 = Q[head][16 ks + 2 t4, + 1], b1 = + 8, + 9; head = 8 nt + g8
             uint32_t qb[kNT][8][2];
-            float qs[kNT][2][2];  // [nt][group][head]: sum of q over the group, times 2^-24
+            float qs[kNT][2][2];  // [nt][group][head]: sum of q over the group, times xk 2^-24
             const uint8_t* qrow = smem + L::off_q + slot * G * kRowBytes;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {  // from the lanes of that head
-                    qs[nt][0][i] = __shfl_sync(0xffffffffu, s0, (col + i) * 4) * 5.9604644775390625e-8f;
-                    qs[nt][1][i] = __shfl_sync(0xffffffffu, s1, (col + i) * 4) * 5.9604644775390625e-8f;
+                    qs[nt][0][i] = __shfl_sync(0xffffffffu, s0, (col + i) * 4) * (xk * 5.9604644775390625e-8f);
+                    qs[nt][1][i] = __shfl_sync(0xffffffffu, s1, (col + i) * 4) * (xk * 5.9604644775390625e-8f);
                 }
             }
             __syncwarp();
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             float o[kNT][8][4];  // O^T: tile dt < 4 dims 16 dt + g8, + 8 of group 0; 4 + dt the same of group 1
             // Weights are 2^(x - ref) with ref chosen per head so that weight * V's scale stays below 2^14 and its
             // largest values above 1; ref is raised only when a unit would go beyond, then by what brings it to 2^7.
-            float osum[kNT][2][2], taken[kNT][2][2], ref[kNT][2], l[kNT][2], l_taken[kNT][2];
+            float osum[kNT][2][2], taken[kNT][2][2], ref[kNT][2], l[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     ref[nt][i] = -INFINITY;
-                    l[nt][i] = osum[nt][0][i] = osum[nt][1][i] = taken[nt][0][i] = taken[nt][1][i] = l_taken[nt][i] = 0.f;
+                    l[nt][i] = osum[nt][0][i] = osum[nt][1][i] = taken[nt][0][i] = taken[nt][1][i] = 0.f;
                 }
             }
             // Unit j of the piece lives in stage j % NS and goes to warp j % NC; NS is a multiple of NC, so a stage
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             const uint32_t sv = __byte_perm(pv.x, pv.y, 0x5410);
                             top = __hmax2(top, *reinterpret_cast<const __half2*>(&sv));
                             const float2 a0 = half2_of(pk.x), a1 = half2_of(pk.y);
-                            const float a1s = a1.x * 0.0625f;  // group 1's codes lie 4 bits higher
+                            const float a0s = a0.x * xk, a1s = a1.x * (0.0625f * xk);  // group 1's codes lie 4 bits higher
 #pragma unroll
                             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                                         d0 = c0[y][nt][2 + i2];
                                         d1 = c1[y][nt][2 + i2];
                                     }
-                                    x[nt][pg][u2][i2] = fmaf(d0, a0.x, fmaf(d1, a1s, fmaf(a0.y, qs[nt][0][i2], a1.y * qs[nt][1][i2])));
+                                    x[nt][pg][u2][i2] = fmaf(d0, a0s, fmaf(d1, a1s, fmaf(a0.y, qs[nt][0][i2], a1.y * qs[nt][1][i2])));
                                 }
                         }
                     }
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                             for (int u2 = 0; u2 < kTok; ++u2) v = fmaxf(v, x[nt][pg][u2][i2]);
                         mx[nt][i2] = v;
-                        raise = raise || fmaf(v, xk, need) > ref[nt][i2] + 7.f;
+                        raise = raise || (v - ref[nt][i2]) + need > 7.f;
                     }
                 if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -605,14 +605,15 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             float v = mx[nt][i2];
 #pragma unroll
                             for (int s = kFirstLane; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-                            v = fmaf(v, xk, need);
-                            if (v > ref[nt][i2] + 7.f) {
+                            if ((v - ref[nt][i2]) + need > 7.f) {
+                                // a score of which an fp32 has no fractions is the reference itself: the weights' exponents
+                                // (x - ref) are then exact, and the largest weight is 1
+                                if (fabsf(v) < 16777216.f) v += need;
                                 const float f = fast_exp2(ref[nt][i2] - v);
                                 ref[nt][i2] = v;
                                 l[nt][i2] *= f;
                                 osum[nt][0][i2] *= f;
                                 osum[nt][1][i2] *= f;
-                                l_taken[nt][i2] *= f;
                                 taken[nt][0][i2] *= f;
                                 taken[nt][1][i2] *= f;
 #pragma unroll
@@ -633,6 +634,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 // times the output's own rounding. Folded, the two parts share the columns (0-3, 4-7) and take no
                 // more products than one.
                 uint32_t pb[kUnitPages][kNT][2][kFold ? 1 : 2][2];  // [page][nt][group][part][tokens 0-7, 8-15]
+                float ws[kNT][2][2];  // weights * scale of this lane's tokens of the first page: [nt][group][head]
 #pragma unroll
                 for (int pg = 0; pg < kUnitPages; ++pg)
 #pragma unroll
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                             float w[2];
 #pragma unroll
                             for (int i2 = 0; i2 < 2; ++i2) {
-                                w[i2] = fast_exp2(fmaf(x[nt][pg][u2][i2], xk, nref[nt][i2]));
+                                w[i2] = fast_exp2(x[nt][pg][u2][i2] + nref[nt][i2]);
                                 l[nt][i2] += w[i2];
                                 osum[nt][0][i2] = fmaf(w[i2], par[0].y, osum[nt][0][i2]);
                                 osum[nt][1][i2] = fmaf(w[i2], par[1].y, osum[nt][1][i2]);
@@ -652,6 +654,10 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
                                 const float v0 = w[0] * par[g].x, v1 = w[1] * par[g].x;
+                                if (pg == 0) {
+                                    ws[nt][g][0] = u2 ? ws[nt][g][0] + v0 : v0;
+                                    ws[nt][g][1] = u2 ? ws[nt][g][1] + v1 : v1;
+                                }
                                 const uint32_t hi = pack_half2(v0, v1);
                                 const float2 hf = half2_of(hi);
                                 const uint32_t th = transpose8x8(hi), tl = transpose8x8(pack_half2(v0 - hf.x, v1 - hf.y));
@@ -670,20 +676,16 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                     }
                 // The matrix instructions cut their sums to fp32 towards zero, which over a long row of codes of one sign adds
                 // up (48 rows, 54 units a warp: 5.2e-4 of the output, its own rounding is 2.1e-4). So every unit
-                // takes the codes' common offset out of the accumulators in advance, and the end puts it back: about 8
-                // times the weights * scale, which this lane estimates from its own tokens (any amount would be right).
+                // takes the codes' common offset out of the accumulators in advance, and the end puts it back: 8 times the
+                // weights * scale, which this lane estimates from its own tokens of the first page (any amount would be
+                // right; from its tokens of all pages: 1 % slower, and the same error).
                 {
-                    const uint2 pv = *reinterpret_cast<const uint2*>(stage + kQ4Half + kQ4Codes + tok0 * 8);
-                    const bool mine = !kFold || t4 < 2;  // the columns of the weights' second part need none
-                    constexpr float k = 8.f * 16.f / kTok * 5.9604644775390625e-8f;  // of 16 tokens it has kTok
-                    const float k0 = mine ? half2_of(pv.x).x * k : 0.f, k1 = mine ? half2_of(pv.y).x * (16.f * k) : 0.f;
+                    const float k0 = !kFold || t4 < 2 ? 8.f * kUnitTokens / kTok * 5.9604644775390625e-8f : 0.f;  // not the second part
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                         for (int i2 = 0; i2 < 2; ++i2) {
-                            const float dl = l[nt][i2] - l_taken[nt][i2];  // of this unit
-                            const float t0 = dl * k0, t1 = dl * k1;
-                            l_taken[nt][i2] = l[nt][i2];
+                            const float t0 = ws[nt][0][i2] * k0, t1 = ws[nt][1][i2] * (16.f * k0);
                             taken[nt][0][i2] += t0;
                             taken[nt][1][i2] += t1;
 #pragma unroll

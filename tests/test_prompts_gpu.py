@@ -557,6 +557,60 @@ def test_q4_decode_value_scales_that_grow_along_the_row():
     check_q4(q, pool, bt, [n, n], out)
 
 
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 1)])
+@pytest.mark.parametrize("vscale", [1.0, 1e-3, 3e3])
+@pytest.mark.parametrize("size", [64.0, 512.0, 8192.0])
+@pytest.mark.parametrize("order,sign", [("up", 1), ("down", 1), ("random", -1)])
+def test_q4_decode_scores_of_which_fp32_has_no_fractions(order, sign, size, vscale, hq, hkv):
+    """Scores from 2^24 to 2^31 (in log2), thousands apart: the output is the value that the greatest key's V stands
+    for, up to the fp32 sum of its parts and its own rounding."""
+    n, g = 250, gen(96)
+    lens = [n, 77, 1]
+    bt, pool = q4_cache(g, lens, hkv)
+    best = []
+    for b, m in enumerate(lens):
+        level, at = one_hot_levels(g, order, sign, m)
+        k = level.half()[:, None, None].expand(m, hkv, D)  # groups of equal values: exact
+        v = (torch.randn((m, hkv, D), generator=g, device="cuda") * vscale).half()
+        ref.put_tokens(pool, bt[b], torch.arange(m, device="cuda"), k, v)
+        best.append(int(at[-1]))
+    q = torch.full((3, hq, D), size, dtype=torch.float16, device="cuda")
+    ws = q4_ws(q, pool, bt)
+    out = pkv.q4_decode(q, pool, bt, ints(lens), ws=ws)
+    assert status(ws) == 0
+    for b in range(3):
+        _, (c, sc, off) = ref.get_tokens(pool, bt[b], torch.tensor([best[b]], device="cuda"))
+        coded = ref.values(c, sc, torch.zeros_like(off))
+        want = ref.values(c, sc, off)
+        parts = coded.abs() + off.double().abs().repeat_interleave(64, -1)
+        # two fp16 parts of the scale (2^-21), the codes' common offset of up to 128 steps in and out (2^-24 each)
+        bound = ref.HALF_STEP * want.abs() + 2.0 ** -15 * parts + 128 * 2.0 ** -22 * sc.double().repeat_interleave(64, -1) + ref.TINY
+        bound = bound + 15 * ref.TINY * 2.0 ** -7
+        ref.check(out[b], want[0].repeat_interleave(hq // hkv, 0), bound[0].repeat_interleave(hq // hkv, 0), f"row {b}")
+
+
+def test_q4_decode_small_values_beside_large_ones():
+    """The weights lie on tokens whose V is 2^14 times smaller than that of their neighbours, which have none."""
+    g = gen(97)
+    n = 700
+    bt, pool = q4_cache(g, [n], 2)
+    q = normal(g, 1, 8, D)
+    q[:, :, 0] = 8.0
+    small = torch.rand(n, generator=g, device="cuda") < 0.3
+    small[::16] = False  # a page's first token is a large one
+    k = normal(g, n, 2, D)
+    k[:, :, 0] = torch.where(small, 60.0, -60.0).half()[:, None]
+    v = (torch.randn((n, 2, D), generator=g, device="cuda") * torch.where(small, 2.0 ** -4, 2.0 ** 10)[:, None, None]).half()
+    ref.put_tokens(pool, bt[0], torch.arange(n, device="cuda"), k, v)
+    out = pkv.q4_decode(q, pool, bt, ints([n]))
+    w, bound = ref.q4_row(q[0], pool, bt[0], n, SCALE)
+    # Without the term for weights * scale below fp16's least steps: the largest is 2^7 for the large tokens' scale, thus
+    # at least 2^-8 for the small ones', of which the second part's half step, 2^-25, is 2^-17.
+    scales = ref.get_tokens(pool, bt[0], torch.arange(n, device="cuda"))[1][1].double()
+    bound = bound - 15 * n * ref.TINY * float(scales.max()) * 2.0 ** -7
+    ref.check(out[0], w, bound)
+
+
 @pytest.mark.parametrize("hq,hkv", [(32, 8), (16, 1), (3, 3)])
 def test_q4_decode_appends_the_new_token(hq, hkv):
     g = gen(52)
