@@ -21,7 +21,7 @@
 //                   from TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
 //                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
 //   warp 17         one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
-//   warp 18         claims work, one pair ahead, and publishes it.
+//   warp 18         claims work, two steps before the end of the current pair, and publishes it.
 //   warp 19         clears the rows behind a sequence's end in its last tile of V, before the tile counts as loaded (in
 //                   the other warps it costs 2-4 %).
 // TMEM (512 columns): S_A, S_B (P over columns 0-31 and 64-95 of each), O_A, O_B. Instructions of one thread run in
@@ -68,7 +68,6 @@ constexpr int kRows = 128;                   // rows of a tile, keys of a step
 constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two boxes of 64 dims
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kStages = 4;                   // K and V tiles in flight; loads are not what the tensor core waits for
-constexpr int kSlots = 1;  // a CTA claims its next pair when its softmax begins the current one
 constexpr int kSoftmax = 512;                // threads of the softmax
 constexpr int kThreads = kSoftmax + 128;
 // 512 * 104 + 128 * 64 = 640 * 96, what the launch has; equal shares of 96 are 1-3 % slower
@@ -84,9 +83,9 @@ constexpr int off_ring = 2 * kTileBytes;
 constexpr int off_prefix = off_ring + kStages * kTileBytes;  // work pairs before the i-th sequence of the order
 constexpr int off_order = off_prefix + (PKV_MAX_BATCH + 1) * 4 + 12;
 constexpr int off_work = off_order + PKV_MAX_BATCH * 2;
-constexpr int off_hist = off_work + kSlots * (int)sizeof(Work);
+constexpr int off_hist = off_work + (int)sizeof(Work);
 constexpr int off_bars = off_hist + 32 * 4;
-constexpr int kBars = 2 * kStages + 2 * kSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 2 + 1;
+constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 2 + 1;
 constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
 constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
 constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
@@ -240,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + off_bars);
     uint64_t* kv_empty = kv_full + kStages;
-    uint64_t* w_full = kv_empty + kStages;
-    uint64_t* w_empty = w_full + kSlots;
-    uint64_t* q_full = w_empty + kSlots;  // [2], like those below: tile A, tile B
+    uint64_t* w_full = kv_empty + kStages;  // the CTA's next work has been published
+    uint64_t* w_empty = w_full + 1;         // every warp has taken it, and its copies have been issued
+    uint64_t* q_full = w_empty + 1;       // [2], like those below: tile A, tile B
     uint64_t* q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
     uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
@@ -263,10 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kSoftmax / 32 + 3);  // and warps 16, 17, 19
-        }
+        mbar_init(w_full, 1);
+        mbar_init(w_empty, kSoftmax / 32 + 3);  // and warps 16, 17, 19
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -294,12 +291,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
     if (warp >= kSoftmax / 32) {
         regs_shrink<kOtherRegs>();
-        auto publish = [&](const Work& w, int k) {  // the CTA's k-th work; false: it was the last
-            const int slot = k % kSlots;
-            if (!warp_wait(&w_empty[slot], ((k / kSlots) & 1) ^ 1, ctx)) return false;
+        auto claim = [&](int k, int64_t& at) {  // the index of the CTA's k-th work, once the warps have taken the one before
+            at = blockIdx.x;
+            if (k == 0) return true;
+            if (!warp_wait(w_empty, (k - 1) & 1, ctx)) return false;
+            uint32_t c = 0;
+            if (lane == 0) c = atomicAdd(&p.hdr->queue_head, 1u);
+            at = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, c, 0);
+            return true;
+        };
+        auto publish = [&](const Work& w) {  // false: it was the last
             if (lane == 0) {
-                work[slot] = w;
-                mbar_arrive(&w_full[slot]);
+                *work = w;
+                mbar_arrive(w_full);
             }
             __syncwarp();
             return w.h >= 0;
@@ -331,12 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             const int64_t total = (int64_t)all * p.Hkv;
             for (int k = 0;; ++k) {
-                int64_t at = blockIdx.x;
-                if (k > 0) {
-                    uint32_t c = 0;
-                    if (lane == 0) c = atomicAdd(&p.hdr->queue_head, 1u);
-                    at = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, c, 0);
-                }
+                int64_t at;
+                if (!claim(k, at)) break;
                 Work w{0, 0, 0, -1};
                 if (at < total) {
                     const int pair = (int)(at / p.Hkv);
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     w.t0 = __shfl_sync(0xffffffffu, (t - 1 - (pair - before)) * 2 * kTokens, src);
                     w.h = (int)(at - (int64_t)pair * p.Hkv);
                 }
-                if (!publish(w, k)) break;
+                if (!publish(w)) break;
             }
             rearm();
         } else if (warp == 18) {
@@ -414,12 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             __syncwarp();
             const int64_t total = (int64_t)run * p.Hkv;
             for (int k = 0;; ++k) {
-                int64_t t = blockIdx.x;  // the first pair of a CTA is its index, later ones come from the counter
-                if (k > 0) {
-                    uint32_t c = 0;
-                    if (lane == 0) c = atomicAdd(&p.hdr->queue_head, 1u);
-                    t = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, c, 0);
-                }
+                int64_t t;
+                if (!claim(k, t)) break;
                 Work w{0, 0, 0, -1};
                 if (t < total) {
                     const int pair = (int)(t / p.Hkv);
@@ -436,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     w.t0 = (tiles_of(w.n, 2 * kTokens) - 1 - (pair - prefix[lo])) * 2 * kTokens;
                     w.h = (int)(t - (int64_t)pair * p.Hkv);
                 }
-                if (!publish(w, k)) break;
+                if (!publish(w)) break;
             }
             rearm();
         } else if (warp == 17) {
@@ -452,11 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             int seq = 0, nq[2] = {0, 0}, nc = 0;
             bool stop = false;
             for (int k = 0; !stop; ++k) {
-                const int slot = k % kSlots;
-                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
-                const Work w = work[slot];
+                if (!warp_wait(w_full, k & 1, ctx)) break;
+                const Work w = *work;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[slot]);
                 if (w.h < 0) break;
                 const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
                 const int steps = (end + kRows - 1) / kRows;
@@ -492,6 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 auto load_v = [&](int j) { return load_kv(&prm.v, j, j == steps - 1 && (end & 15)); };
                 stop = !load_q(0) || !load_kv(&prm.k, 0) || !load_q(1) || !load_v(0);
                 for (int j = 1; j < steps && !stop; ++j) stop = !load_kv(&prm.k, j) || !load_v(j);
+                // The next claim, about two steps before this pair's end. (Claimed when this one begins, a pair may go to a
+                // CTA that is not done for long: 4096 tokens of 4 KV heads took 77 us, the longest pair takes 60.)
+                if (lane == 0) mbar_arrive(w_empty);
             }
             // every copy that this warp issued lands before the CTA may end
             for (int j = max(0, nc - 2); j < nc; ++j) warp_drain(&tail_full[j & 1], (j >> 1) & 1);
@@ -503,11 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             // The products' last step of 16 keys reads them (a pair of tiles ends at a multiple of 16 tokens elsewhere).
             int kv = 0, nc = 0;
             for (int k = 0;; ++k) {
-                const int slot = k % kSlots;
-                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
-                const Work w = work[slot];
+                if (!warp_wait(w_full, k & 1, ctx)) break;
+                const Work w = *work;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                if (lane == 0) mbar_arrive(w_empty);
                 if (w.h < 0) break;
                 const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
                 const int steps = (end + kRows - 1) / kRows;
@@ -534,11 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                const int slot = k % kSlots;
-                if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
-                const Work w = work[slot];
+                if (!warp_wait(w_full, k & 1, ctx)) break;
+                const Work w = *work;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                if (lane == 0) mbar_arrive(w_empty);
                 if (w.h < 0) break;
                 const int end0 = tile_end(w, 0, kTokens), end1 = tile_end(w, 1, kTokens);
                 const int steps = (max(end0, end1) + kRows - 1) / kRows;
@@ -644,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         int step2 = 0;       // steps with keys in the second half, as the first half counts them
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            const int slot = k % kSlots;
-            if (!warp_wait(&w_full[slot], (k / kSlots) & 1, ctx)) break;
-            const Work w = work[slot];
+            if (!warp_wait(w_full, k & 1, ctx)) break;
+            const Work w = *work;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&w_empty[slot]);
+            if (lane == 0) mbar_arrive(w_empty);
             if (w.h < 0) break;
             const int end = tile_end(w, x, kTokens);
             if (end == 0) continue;
