@@ -797,17 +797,28 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
             fetch(0);
         }
         for (int g = warp; g < G; g += NC + 2) {
+            auto state = [&](int c) { return __ldcg(p.ml + (first + 2 * c + (c == 0)) * G + g); };
             float M = -INFINITY, l = 0.f;
-            for (int c = lane; c < s.ctas; c += 32) M = fmaxf(M, __ldcg(p.ml + (first + 2 * c + (c == 0)) * G + g).x);
+            float2 kept[2];  // of the first 64 pieces
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = lane + 32 * i;
+                kept[i] = c < s.ctas ? state(c) : make_float2(-INFINITY, 0.f);
+            }
+            M = fmaxf(kept[0].x, kept[1].x);
+            for (int c = lane + 64; c < s.ctas; c += 32) M = fmaxf(M, state(c).x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             const float ref = M == -INFINITY ? 0.f : M;
-            for (int c = lane; c < s.ctas; c += 32) {
-                const float2 ml = __ldcg(p.ml + (first + 2 * c + (c == 0)) * G + g);
+            auto put = [&](int c, float2 ml) {
                 const float f = fast_exp2(ml.x - ref);
                 factor[c * G + g] = f;
                 l += f * ml.y;
-            }
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (lane + 32 * i < s.ctas) put(lane + 32 * i, kept[i]);
+            for (int c = lane + 64; c < s.ctas; c += 32) put(c, state(c));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (lane == 0) sums[g] = l;
