@@ -45,8 +45,8 @@
 // keys alone (row_attention). A row whose weights' sum is NaN has a NaN score that it attends to: it stays NaN.
 //
 // Bound: the tensor core and the paths of its operands. Measured on a GB300 (32 query heads, 8 KV heads): 16384 tokens
-// 1.55 ms, 1420 TFLOP/s (0.74 of the measured cuBLAS burst), the tensor pipe active 62 % of the time at 4096 tokens; the
-// issuing warp's stream without the softmax 1910 TFLOP/s; 2048 tokens 44 us; one prompt of 17 tokens 6.4 us.
+// 1.54 ms, 1430 TFLOP/s (0.74 of the measured cuBLAS burst), the tensor pipe active 62 % of the time at 4096 tokens; the
+// issuing warp's stream without the softmax 1910 TFLOP/s; 2048 tokens 35 us; one prompt of 17 tokens 6.6 us.
 //
 // Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
 // have in flight, and the CTA frees its TMEM and returns.
