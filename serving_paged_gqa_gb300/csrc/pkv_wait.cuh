@@ -40,6 +40,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     }
 }
 
+// The same for one thread of a warp.
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (it % kPollEvery == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (*ctx.abort_flag != 0 || now - t0 > kWaitLimitNs) {
+                if (*ctx.abort_flag == 0) {
+                    *ctx.abort_flag = 1;
+                    raise_status(ctx.status, PKV_STATUS_TIMEOUT);
+                }
+                return false;
+            }
+        }
+    }
+}
+
 // Bounded wait that ignores the abort flag (used to drain a warp's own copies before it returns).
 __device__ __forceinline__ void warp_drain(uint64_t* bar, uint32_t parity) {
     uint64_t t0 = 0;

@@ -524,57 +524,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
         } else if (warp == 16) {
             // ------------------------------------------------------------------------- matrix instructions
-            // (The votes of the waits keep the warp together; a __syncwarp after every elected block costs 6 %.)
-            int kv = 0;                        // ring position of the next K tile of the current work
-            int nq[2] = {0, 0}, no[2] = {0, 0};  // tiles begun; accumulators begun
-            int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
-            bool ok = true;
-            for (int k = 0; ok; ++k) {
-                if (!warp_wait(w_full, k & 1, ctx)) break;
-                const Work w = *work;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(w_empty);
-                if (w.h < 0) break;
-                const int end0 = tile_end(w, 0, kTokens), end1 = tile_end(w, 1, kTokens);
-                const int steps = (max(end0, end1) + kRows - 1) / kRows;
-                // ring positions: K_j at kv + 2j, V_j one behind it
-                const uint32_t ring = smem_addr(smem + off_ring);
-                auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
-                auto wait_stage = [&](int pos) { return warp_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
-                // keys of step j that tile x needs (0: none)
-                auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
-                auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
-                    const int n = (keys(x, j) + 15) & ~15;
-                    if (n == 0) return;
-                    const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
-                    const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
-                    const uint32_t idesc = mma_idesc(n, false);
-                    const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
-                    if (elect_one()) {
+            // One thread does everything: the step's six waits are then 40 cycles each where there is nothing to wait for, and
+            // 100 as votes of a warp, during which the tensor core runs dry (16384 tokens: 1440 TFLOP/s, now 1600).
+            if (elect_one()) {
+                int kv = 0;                        // ring position of the next K tile of the current work
+                int nq[2] = {0, 0}, no[2] = {0, 0};  // tiles begun; accumulators begun
+                int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    if (!thread_wait(w_full, k & 1, ctx)) break;
+                    const Work w = *work;
+                    mbar_arrive(w_empty);
+                    if (w.h < 0) break;
+                    const int end0 = tile_end(w, 0, kTokens), end1 = tile_end(w, 1, kTokens);
+                    const int steps = (max(end0, end1) + kRows - 1) / kRows;
+                    // ring positions: K_j at kv + 2j, V_j one behind it
+                    const uint32_t ring = smem_addr(smem + off_ring);
+                    auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
+                    auto wait_stage = [&](int pos) { return thread_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
+                    // keys of step j that tile x needs (0: none)
+                    auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
+                    auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
+                        const int n = (keys(x, j) + 15) & ~15;
+                        if (n == 0) return;
+                        const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
+                        const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
+                        const uint32_t idesc = mma_idesc(n, false);
+                        const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
                         mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, idesc);
                         mma_commit(&s_full[x]);
                         if (last) mma_commit(&q_empty[x]);
-                    }
-                };
-                auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
-                    const int n = (keys(x, j) + 15) >> 4;
-                    if (n == 0) return true;
-                    constexpr uint32_t idesc = mma_idesc(kHeadDim, true);
-                    const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
-                    const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
-                    const bool last = keys(x, j + 1) == 0;
-                    if (j == 0) {  // the previous tile's rows have been read
-                        if (!warp_wait(&o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
-                        ++no[x];
-                    }
+                    };
+                    auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
+                        const int n = (keys(x, j) + 15) >> 4;
+                        if (n == 0) return true;
+                        constexpr uint32_t idesc = mma_idesc(kHeadDim, true);
+                        const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
+                        const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
+                        const bool last = keys(x, j + 1) == 0;
+                        if (j == 0) {  // the previous tile's rows have been read
+                            if (!thread_wait(&o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
+                            ++no[x];
+                        }
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {  // 64 keys each
-                        const int c = min(4, n - 4 * half);  // steps of 16 keys
-                        if (c <= 0) break;
-                        if (!warp_wait(&p_full[2 * x + half], np[x][half] & 1, ctx)) return false;
-                        ++np[x][half];
-                        tc_fence_after();
-                        if (elect_one()) {
+                        for (int half = 0; half < 2; ++half) {  // 64 keys each
+                            const int c = min(4, n - 4 * half);  // steps of 16 keys
+                            if (c <= 0) break;
+                            if (!thread_wait(&p_full[2 * x + half], np[x][half] & 1, ctx)) return false;
+                            ++np[x][half];
+                            tc_fence_after();
                             if (c == 4)
                                 mma_ts_64(o, pw + 64 * half, v + 512 * half, idesc, j > 0 || half > 0);
                             else
@@ -583,41 +581,39 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                             if (half == 0) mma_commit(&lo_done[x]);
                             if (last && n - 4 * half <= 4) mma_commit(&o_full[x]);
                         }
+                        return true;
+                    };
+                    auto release = [&](int pos) { mma_commit(&kv_empty[pos % kStages]); };
+                    ok = wait_stage(kv);
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (keys(x, 0) == 0) continue;
+                        ok = thread_wait(&q_full[x], nq[x] & 1, ctx);
+                        ++nq[x];
+                        tc_fence_after();
+                        if (ok) scores(x, 0);
                     }
-                    return true;
-                };
-                auto release = [&](int pos) {
-                    if (elect_one()) mma_commit(&kv_empty[pos % kStages]);
-                };
-                ok = wait_stage(kv);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (keys(x, 0) == 0) continue;
-                    ok = warp_wait(&q_full[x], nq[x] & 1, ctx);
-                    ++nq[x];
-                    tc_fence_after();
-                    if (ok) scores(x, 0);
-                }
-                if (!ok) break;
-                release(kv);
-                for (int j = 0; j < steps && ok; ++j) {
-                    ok = wait_stage(kv + 2 * j + 1) && values(0, j);
-                    if (ok && j + 1 < steps) {
-                        ok = wait_stage(kv + 2 * j + 2);
-                        if (ok) scores(0, j + 1);
-                    }
-                    ok = ok && values(1, j);
                     if (!ok) break;
-                    release(kv + 2 * j + 1);
-                    if (j + 1 < steps) {
-                        scores(1, j + 1);
-                        release(kv + 2 * j + 2);
+                    release(kv);
+                    for (int j = 0; j < steps && ok; ++j) {
+                        ok = wait_stage(kv + 2 * j + 1) && values(0, j);
+                        if (ok && j + 1 < steps) {
+                            ok = wait_stage(kv + 2 * j + 2);
+                            if (ok) scores(0, j + 1);
+                        }
+                        ok = ok && values(1, j);
+                        if (!ok) break;
+                        release(kv + 2 * j + 1);
+                        if (j + 1 < steps) {
+                            scores(1, j + 1);
+                            release(kv + 2 * j + 2);
+                        }
                     }
+                    kv += 2 * steps;
                 }
-                kv += 2 * steps;
+                mma_commit(drain);
             }
-            // every matrix instruction has completed before the TMEM is freed and the CTA ends
-            if (elect_one()) mma_commit(drain);
             __syncwarp();
+            // every matrix instruction has completed before the TMEM is freed and the CTA ends
             warp_drain(drain, 0);
         }
     } else {
