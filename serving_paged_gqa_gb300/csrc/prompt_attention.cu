@@ -14,12 +14,12 @@
 // first. Warp roles:
 //   warps 0-15      softmax: warps 0-3 and 4-7 the first and second 64 keys of every step of tile A, 8-15 those of tile
 //                   B; thread = row. The scores come from TMEM into registers (tcgen05.ld), the weights go back as fp16
-//                   over them. (With one thread for all 128 keys of a row the softmax of a step took 2000 cycles, and
-//                   the tensor core, which has 1024 cycles of the other tile's work meanwhile, waited.) Finally they
+//                   over them. (With one thread for all 128 keys of a row the softmax of a step takes 2000 cycles, and
+//                   the tensor core, which has 1024 cycles of the other tile's work meanwhile, waits.) Finally they
 //                   divide, round and store the output rows, 64 dims each.
-//   warp 16         one (elected) lane issues the matrix instructions: S = Q K^T (both from shared memory), O += P V (P
-//                   from TMEM). While tile A's softmax runs, the tensor core works on B's products, and the other way
-//                   round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
+//   warp 16         one (elected) thread waits for and issues the matrix instructions: S = Q K^T (both from shared memory),
+//                   O += P V (P from TMEM). While tile A's softmax runs, the tensor core works on B's products, and the
+//                   other way round: order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
 //   warp 17         one lane issues the TMA copies: q tiles, and K, V tiles of 128 tokens through a ring of 4 stages.
 //   warp 18         claims work, two steps before the end of the current pair, and publishes it.
 //   warp 19         clears the rows behind a sequence's end in its last tile of V, before the tile counts as loaded (in
@@ -45,8 +45,8 @@
 // keys alone (row_attention). A row whose weights' sum is NaN has a NaN score that it attends to: it stays NaN.
 //
 // Bound: the tensor core and the paths of its operands. Measured on a GB300 (32 query heads, 8 KV heads): 16384 tokens
-// 1.54 ms, 1430 TFLOP/s (0.74 of the measured cuBLAS burst), the tensor pipe active 62 % of the time at 4096 tokens; the
-// issuing warp's stream without the softmax 1910 TFLOP/s; 2048 tokens 35 us; one prompt of 17 tokens 6.6 us.
+// 1.37 ms, 1600 TFLOP/s (0.83 of the measured cuBLAS burst, 0.93 of its sustained rate under the power cap); 2048 tokens
+// 30.5 us; one prompt of 17 tokens 6.3 us. The tensor pipe is active 68 % of the time at 4096 tokens.
 //
 // Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
 // have in flight, and the CTA frees its TMEM and returns.
