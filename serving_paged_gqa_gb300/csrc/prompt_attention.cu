@@ -778,11 +778,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         tmem_ld32(s_at + 64, t);
                         tmem_wait_ld();
                         tmem_use32(t);
-                        const __half2 hf = __float2half2_rn(f2);  // a power of two: exact
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&t[i]), hf);
-                            t[i] = *reinterpret_cast<const uint32_t*>(&v);
+                        for (int i = 0; i < 32; ++i) {  // in fp32: weights of 2^15 times a power of two that fp16 may not have
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
+                            t[i] = pack_half2(v.x * f2, v.y * f2);
                         }
                         tmem_st32(s_at + 64, t);
                     }

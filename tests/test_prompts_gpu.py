@@ -147,6 +147,25 @@ def test_prompt_scores_that_grow_along_the_keys(step, shape):
     check_prompt(q, k, v, cu, out)
 
 
+@pytest.mark.parametrize("rise", [15.5, 20.0, 23.9, 25.0, 26.5, 29.0])
+@pytest.mark.parametrize("first,second", [(130, 200), (200, 130), (150, 255), (70, 10)])
+def test_prompt_a_step_whose_halves_rise_differently(rise, first, second):
+    """Key `first` raises the running reference by `rise` (in log2), while key `second` of the same step's other half stays
+    just below the 2^15 that lets its weight as it is; its V is large enough to be seen."""
+    n, g = 300, gen(98)
+    q, k, v, cu = packed(g, [n], 8, 1, fused=False)
+    unit = 1.0 / (8.0 * SCALE * math.log2(math.e))  # of k's dim 0, for a score of 1 in log2
+    q.zero_()
+    k.zero_()
+    q[:, :, 0] = 8.0
+    k[first, :, 0], k[second, :, 0] = rise * unit, 14.9 * unit
+    v[second] *= 2.0 ** max(0.0, rise - 14.9)
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
+
+
 def one_hot_levels(g, order, sign, n):
     """Levels between 16384 and 2^15 in steps of 64 (exact in fp16), and for each row the key of the greatest up to it."""
     at = torch.randperm(n, generator=g, device="cuda") if order == "random" else torch.arange(n, device="cuda")
