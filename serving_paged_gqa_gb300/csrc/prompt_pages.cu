@@ -159,13 +159,14 @@ struct __align__(16) Group {
 __device__ __forceinline__ Group group_of(__half2 extremes) {  // (min, -max)
     const float mn = __low2float(extremes), mx = -__high2float(extremes);
     Group g;
-    g.par = q4_params(mn, mx, isfinite(mn) && isfinite(mx));
+    const bool finite = isfinite(mn) && isfinite(mx);
+    g.par = q4_params(mn, mx, finite);
     const float scale = __low2float(g.par);
     const bool some = scale > 0.f;  // neither equal values (codes 0) nor a group that stands for NaN
     g.inv = some ? __frcp_rn(scale) : 0.f;
     const float off = some ? mn * g.inv : 0.f;
     g.add = 192.5f + 0x1p-15f - off;
-    g.exact = some && (fabsf(off) > 60.f || scale < 6.2e-5f);
+    g.exact = some ? fabsf(off) > 60.f || scale < 6.2e-5f : !finite;  // (codes 0 for a group that stands for NaN)
     return g;
 }
 

@@ -460,6 +460,31 @@ def test_q4_quantises_every_kind_of_group(make):
         assert torch.equal(pool, want)
 
 
+def test_q4_writers_agree_on_every_byte():
+    """A token has one 4-bit form, whether the prompt append or a decode step writes it: also with infinities and NaN, whose
+    groups have codes 0."""
+    g = gen(99)
+    x = normal(g, 6, 2, 3, D)  # [token, K or V, head, d]
+    x[1, 0, 0, 5], x[1, 1, 2, 127] = math.nan, math.inf
+    x[2, :, :, :64] = -math.inf
+    x[3, 0, 1] = 0.0
+    x[4, 0, 1, ::2], x[4, 0, 1, 1::2] = 0.0, -0.0
+    x[5] *= 1e-6
+    bt = torch.arange(6, dtype=torch.int32, device="cuda").view(6, 1)
+    one = torch.zeros((6, 3, ref.BLOCK), dtype=torch.uint8, device="cuda")
+    two = one.clone()
+    ws = new_ws()
+    pkv.q4_prompt_append(x[:, 0].contiguous(), x[:, 1].contiguous(), cu_of([1] * 6), one, bt, ws=ws)
+    q = normal(g, 6, 12, D)
+    wd = q4_ws(q, two, bt)
+    pkv.q4_decode(q, two, bt, ints([1] * 6), x[:, 0].contiguous(), x[:, 1].contiguous(), ws=wd)
+    assert status(ws) == 0 and status(wd) == 0
+    assert torch.equal(one, two)
+    (kc, ks, _), (vc, vs, _) = ref.get_tokens(one, bt[1], torch.tensor([0], device="cuda"))
+    assert torch.isnan(ks[0, 0, 0]) and (kc[0, 0, :64] == 0).all()
+    assert torch.isnan(vs[0, 2, 1]) and (vc[0, 2, 64:] == 0).all()
+
+
 def test_appends_report_bad_pages_and_lengths():
     g = gen(32)
     _, k, v, cu = packed(g, [40, 20], 2, 2)
