@@ -437,7 +437,7 @@ int pkv_check_prompt(const pkv_prompt* prompt);
  * A value in k or v of a token that a row does not attend to (a later token, another sequence) never reaches that
  * row, infinities and NaN included (the rows just before a token whose v is not finite are computed again key by key,
  * which is slow). An attended infinity of v makes its dim infinite, of both signs NaN, whatever the weights. ws:
- * PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once. out must not overlap q, k or v.
+ * PKV_PROMPT_WS_BYTES, 256-byte aligned, zeroed once. out must not overlap q, k or v (the same address is refused).
  */
 int pkv_prompt_attention(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
                          const int32_t* cu_seqlens, float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out,
@@ -480,8 +480,8 @@ int pkv_q4_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size_t* 
  * One decode step over 4-bit pages: as pkv_decode_step, with q, block_table, seq_lens and out of the same layouts and
  * attention over the values that the codes stand for (the products take the codes as they are; scales and offsets are
  * applied in fp32). There is no plan: the division of the step's pages over the GPU is worked out on the device from
- * seq_lens, so one captured graph serves every step of a batch. |scale| <= 1e12. A row of length 0
- * gets 0. Errors the kernels detect: PKV_STATUS_BAD_PAGE (a page outside the pool: its tokens are left out),
+ * seq_lens, so one captured graph serves every step of a batch. |scale| <= 1e12. out must not overlap q.
+ * A row of length 0 gets 0. Errors the kernels detect: PKV_STATUS_BAD_PAGE (a page outside the pool: its tokens are left out),
  * PKV_STATUS_BAD_LEN (the row counts as empty), PKV_STATUS_TIMEOUT.
  */
 int pkv_q4_decode_step(const pkv_problem* problem, const void* q, const void* pool, const int32_t* block_table,

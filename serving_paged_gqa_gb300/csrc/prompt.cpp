@@ -76,6 +76,7 @@ int q4_step(const pkv_problem* pr, const void* q, const void* k_new, const void*
     if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
         !aligned(block_table, 4) || !aligned(seq_lens_dev, 4))
         return PKV_E_ALIGN;
+    if (out == q) return PKV_E_INVAL;  // the pieces of a row read q when others are done
     Q4Params p{};
     p.q = q;
     p.k_new = k_new;
@@ -125,6 +126,7 @@ extern "C" int pkv_prompt_attention(const pkv_prompt* pm, const void* q, const v
     if (!q || !k || !v || !cu_seqlens || !out) return PKV_E_NULLPTR;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 4))
         return PKV_E_ALIGN;
+    if (out == q || out == k || out == v) return PKV_E_INVAL;  // tiles are read while others are written
     PromptParams p{};
     p.q = q;
     p.k = k;

@@ -65,6 +65,13 @@ def test_prompt_attention_refuses_before_any_work(change, code):
     assert attention(**change) == code
 
 
+def test_an_output_at_the_address_of_an_input_is_refused():
+    b = vp(1 << 21)
+    for call in (dict(out=A, k=b, v=b), dict(q=b, out=A, v=b), dict(q=b, k=b, out=A)):
+        assert attention(**call) == INVAL
+    assert decode(False) == INVAL and decode(True) == INVAL
+
+
 def pages(call, pr=None, p=None, k=A, v=A, cu=A, start=None, pool=A, pool2=A, bt=A, sms=152, ws=A, n=256):
     pr, p = problem() if pr is None else pr, prompt() if p is None else p
     lib, a, b = pkv.load(), ctypes.byref(pr), ctypes.byref(p)
