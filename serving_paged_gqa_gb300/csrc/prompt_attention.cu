@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 uint8_t* v = smem + off_ring + (pos % kStages) * kTileBytes;
                 const int first = end - (steps - 1) * kRows, last = (first + 15) & ~15;
                 for (int i = first * 16 + lane; i < last * 16; i += 32)
-                    *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kv_full[pos % kStages]);
@@ -951,7 +952,8 @@ int launch(const Params& prm, int num_sms, cudaStream_t stream) {
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
     // at most this many pairs of tiles: every sequence begins one, and the rest are full
-    const int64_t pairs = ((int64_t)prm.p.total_tokens * G / (2 * kRows) + std::min(prm.p.num_seqs, prm.p.total_tokens)) * prm.p.Hkv;
+    const int64_t pairs =
+        ((int64_t)prm.p.total_tokens * G / (2 * kRows) + std::min(prm.p.num_seqs, prm.p.total_tokens)) * prm.p.Hkv;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(pairs, num_sms));
     return launch_kernel(prompt_kernel<G>, grid, kThreads, kSmem, stream, prm);
 }

@@ -13,8 +13,8 @@
 //
 // Bound: HBM; a (token, KV head) is 144 bytes against 512 in fp16. A unit is 4 pages (64 tokens) of one (row, KV head),
 // four bulk copies of 2304 bytes into one ring stage, and goes to one consumer warp. Measured on a GB300 (G = 4): 48 rows
-// of 900-32768 tokens, 765 MB, 143 us: 5.4 TB/s, 0.80 of the copy bandwidth;
-// copies alone 125 us, arithmetic alone 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.4 us.
+// of 900-32768 tokens, 765 MB, 143 us: 5.4 TB/s, 0.80 of the copy bandwidth; copies alone 125 us, arithmetic alone
+// 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.8 us.
 // Division: the units of all (row, KV head) pairs form one line, and each CTA takes an equal piece of it, whatever the
 // rows' lengths; every CTA finds its piece itself from a scan of seq_lens, so there is no plan. A pair that lies in one
 // piece is written out at once. The others leave a state (m, l, accumulator) per piece, and the last of a pair's
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                          G * kRowBytes, &seg_q[slot]);
             }
             __syncwarp();
-            // Sixteen units at a time, a lane each: the warp sleeps on the first stage that is still in use, then every
+            // Eight units (kChunk) at a time, a lane each: the warp sleeps on the first stage that is still in use, then every
             // lane whose stage is free announces its unit and issues its copies (one unit after the other, a loader
             // needs 600 cycles a unit, which halves the bandwidth).
             for (int c0 = 0; c0 < n && ok; c0 += kChunk) {
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(Shape<G>::threads, Shape<G>::per_sm) q4_decode
                 // weights * scale, which this lane estimates from its own tokens of the first page (any amount would be
                 // right; from its tokens of all pages: 1 % slower, and the same error).
                 {
-                    const float k0 = !kFold || t4 < 2 ? 8.f * kUnitTokens / kTok * 5.9604644775390625e-8f : 0.f;  // not the second part
+                    const float k0 = !kFold || t4 < 2 ? 8.f * kUnitTokens / kTok * 5.9604644775390625e-8f : 0.f;  // (not part 2)
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
