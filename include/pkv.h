@@ -410,7 +410,10 @@ int pkv_decode_step_static(const pkv_plan_t* plan, const pkv_problem* problem, c
  * num_sms below is the SM count of the current GPU, at most PKV_MAX_SMS.
  *
  * A workspace serves one call at a time: calls (and replays of captured ones) that share one are ordered on a stream. It
- * is zeroed once (pkv_workspace_init), and again after a call that raised PKV_STATUS_TIMEOUT.
+ * is zeroed once (pkv_workspace_init), and again after a call that raised PKV_STATUS_TIMEOUT. One that is large enough
+ * for each serves 4-bit decode steps of different heads, batches and num_sms in turn. The steps of the FP16 cache keep
+ * other things in theirs: a workspace that goes from a pkv_decode* step to a 4-bit one, or back, is zeroed in between. The
+ * prompt calls and pkv_q4_read use the header alone and may be given any workspace of the library.
  */
 #define PKV_MAX_SMS 4096
 #define PKV_Q4_BLOCK_BYTES 2304

@@ -43,6 +43,9 @@ constexpr int kStageBytes = kUnitPages * kQ4Block;
 constexpr int kChunk = 32 / kUnitPages;  // units whose block-table entries one warp-wide read brings
 constexpr int kCombRow = kHeadDim + 4;  // floats per partial output row: rows land 4 banks apart
 constexpr uint32_t kAllPages = (1u << kUnitPages) - 1u;
+// Arrival counters behind the workspace's header, one a piece. They are zero between steps, so they lie where no step of
+// other heads or of a grid of another size puts its states: their place and number depend on nothing.
+constexpr int kMaxPieces = 2 * 4 * kCombRow;
 // Units per CTA below which fewer CTAs take part: two a consumer warp. A row of 512 tokens (8 units a KV head) takes 8.4 us
 // with 8, and 9.7 with 4 (two pieces a pair, and their merge) or 12.4 with 12.
 constexpr int kMinUnits = 8;
@@ -80,6 +83,7 @@ struct Shape {
     static constexpr int smem = off_new + kQ4Block;
     static_assert(off_bars % 8 == 0 && off_comb % 16 == 0 && smem <= 227 * 1024, "layout");
     static constexpr int kFactors = NB * NC * kCombRow;  // pieces of a pair whose factors fit (the grid is smaller)
+    static_assert(kFactors <= kMaxPieces, "an arrival counter for every piece");
 };
 
 __device__ __forceinline__ int row_length(const Q4Params& p, int b) {
@@ -890,7 +894,7 @@ int launch(Q4Params p, int num_sms, cudaStream_t stream) {
     char* ws = reinterpret_cast<char*>(p.hdr);
     int64_t off = sizeof(pkv_ws_header);
     p.counters = reinterpret_cast<uint32_t*>(ws + off);
-    off += align_ws(4 * (int64_t)ctas);
+    off += align_ws(4 * kMaxPieces);
     p.ml = reinterpret_cast<float2*>(ws + off);
     off += align_ws(8 * 2 * (int64_t)ctas * G);
     p.acc = reinterpret_cast<float*>(ws + off);
@@ -905,7 +909,7 @@ int launch(Q4Params p, int num_sms, cudaStream_t stream) {
 size_t q4_workspace_bytes(const pkv_problem& pr, int num_sms) {
     const int g = pr.num_q_heads / pr.num_kv_heads;
     const int64_t ctas = max_ctas(g, num_sms);
-    return sizeof(pkv_ws_header) + align_ws(4 * ctas) + align_ws(16 * ctas * g) + 2 * ctas * g * kHeadDim * 4;
+    return sizeof(pkv_ws_header) + align_ws(4 * kMaxPieces) + align_ws(16 * ctas * g) + 2 * ctas * g * kHeadDim * 4;
 }
 
 int launch_q4_decode(const Q4Params& p, int num_sms, void* stream) {
