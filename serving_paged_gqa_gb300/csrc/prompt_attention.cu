@@ -647,13 +647,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const int token = w.t0 + x * kTokens + row / G;
             float ref = -INFINITY, l = 0.f;
             for (int j = 0; j < steps; ++j) {
-                if (!warp_wait(&s_full[x], ns & 1, ctx)) {
+                const int step = ns++;
+                const int last = end - j * kRows - h * 64;  // keys of this half, counted from its first
+                // The tile's last step ends in the first half: the second does not wait for its scores (nothing would keep
+                // the next tile's from coming before it looks, and a parity two phases on does not pass). They have come
+                // when the tile's accumulator is complete, for which it waits below.
+                if (last <= 0) continue;
+                if (!warp_wait(&s_full[x], step & 1, ctx)) {
                     ok = false;
                     break;
                 }
-                const int step = ns++;
-                const int last = end - j * kRows - h * 64;  // keys of this half, counted from its first
-                if (last <= 0) continue;                    // the tile's last step ends in the first half
                 tc_fence_after();
                 // The step with the diagonal and the sequence's end is masked; the others are whole.
                 const bool tail = j == steps - 1;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import serving_paged_gqa_gb300 as pkv
-from test_prompts_gpu import D, SCALE, check_q4, gen, ints, new_ws, normal, q4_cache, status
+from test_prompts_gpu import D, SCALE, check_prompt, check_q4, gen, ints, new_ws, normal, packed, q4_cache, status
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,21 @@ def test_q4_steps_of_different_heads_share_a_workspace():
             q4_step(p, q, pool, bt, ints(lens), n, ws, out)
             assert status(ws) == 0
             check_q4(q, pool, bt, lens, out, what=f"{hq} heads on {n} SMs")
+
+
+# ------------------------------------------------------------------------------------- tiles that end in a step's first half
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 3), (16, 1)])
+@pytest.mark.parametrize("num_sms", [1, 2, 7])
+def test_prompt_many_tiles_that_end_in_a_first_half(num_sms, hq, hkv):
+    """Sequences whose last step has 1 to 64 keys, among others, dozens of pairs of tiles one after the other in a CTA: the
+    warps of the second 64 keys have nothing to do in those steps, and meet the next tile's in phase all the same."""
+    lens = [40, 300, 1, 64, 65, 128, 190, 129, 20, 192, 257, 0, 60, 384 + 33, 5, 64] * 2
+    q, k, v, cu = packed(gen(230 + hq), lens, hq, hkv, fused=False)
+    out = torch.full_like(q, math.nan)
+    ws = new_ws()
+    p = pkv.make_prompt(len(lens), q.shape[0], hq, hkv, D)
+    for call in range(3):
+        rc = pkv.load().pkv_prompt_attention(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), SCALE, num_sms, ws.data_ptr(),
+                                             ws.numel(), out.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and status(ws) == 0
+        check_prompt(q, k, v, cu, out, what=f"call {call}")
