@@ -27,13 +27,23 @@
 // TMEM (512 columns): S_A, S_B (P over columns 0-31 and 64-95 of each), O_A, O_B. Instructions of one thread run in
 // order, so S(j+1) may be issued over P(j) right after PV(j).
 //
-// Weights are 2^(x - ref), one ref a row. It is the maximum of the row's first 64 keys, and stays as it is while no weight
-// exceeds 2^15, for which 64 keys' sum of weights, needed anyway, is the test: an ordinary step has no search for a
-// maximum. A thread whose keys fail the test (before their weights are announced) raises ref by a whole number to its
-// keys' maximum, scales what has been accumulated, and computes its weights again. The two threads of a row do not wait
-// for each other in ordinary steps (that cost 450 cycles a step): products of a step's second half never begin before
-// those of its first, so where the first half raises, it scales the second half's weights in TMEM as well (by a power
-// of two: exactly), and where the second half does, it first waits for the first half's products. Each sees what the
+// Weights are 2^(x - ref), one ref a row, and enter the second product as fp16, the type of V, which both operands must
+// have: the relative error of 16384 normal tokens' outputs is 2.9e-4, with 32-bit weights 2.1e-4, of which the output's
+// rounding is most; a second fp16 part would be half as many matrix products again. Sums and accumulators are fp32.
+// ref is the maximum of the row's first 64 keys less kLift, and stays as it is while the sum of 64 keys' weights, needed
+// anyway, fits fp16: an ordinary step has no search for a maximum. A thread whose keys fail the test (before their
+// weights are announced) raises ref by a whole number to its keys' maximum less kLift, scales what has been accumulated,
+// and computes its weights again.
+// kLift divides fp16's 40 powers of two between weights that are small beside a row's largest and scores that grow behind
+// its first 64 keys. Weights below 2^-(14 + kLift) of the largest lose bits, and below 2^-(25 + kLift) are 0, which shows
+// where a token whose V is 0 takes most of the weight. Relative error with such a first token 16 / 18 / 20 nats above
+// 16384 others, and us of 2048 tokens whose scores have a standard deviation of 1-2 / 3 / 4 / 6 nats: kLift 0 1.3e-3,
+// 0.27, 0.93; 30, 30, 35, 53. 4: 2.1e-4, 4.4e-4, 6.6e-2; 30, 35, 46, 67. 5: 2.1e-4, 2.5e-4, 9e-3; 31, 37, 51, 69. 6: 2.1e-4,
+// 2.1e-4, 9e-4; 31, 40, 57, 71. (32-bit weights 1.7-2.1e-4. 16384 tokens take 4, 11, 23 % longer with 5 than with 0 at
+// 3, 4, 6 nats.)
+// The two threads of a row do not wait for each other in ordinary steps (that cost 450 cycles a step): products of a
+// step's second half never begin before those of its first, so where the first half raises, it scales the second half's
+// weights in TMEM as well, and where the second half does, it first waits for the first half's products. Each sees what the
 // other has raised at the next step.
 //
 // A value that a row does not attend to is multiplied by a weight of 0, which does not remove an infinity or a NaN of
@@ -72,7 +82,8 @@ constexpr int kSoftmax = 512;                // threads of the softmax
 constexpr int kThreads = kSoftmax + 128;
 // 512 * 104 + 128 * 64 = 640 * 96, what the launch has; equal shares of 96 are 1-3 % slower
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-constexpr float kMost = 32768.f;             // sum of 64 weights above which the row's reference is raised
+constexpr float kMost = 65504.f;             // sum of 64 weights above which the row's reference is raised
+constexpr float kLift = 5.f;                 // the largest weight where the reference was set, in powers of two
 
 struct Work {
     int32_t first, n, t0, h;  // sequence's first packed row and length; first token of tile A; KV head (-1: no more work)
@@ -111,6 +122,10 @@ __device__ __forceinline__ Row4 floats4(const uint2& u) {
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
     return Row4{{a.x, a.y, b.x, b.y}};
 }
+
+// The reference for a largest score. Scores of which an fp32 has no fractions are it themselves: nothing is then added to
+// their rounding.
+__device__ __forceinline__ float ref_for(float top) { return fabsf(top) < 16777216.f ? top - kLift : top; }
 
 // One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, 4 at a time; lane l holds dims
 // 4l..4l+3. Stores dims 64 half .. + 63. (With 8 at a time the kernel's ordinary steps spill registers.)
@@ -743,15 +758,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 };
                 // The reference that this half's keys ask for: above the present one by a whole number.
                 auto raised = [&]() {
-                    const float top = greatest() * sl2;
-                    return ref == -INFINITY ? top : top > ref ? ref + ceilf(top - ref) : ref;
+                    const float to = ref_for(greatest() * sl2);
+                    return ref == -INFINITY ? to : to > ref ? ref + ceilf(to - ref) : ref;
                 };
                 if (j > 0) {  // the other half may have raised it in the step before
                     const float r = *ref_at;
                     scale_sum(r);
                     ref = r;
                 } else if (h == 0) {
-                    ref = greatest() * sl2;
+                    ref = ref_for(greatest() * sl2);
                     *ref_at = ref;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(settled);
@@ -783,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         tmem_wait_ld();
                         tmem_use32(t);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {  // in fp32: weights of 2^15 times a power of two that fp16 may not have
+                        for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
                             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
                             t[i] = pack_half2(v.x * f2, v.y * f2);
                         }
@@ -894,7 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
             }
             ++no;
-            // The largest weight is 1 next to the row's reference, or above 1/2 where it was raised.
+            // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
+            // themselves 1, or above 1/2.
             const bool low_sum = !(total >= 0.25f);
             const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
             const unsigned again = __ballot_sync(0xffffffffu, mine && odd && !isnan(total));

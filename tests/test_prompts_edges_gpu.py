@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import prompt_reference as ref
 import serving_paged_gqa_gb300 as pkv
 from test_prompts_gpu import D, SCALE, check_prompt, check_q4, gen, ints, new_ws, normal, packed, q4_cache, status
 
@@ -65,3 +66,48 @@ def test_prompt_many_tiles_that_end_in_a_first_half(num_sms, hq, hkv):
                                              ws.numel(), out.data_ptr(), torch.cuda.current_stream().cuda_stream)
         assert rc == 0 and status(ws) == 0
         check_prompt(q, k, v, cu, out, what=f"call {call}")
+
+
+# ----------------------------------------------------------------------------------------------- small softmax weights
+@pytest.mark.parametrize("n,hq,hkv", [(3000, 8, 2), (16384, 4, 4)])
+@pytest.mark.parametrize("nats", [10.0, 14.0, 16.0, 18.0])
+def test_prompt_small_weights_beside_a_large_one(nats, n, hq, hkv):
+    """An attention sink: the first key's score is `nats` above the mean of the others, and its V is 0, so that the output
+    is made of the small weights. Their numerator keeps what their sum counts."""
+    g = gen(210)
+    q, k, v, cu = packed(g, [n], hq, hkv, fused=False)
+    q[:, :, 0] = 8.0
+    k[:, :, 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = nats / (8.0 * SCALE)
+    v = (v.float() * 0.5 + 1.0).half()
+    v[0] = 0.0
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    for a in (1, n // 2, n - 130):
+        e = min(n, a + 130)
+        w, mag = ref.attend(q[a:e], k[:e], v[:e], SCALE, a)
+        # As ref.prompt_bound, but for weights below fp16's least normal one: the first key's weight is 2^5 (what a row's
+        # first maximum gets), so half the least subnormal is 2^-30 of it; the sum of all weights is at least that.
+        ds = ref.prompt_bound(w, mag, 0, q[a:e], k[:e], v[:e], SCALE)
+        ref.check(out[a:e], w, ds + e * 2.0 ** -30 * float(v.abs().max()), f"rows {a}..")
+
+
+@pytest.mark.parametrize("rise", [11.5, 16.9, 18.0, 19.9, 21.0, 25.0])
+@pytest.mark.parametrize("first,second", [(130, 200), (200, 130), (150, 255), (70, 10)])
+def test_prompt_a_step_whose_halves_rise_by_little(rise, first, second):
+    """Key `first` raises the running reference by `rise` (in log2), while key `second` of the same step's other half stays
+    just below the 2^16 that lets its weight as it is (the first keys have 2^5); its V is large enough to be seen."""
+    n, g = 300, gen(240)
+    q, k, v, cu = packed(g, [n], 8, 1, fused=False)
+    unit = 1.0 / (8.0 * SCALE * math.log2(math.e))  # of k's dim 0, for a score of 1 in log2
+    q.zero_()
+    k.zero_()
+    q[:, :, 0] = 8.0
+    k[first, :, 0], k[second, :, 0] = rise * unit, 10.9 * unit
+    v[second] *= 2.0 ** max(0.0, rise - 10.9)
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
