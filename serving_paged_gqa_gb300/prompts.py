@@ -132,6 +132,16 @@ def _table(block_table: torch.Tensor, problem: Problem) -> int:
     return _addr(block_table, torch.int32, "block_table")
 
 
+def _pool(t: torch.Tensor, name: str, problem: Problem, prompt: Prompt) -> None:
+    """Checks that a pool is the one that the problem describes (the kernels bound their pages by the problem)."""
+    if name == "pool":
+        want = (problem.num_pages, prompt.num_kv_heads, PKV_Q4_BLOCK_BYTES)
+    else:
+        want = (problem.num_pages, problem.page_size, prompt.num_kv_heads, prompt.head_dim)
+    if t.shape != want:
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+
+
 def _attention(dev, prompt, q, k, v, cu_seqlens, scale, ws, out, stream) -> None:
     _call(dev, "pkv_prompt_attention", _byref(prompt), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           _seqs(cu_seqlens, prompt.num_seqs), scale, _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(),
@@ -172,6 +182,8 @@ def pkv_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, start,
                       stream=None) -> None:
     _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride)
     _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _pool(k_pool, "k_pool", problem, prompt)
+    _pool(v_pool, "v_pool", problem, prompt)
     _append(_device(k, v, cu_seqlens, start, k_pool, v_pool, block_table, ws), problem, prompt, k, v, cu_seqlens, start,
             k_pool, v_pool, block_table, ws, stream)
 
@@ -180,6 +192,7 @@ def pkv_q4_prompt_append(problem: Problem, prompt: Prompt, k, v, cu_seqlens, sta
                          stream=None) -> None:
     _fits(k, "k", prompt, prompt.num_kv_heads, prompt.k_stride)
     _fits(v, "v", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _pool(pool, "pool", problem, prompt)
     _q4_append(_device(k, v, cu_seqlens, start, pool, block_table, ws), problem, prompt, k, v, cu_seqlens, start, pool,
                block_table, ws, stream)
 
@@ -188,6 +201,7 @@ def pkv_q4_read(problem: Problem, prompt: Prompt, cu_seqlens, start, pool, block
                 stream=None) -> None:
     _fits(k_out, "k_out", prompt, prompt.num_kv_heads, prompt.k_stride)
     _fits(v_out, "v_out", prompt, prompt.num_kv_heads, prompt.v_stride)
+    _pool(pool, "pool", problem, prompt)
     _q4_read(_device(pool, k_out, v_out, cu_seqlens, start, block_table, ws), problem, prompt, cu_seqlens, start, pool,
              block_table, k_out, v_out, ws, stream)
 
