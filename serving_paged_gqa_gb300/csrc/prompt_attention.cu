@@ -128,9 +128,12 @@ __device__ __forceinline__ Row4 floats4(const uint2& u) {
 __device__ __forceinline__ float ref_for(float top) { return fabsf(top) < 16777216.f ? top - kLift : top; }
 
 // One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, 4 at a time; lane l holds dims
-// 4l..4l+3. Stores dims 64 half .. + 63. (With 8 at a time the kernel's ordinary steps spill registers.)
+// 4l..4l+3. Stores dims 64 half .. + 63. (With 8 at a time the kernel's ordinary steps spill registers.) Factors of the
+// numerator stay at 2^-126 or above, which is nothing to finite values, and keeps infinities of V that no weight is too
+// small for: 0 times one would be NaN.
 __device__ __forceinline__ void row_attention(const PromptParams& p, int64_t first, int pos, int hq, int half, int lane) {
     constexpr int kKeys = 4;
+    constexpr float kLeast = 0x1p-126f;
     const int h = hq / (p.Hq / p.Hkv);
     const __half* k = static_cast<const __half*>(p.k) + first * p.k_stride + h * kHeadDim + lane * 4;
     const __half* v = static_cast<const __half*>(p.v) + first * p.v_stride + h * kHeadDim + lane * 4;
@@ -162,7 +165,7 @@ __device__ __forceinline__ void row_attention(const PromptParams& p, int64_t fir
         const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref);
         l *= f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[x] *= f;
+        for (int x = 0; x < 4; ++x) o[x] *= fmaxf(f, kLeast);
 #pragma unroll
         for (int i = 0; i < kKeys; ++i)
             if (j + i <= pos) {
@@ -170,11 +173,11 @@ __device__ __forceinline__ void row_attention(const PromptParams& p, int64_t fir
                 const Row4 x = floats4(b[i]);
                 l += e;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) o[y] += e * x.x[y];
+                for (int y = 0; y < 4; ++y) o[y] += fmaxf(e, kLeast) * x.x[y];
             }
         m = mn;
     }
-    const float inv = 1.f / l;
+    const float inv = l > 0.f ? 1.f / l : NAN;  // NaN: a score is, or all of them are -inf
     uint2 u;
     u.x = pack_half2(o[0] * inv, o[1] * inv);
     u.y = pack_half2(o[2] * inv, o[3] * inv);

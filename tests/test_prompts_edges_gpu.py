@@ -111,3 +111,33 @@ def test_prompt_a_step_whose_halves_rise_by_little(rise, first, second):
     out = pkv.prompt_attention(q, k, v, cu, ws=ws)
     assert status(ws) == 0
     check_prompt(q, k, v, cu, out)
+
+
+# ------------------------------------------------------------------------------------- infinities in recomputed rows
+@pytest.mark.parametrize("far", [40.0, 400.0])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (2, 2)])
+def test_prompt_infinities_in_rows_that_are_computed_again(hq, hkv, far):
+    """V has infinities in a token whose weight is 0 in fp32, before and after the row's greatest score, and a NaN that the
+    row does not attend to, for which it is computed again: infinities still make their dims infinite, of both signs NaN."""
+    n, hit, g = 200, 180, gen(220)
+    q, k, v, cu = packed(g, [n], hq, hkv, fused=False)
+    q[:, :, 0] = 8.0
+    k[:, :, 0] = 0.0
+    k[100, :, 0] = far / (8.0 * SCALE * math.log2(math.e))  # from here on the others' weights are about 2^-far
+    vb = v.clone()
+    vb[5, :, 10], vb[150, :, 11], vb[7, :, 12], vb[151, :, 12], vb[9, :, 13] = math.inf, -math.inf, math.inf, -math.inf, math.nan
+    vb[hit, :, 20] = math.nan  # its tile's rows before it are computed again
+    vb[hit, :, 100] = math.inf
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, vb, cu, ws=ws)
+    assert status(ws) == 0
+    v[[5, 150, 7, 151, 9, hit, hit], :, [10, 11, 12, 12, 13, 20, 100]] = 0.0
+    w, mag = ref.attend(q, k, v, SCALE, 0)
+    bound = ref.prompt_bound(w, mag, n, q, k, v, SCALE)
+    want = w.clone()
+    want[5:, :, 10], want[150:, :, 11], want[7:151, :, 12], want[151:, :, 12], want[9:, :, 13] = math.inf, -math.inf, math.inf, math.nan, math.nan
+    want[hit:, :, 20], want[hit:, :, 100] = math.nan, math.inf
+    fin = torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert (out.double()[torch.isinf(want)] == want[torch.isinf(want)]).all()
+    ref.check(torch.where(fin, out.double(), 0.0), torch.where(fin, want, 0.0), bound)
