@@ -141,3 +141,62 @@ def test_prompt_infinities_in_rows_that_are_computed_again(hq, hkv, far):
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     assert (out.double()[torch.isinf(want)] == want[torch.isinf(want)]).all()
     ref.check(torch.where(fin, out.double(), 0.0), torch.where(fin, want, 0.0), bound)
+
+
+# ------------------------------------------------------------------------------------------------- rows without a finite score
+def graph_us(call, reps=6, best_of=9):
+    """Device time of a call: the shortest of several replays of a graph of `reps` calls."""
+    for _ in range(3):
+        call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(reps):
+            call()
+    times = []
+    for _ in range(best_of + 1):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / reps * 1e3)
+    return min(times[1:])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_prompt_rows_of_nan_behind_the_end_cost_nothing(bad):
+    """A padded batch's garbage: the queries behind a sequence share its last tile's warps, whose steps stay ordinary."""
+    n = 2043
+    q, k, v, cu = packed(gen(250), [n], 32, 8, behind=60, fused=False)
+    out, ws = torch.empty_like(q), new_ws()
+    took = []
+    for x in (1.0, bad):
+        q[n:] = x
+        took.append(graph_us(lambda: pkv.prompt_attention(q, k, v, cu, out=out, ws=ws)))
+        assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
+    assert took[1] < 1.5 * took[0], took
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (2, 2)])
+def test_prompt_rows_whose_first_scores_are_minus_infinity(hq, hkv):
+    """Keys of which every query makes -inf, at the beginning, in whole steps and in a step's second half: rows that attend
+    to nothing else are NaN (a softmax of -inf alone), and the others are as if those keys were not there."""
+    n, g = 420, gen(251)
+    for hide in (list(range(0, 3)), list(range(0, 64)), list(range(0, 70)), list(range(0, 200)), list(range(0, 300)),
+                 [*range(0, 64), *range(128, 192)], list(range(64, 128))):
+        q, k, v, cu = packed(g, [n], hq, hkv, fused=False)
+        q[:, :, 0] = 4.0
+        k[:, :, 0] = 0.0
+        kb = k.clone()
+        kb[hide, :, 0] = -math.inf
+        ws = new_ws()
+        out = pkv.prompt_attention(q, kb, v, cu, ws=ws)
+        assert status(ws) == 0
+        keep = torch.tensor([i for i in range(n) if i not in set(hide)], device="cuda")
+        first = int(keep[0])
+        assert torch.isnan(out[:first]).all()
+        for i in range(first, n, 29):
+            seen = keep[keep <= i]
+            w, mag = ref.attend(q[i:i + 1], k[seen], v[seen], SCALE, len(seen) - 1)
+            ref.check(out[i:i + 1], w, ref.prompt_bound(w, mag, len(seen), q[i:i + 1], k[seen], v[seen], SCALE), f"{hide[-1]} row {i}")
