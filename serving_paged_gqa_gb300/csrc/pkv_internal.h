@@ -79,6 +79,7 @@ struct PromptParams {
     int64_t q_stride, k_stride, v_stride, out_stride;  // elements between tokens
     int32_t num_seqs, total_tokens, Hq, Hkv;
     float scale_log2;
+    uint64_t wait_ns;  // limit of a wait (set by the launcher)
 };
 
 // Arguments of the kernels that move packed prompts into pages and back (prompt_pages.cu).

@@ -11,6 +11,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 struct WaitCtx {
     volatile int* abort_flag;
     uint32_t* status;
+    uint64_t limit_ns = kWaitLimitNs;
 };
 
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) { atomicOr(status, bits); }
@@ -28,7 +29,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
         if (it % kPollEvery == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
-            const bool stop = (*ctx.abort_flag != 0) || (now - t0 > kWaitLimitNs);
+            const bool stop = (*ctx.abort_flag != 0) || (now - t0 > ctx.limit_ns);
             if (__any_sync(0xffffffffu, stop)) {
                 if ((threadIdx.x & 31) == 0 && *ctx.abort_flag == 0) {
                     *ctx.abort_flag = 1;
@@ -49,7 +50,7 @@ __device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, cons
         if (it % kPollEvery == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
-            if (*ctx.abort_flag != 0 || now - t0 > kWaitLimitNs) {
+            if (*ctx.abort_flag != 0 || now - t0 > ctx.limit_ns) {
                 if (*ctx.abort_flag == 0) {
                     *ctx.abort_flag = 1;
                     raise_status(ctx.status, PKV_STATUS_TIMEOUT);

@@ -59,7 +59,8 @@
 // 30.5 us; one prompt of 17 tokens 6.3 us. The tensor pipe is active 68 % of the time at 4096 tokens.
 //
 // Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
-// have in flight, and the CTA frees its TMEM and returns.
+// have in flight, and the CTA frees its TMEM and returns. The limit grows with the prompt: a warp may finish 32 rows from
+// all keys before them (0.16 us a key), while the others wait for it.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -74,6 +75,7 @@
 namespace pkv {
 namespace {
 
+constexpr uint64_t kFinishNs = 32 * 1000;    // a warp's 32 rows, by the key that they are computed from again, at most
 constexpr int kRows = 128;                   // rows of a tile, keys of a step
 constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two boxes of 64 dims
 constexpr int kBoxBytes = kTileBytes / 2;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     Work* work = reinterpret_cast<Work*>(smem + off_work);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
-    const WaitCtx ctx{abort_flag, &p.hdr->status};
+    const WaitCtx ctx{abort_flag, &p.hdr->status, p.wait_ns};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -987,6 +989,7 @@ int launch(const Params& prm, int num_sms, cudaStream_t stream) {
 int launch_prompt_attention(const PromptParams& p, int num_sms, void* stream) {
     Params prm;
     prm.p = p;
+    prm.p.wait_ns = kWaitLimitNs + kFinishNs * p.total_tokens;
     const int g = p.Hq / p.Hkv;
     if (!encode(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g) ||
         !encode(&prm.k, p.k, p.Hkv, p.total_tokens, p.k_stride, 1) ||

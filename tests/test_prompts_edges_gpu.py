@@ -200,3 +200,20 @@ def test_prompt_rows_whose_first_scores_are_minus_infinity(hq, hkv):
             seen = keep[keep <= i]
             w, mag = ref.attend(q[i:i + 1], k[seen], v[seen], SCALE, len(seen) - 1)
             ref.check(out[i:i + 1], w, ref.prompt_bound(w, mag, len(seen), q[i:i + 1], k[seen], v[seen], SCALE), f"{hide[-1]} row {i}")
+
+
+def test_prompt_rows_computed_again_for_longer_than_a_wait_may_take():
+    """A NaN in the last of half a million tokens: a warp computes 32 rows before it again from all their keys, which takes
+    more than the 2 s after which a wait of the kernel's other warps gives up."""
+    n = 1 << 19
+    q, k, v, cu = packed(gen(260), [n], 1, 1, fused=False)
+    v[n - 1, 0, 77] = math.nan
+    ws = new_ws()
+    out = torch.full_like(q, math.inf)
+    pkv.prompt_attention(q, k, v, cu, out=out, ws=ws)
+    assert status(ws) == 0
+    assert torch.isnan(out[n - 1, 0, 77]) and int((~torch.isfinite(out)).sum()) == 1
+    v[n - 1, 0, 77], out[n - 1, 0, 77] = 0.0, 0.0
+    for a in (n - 128, n // 2):
+        w, mag = ref.attend(q[a:a + 127], k[:a + 127], v[:a + 127], SCALE, a)
+        ref.check(out[a:a + 127], w, ref.prompt_bound(w, mag, a + 127, q[a:a + 127], k[:a + 127], v[:a + 127], SCALE), f"rows {a}..")
