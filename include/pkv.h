@@ -454,6 +454,7 @@ int pkv_prompt_attention(const pkv_prompt* prompt, const void* q, const void* k,
  * of prompt only num_seqs, total_tokens, num_kv_heads, head_dim, k_stride and v_stride matter beyond that check. A
  * row that would outgrow its block table raises PKV_STATUS_BAD_LEN and is skipped; a token whose page is outside the
  * pool raises PKV_STATUS_BAD_PAGE and is skipped. Two tokens must not share a slot. Other slots keep their values.
+ * The two pools are different memory (one address for both is refused).
  */
 int pkv_prompt_append(const pkv_problem* problem, const pkv_prompt* prompt, const void* k, const void* v,
                       const int32_t* cu_seqlens, const int32_t* start, void* k_pool, void* v_pool,
@@ -467,7 +468,8 @@ int pkv_q4_prompt_append(const pkv_problem* problem, const pkv_prompt* prompt, c
 /*
  * Tokens of 4-bit pages back as packed FP16 rows (the values that the codes stand for, rounded once): row
  * cu_seqlens[s] + i of k_out and v_out receives token start[s] + i of row s. Arguments as for pkv_q4_prompt_append;
- * k_stride and v_stride are those of k_out and v_out.
+ * k_stride and v_stride are those of k_out and v_out, which must not overlap each other or the pool (the same address is
+ * refused).
  */
 int pkv_q4_read(const pkv_problem* problem, const pkv_prompt* prompt, const int32_t* cu_seqlens, const int32_t* start,
                 const void* pool, const int32_t* block_table, void* k_out, void* v_out, int32_t num_sms, void* ws,
@@ -484,7 +486,8 @@ int pkv_q4_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size_t* 
  * One decode step over 4-bit pages: as pkv_decode_step, with q, block_table, seq_lens and out of the same layouts and
  * attention over the values that the codes stand for (the products take the codes as they are; scales and offsets are
  * applied in fp32). There is no plan: the division of the step's pages over the GPU is worked out on the device from
- * seq_lens, so one captured graph serves every step of a batch. |scale| <= 1e12. out must not overlap q.
+ * seq_lens, so one captured graph serves every step of a batch. |scale| <= 1e12. out must not overlap q or the pool (the same
+ * address is refused).
  * A row of length 0 gets 0. Errors the kernels detect: PKV_STATUS_BAD_PAGE (a page outside the pool: its tokens are left out),
  * PKV_STATUS_BAD_LEN (the row counts as empty), PKV_STATUS_TIMEOUT.
  */
@@ -495,7 +498,7 @@ int pkv_q4_decode_step(const pkv_problem* problem, const void* q, const void* po
 /*
  * The same with the new token's K/V appended (as pkv_decode_step_append): k_new, v_new [B][Hkv][d] fp16 are quantised
  * into slot (L_b - 1) % 16 of page block_table[b][(L_b - 1) / 16], and the step attends to the quantised token. No two
- * rows may append to one page.
+ * rows may append to one page. out must not overlap k_new or v_new either.
  */
 int pkv_q4_decode_step_append(const pkv_problem* problem, const void* q, const void* k_new, const void* v_new,
                               void* pool, const int32_t* block_table, const int32_t* seq_lens_dev, float scale,

@@ -76,7 +76,8 @@ int q4_step(const pkv_problem* pr, const void* q, const void* k_new, const void*
     if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
         !aligned(block_table, 4) || !aligned(seq_lens_dev, 4))
         return PKV_E_ALIGN;
-    if (out == q) return PKV_E_INVAL;  // the pieces of a row read q when others are done
+    // the pieces of a row read q, k_new and v_new when others are done, and the pool's pages all the time
+    if (out == q || out == k_new || out == v_new || out == pool) return PKV_E_INVAL;
     Q4Params p{};
     p.q = q;
     p.k_new = k_new;
@@ -155,6 +156,7 @@ extern "C" int pkv_prompt_append(const pkv_problem* pr, const pkv_prompt* pm, co
     if (nothing(pm)) return PKV_OK;
     if (!k || !v || !cu_seqlens || !k_pool || !v_pool || !block_table) return PKV_E_NULLPTR;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16)) return PKV_E_ALIGN;
+    if (k_pool == v_pool) return PKV_E_INVAL;
     PagesParams p = pages_params(pr, pm, cu_seqlens, start, block_table, ws);
     p.k = k;
     p.v = v;
@@ -187,6 +189,7 @@ extern "C" int pkv_q4_read(const pkv_problem* pr, const pkv_prompt* pm, const in
     if (nothing(pm)) return PKV_OK;
     if (!k_out || !v_out || !cu_seqlens || !pool || !block_table) return PKV_E_NULLPTR;
     if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(pool, 16)) return PKV_E_ALIGN;
+    if (k_out == v_out || k_out == pool || v_out == pool) return PKV_E_INVAL;
     PagesParams p = pages_params(pr, pm, cu_seqlens, start, block_table, ws);
     p.k_pool = k_out;
     p.v_pool = v_out;

@@ -1,6 +1,7 @@
 """The pkv_* wrappers that take a described problem and prompt: they refuse tensors that the descriptions do not fit, and do
 what the calls that describe the tensors themselves do."""
 
+import ctypes
 import math
 
 import pytest
@@ -82,6 +83,22 @@ def test_wrappers_refuse_tensors_that_the_descriptions_do_not_fit(name, arg, bad
     t[arg] = bad(t[arg])
     with pytest.raises(ValueError, match=f"^{arg}\\b"):
         call(name, t)
+
+
+def test_an_output_at_the_address_of_another_argument_is_refused():
+    """(Stand-ins for addresses, never dereferenced: the call is refused before any device work.)"""
+    lib, p, pr, f = pkv.load(), problem(), prompt(), ctypes.c_float(SCALE)
+    a, b, c, d, e = (ctypes.c_void_p(i << 20) for i in range(1, 6))
+
+    def step(out, q=a, k_new=b, v_new=c, pool=d):
+        return lib.pkv_q4_decode_step_append(p, q, k_new, v_new, pool, a, a, f, 152, e, 1 << 30, out, None)
+
+    for out in (a, b, c, d):
+        assert step(out) == -1
+    assert lib.pkv_q4_decode_step(p, a, b, a, a, f, 152, e, 1 << 30, b, None) == -1
+    assert lib.pkv_prompt_append(p, pr, a, b, a, None, c, c, a, 152, e, 256, None) == -1
+    for k_out, v_out in ((b, b), (a, b), (b, a)):
+        assert lib.pkv_q4_read(p, pr, a, None, a, a, k_out, v_out, 152, e, 256, None) == -1
 
 
 @pytest.mark.gpu
