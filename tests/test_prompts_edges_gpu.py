@@ -2,13 +2,15 @@
 against the plain 64-bit forms of tests/prompt_reference.py."""
 
 import math
+import random
 
 import pytest
 import torch
 
 import prompt_reference as ref
 import serving_paged_gqa_gb300 as pkv
-from test_prompts_gpu import D, SCALE, check_prompt, check_q4, gen, ints, new_ws, normal, packed, q4_cache, status
+from test_prompts_gpu import (D, PS, SCALE, check_prompt, check_q4, gen, ints, new_ws, normal, packed, q4_cache, status,
+                              table)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,9 +42,9 @@ def test_q4_steps_of_different_heads_share_a_workspace():
         bt, pool = q4_cache(g, lens, hkv)
         steps.append((hq, hkv, lens, bt, pool, normal(g, len(lens), hq, D)))
     problems = [pkv.q4_problem(q, pool, bt) for _, _, _, bt, pool, q in steps]
-    counts = (sms, 100, 2 * sms)
+    counts = (sms, 100, sms)
     ws = new_ws(max(pkv.pkv_q4_workspace_bytes(p, n) for p in problems for n in counts))
-    for n in (sms, sms, 100, 2 * sms, sms):
+    for n in counts:
         for p, (hq, hkv, lens, bt, pool, q) in zip(problems, steps):
             out = torch.full_like(q, math.nan)
             q4_step(p, q, pool, bt, ints(lens), n, ws, out)
@@ -217,3 +219,80 @@ def test_prompt_rows_computed_again_for_longer_than_a_wait_may_take():
     for a in (n - 128, n // 2):
         w, mag = ref.attend(q[a:a + 127], k[:a + 127], v[:a + 127], SCALE, a)
         ref.check(out[a:a + 127], w, ref.prompt_bound(w, mag, a + 127, q[a:a + 127], k[:a + 127], v[:a + 127], SCALE), f"rows {a}..")
+
+
+# -------------------------------------------------------------------------------------------- many sequences, other heads
+def mixed(n, seed):
+    """Lengths of n sequences, empty ones and of one to a dozen pairs of tiles (at 16 heads to a KV head, a hundred) among
+    them, in no order."""
+    r = random.Random(seed)
+    lens = [r.choice([0, 1, 2, 40, 129, 300, 517, 1500]) for _ in range(n)]
+    lens[r.randrange(n)] = 1777
+    return lens
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (16, 1), (8, 2)])
+@pytest.mark.parametrize("n", [32, 33, 80])
+def test_prompt_more_sequences_than_a_warp_holds(n, hq, hkv):
+    """Above 32 sequences the claims go by a sorted list: every row of every sequence, on whole and on small grids."""
+    lens = mixed(n, 300 + n)
+    q, k, v, cu = packed(gen(270 + n), lens, hq, hkv, before=1, behind=9)
+    p = pkv.make_prompt(n, q.shape[0], hq, hkv, D, q.stride(0), k.stride(0), v.stride(0))
+    ws = new_ws()
+    whole = None
+    for num_sms in (torch.cuda.get_device_properties(0).multi_processor_count, 5):
+        out = torch.full((q.shape[0], hq, D), 7.0, dtype=torch.float16, device="cuda")
+        rc = pkv.load().pkv_prompt_attention(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), SCALE, num_sms, ws.data_ptr(),
+                                             ws.numel(), out.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and status(ws) == 0
+        assert (out[:1] == 7).all() and (out[-9:] == 7).all()
+        if whole is None:
+            whole = out
+            check_prompt(q, k, v, cu, out)
+        else:
+            assert torch.equal(out, whole)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (16, 2), (16, 1)])
+def test_prompt_longer_with_other_heads(hq, hkv):
+    lens = [2500, 130, 1111]
+    q, k, v, cu = packed(gen(280 + hq), lens, hq, hkv, behind=3)
+    ws = new_ws()
+    out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+    assert status(ws) == 0
+    check_prompt(q, k, v, cu, out)
+
+
+@pytest.mark.parametrize("starts", [False, True])
+@pytest.mark.parametrize("n,hkv", [(33, 2), (70, 1), (70, 3)])
+def test_page_calls_of_more_sequences_than_a_warp_holds(n, hkv, starts):
+    """The warps' items run on from one block of 32 sequences to the next: every token of every sequence is written once, into
+    its slot, and read back from there."""
+    r, g = random.Random(n), gen(290 + n)
+    lens = [r.choice([0, 0, 1, 15, 16, 17, 100, 333]) for _ in range(n)]
+    has = [r.randrange(40) if starts else 0 for _ in range(n)]
+    _, k, v, cu = packed(g, lens, hkv, hkv, before=2, behind=2)
+    bt, pages = table(g, [a + b for a, b in zip(lens, has)])
+    start = ints(has) if starts else None
+    kp, vp = normal(g, pages, PS, hkv, D), normal(g, pages, PS, hkv, D)
+    pool = torch.randint(0, 256, (pages, hkv, ref.BLOCK), dtype=torch.uint8, device="cuda", generator=g)
+    want_k, want_v, want, at = kp.clone(), vp.clone(), pool.clone(), cu.tolist()
+    for b in range(n):
+        rows = slice(at[b], at[b + 1])
+        if lens[b]:
+            pos = torch.arange(lens[b], device="cuda") + has[b]
+            page = bt[b][pos // PS].long()
+            want_k[page, pos % PS], want_v[page, pos % PS] = k[rows], v[rows]
+            ref.put_tokens(want, bt[b], pos, k[rows], v[rows])
+    ws = new_ws()
+    pkv.prompt_append(k, v, cu, kp, vp, bt, start=start, ws=ws)
+    pkv.q4_prompt_append(k, v, cu, pool, bt, start=start, ws=ws)
+    assert status(ws) == 0
+    assert torch.equal(kp, want_k) and torch.equal(vp, want_v) and torch.equal(pool, want)
+    k_out, v_out = (torch.full((k.shape[0], hkv, D), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    pkv.q4_read(cu, pool, bt, start=start, k_out=k_out, v_out=v_out, ws=ws)
+    assert status(ws) == 0
+    for x, y in ((k, k_out), (v, v_out)):
+        w = ref.values(*ref.quantise(x[at[0]:at[-1]]))
+        ref.check(y[at[0]:at[-1]], w, ref.HALF_STEP * w.abs() + 2.0 ** -23 * w.abs() + ref.TINY, "read")
+        assert (y[:at[0]] == 7).all() and (y[at[-1]:] == 7).all()
