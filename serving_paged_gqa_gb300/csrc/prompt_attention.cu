@@ -462,9 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 prefetch_tensormap(&prm.k);
                 prefetch_tensormap(&prm.v);
             }
-            uint64_t keep, stream;
-            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream));
+            // K and V take L2's ordinary policy: kept first (evict_last) they are no faster (2048 tokens 30.1 us, 16384 1.41
+            // ms either way), and the kernels that follow find less of L2 (a copy of 40 MB behind 16384 tokens: 15.5 us
+            // instead of 13.4); evicted first they take 3 % longer.
+            uint64_t ordinary;
+            asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(ordinary));
+            const uint64_t stream = policy_evict_first();
             int seq = 0, nq[2] = {0, 0}, nc = 0;
             bool stop = false;
             for (int k = 0; !stop; ++k) {
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         uint8_t* dst = smem + off_ring + st * kTileBytes;
                         mbar_arrive_expect_tx(bar, kTileBytes);
                         for (int b = 0; b < 2; ++b)
-                            tma_load_3d(dst + b * kBoxBytes, map, b * 64, w.h, w.first + j * kRows, bar, keep);
+                            tma_load_3d(dst + b * kBoxBytes, map, b * 64, w.h, w.first + j * kRows, bar, ordinary);
                     }
                     __syncwarp();
                     ++seq;
