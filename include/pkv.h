@@ -47,7 +47,8 @@ extern "C" {
 #endif
 
 /* 3: serving session (pkv_session_*) and PKV_PLAN_INPUTS_AFTER_PREV; the structs are unchanged from 2. The prompt and
- * 4-bit-cache calls came later; they change nothing that was there. */
+ * 4-bit-cache calls came later; they change nothing that was there, this number included: PKV_Q4_BLOCK_BYTES is defined
+ * where they are declared. */
 #define PKV_VERSION 3
 
 #define PKV_OK 0
@@ -402,8 +403,9 @@ int pkv_decode_step_static(const pkv_plan_t* plan, const pkv_problem* problem, c
  * group) of the parameters, and code c stands for c * scale + offset. offset is the group's least value, scale =
  * fp16((greatest - least) / 15) (the difference and the quotient in fp32, each rounded to nearest even), c =
  * (value - offset) / scale rounded to nearest even and clamped to 0..15 (0 where scale is 0). A group with an infinity
- * or a NaN stands for NaN throughout (both parameters NaN, codes 0). A byte holds one token's dims d (low 4 bits) and
- * d + 64 (high 4 bits), d < 64:
+ * or a NaN stands for NaN throughout (both parameters NaN, codes 0). What code 15 stands for may lie up to 2^-11 of the
+ * group's range above its greatest value, next to 65504 beyond it: read back as FP16 that is an infinity. A byte holds
+ * one token's dims d (low 4 bits) and d + 64 (high 4 bits), d < 64:
  *   K codes, slot r:  byte r * 64 + (d / 2 % 4) * 16 + (d / 16) * 4 + 2 * (d % 2) + d / 8 % 2
  *   V codes, slot r:  byte (r / 8) * 512 + (d % 8) * 64 + (r / 2 % 4) * 16 + (d / 16) * 4 + 2 * (r % 2) + d / 8 % 2
  * (the order in which the decode's matrix instructions take them). A (token, KV head) takes 144 bytes, 512 in FP16.

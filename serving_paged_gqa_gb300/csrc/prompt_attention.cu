@@ -54,9 +54,10 @@
 // values are not finite get what those add up to, and if others are left, the row is computed again from its own
 // keys alone (row_attention). A row whose weights' sum is NaN has a NaN score that it attends to: it stays NaN.
 //
-// Bound: the tensor core and the paths of its operands. Measured on a GB300 (32 query heads, 8 KV heads): 16384 tokens
-// 1.37 ms, 1600 TFLOP/s (0.83 of the measured cuBLAS burst, 0.93 of its sustained rate under the power cap); 2048 tokens
-// 30.5 us; one prompt of 17 tokens 6.3 us. The tensor pipe is active 68 % of the time at 4096 tokens.
+// Bound: the tensor core and the paths of its operands. Measured on GB300s (32 query heads, 8 KV heads): 16384 tokens
+// 1.34-1.47 ms, 1500-1640 TFLOP/s as the power cap of the GPU at hand allows (0.78-0.86 of the measured cuBLAS burst,
+// 0.87-0.95 of its sustained rate); 2048 tokens 30-32 us; one prompt of 17 tokens 6.3 us. The tensor pipe is active 69 %
+// of the time at 4096 tokens.
 //
 // Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
 // have in flight, and the CTA frees its TMEM and returns. The limit grows with the prompt: a warp may finish 32 rows from

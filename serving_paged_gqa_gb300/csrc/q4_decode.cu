@@ -14,7 +14,7 @@
 // Bound: HBM; a (token, KV head) is 144 bytes against 512 in fp16. A unit is 4 pages (64 tokens) of one (row, KV head),
 // four bulk copies of 2304 bytes into one ring stage, and goes to one consumer warp. Measured on a GB300 (G = 4): 48 rows
 // of 900-32768 tokens, 765 MB, 143 us: 5.4 TB/s, 0.80 of the copy bandwidth; copies alone 125 us, arithmetic alone
-// 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.8 us.
+// 120 us; eight rows, 154 MB, 37 us; one row of 512 tokens 8.8 us (from L2 7.9).
 // Division: the units of all (row, KV head) pairs form one line, and each CTA takes an equal piece of it, whatever the
 // rows' lengths; every CTA finds its piece itself from a scan of seq_lens, so there is no plan. A pair that lies in one
 // piece is written out at once. The others leave a state (m, l, accumulator) per piece, and the last of a pair's
@@ -46,8 +46,11 @@ constexpr uint32_t kAllPages = (1u << kUnitPages) - 1u;
 // Arrival counters behind the workspace's header, one a piece. They are zero between steps, so they lie where no step of
 // other heads or of a grid of another size puts its states: their place and number depend on nothing.
 constexpr int kMaxPieces = 2 * 4 * kCombRow;
-// Units per CTA below which fewer CTAs take part: two a consumer warp. A row of 512 tokens (8 units a KV head) takes 8.4 us
-// with 8, and 9.7 with 4 (two pieces a pair, and their merge) or 12.4 with 12.
+// Units per CTA below which fewer CTAs take part: with fewer, short rows are spread wider and more states are merged. Batches
+// of one to eight rows of 40 to 32768 tokens, geometric mean of 24 at (query heads, KV heads) of (8, 8), (32, 8), (32, 4),
+// (16, 1), pages in L2, in us: 4 units 10.1, 10.8, 12.6, 13.4; 8 units 11.3, 11.9, 12.6, 14.6; but one row of 32768 takes
+// 16.2, 17.4, 22, 29 with 4 and 16.2, 17.2, 19, 23 with 8. (Pieces that are whole pairs need no merge: 512 tokens of 8 KV
+// heads 7.9 with 8, 8.8 with 4; 300 tokens 12.1 and 11.7.)
 constexpr int kMinUnits = 8;
 
 // A piece's part of one (row, KV head) pair.
@@ -61,8 +64,8 @@ struct Segment {
 
 // Consumers, stages, partial-result buffers, resident CTAs. Two CTAs an SM share its registers (four consumers of up to 168)
 // and its shared memory (8 units of 9 KB in flight each); at G = 16 the query fragments and accumulators of one CTA's
-// consumers take more than half. With 6 consumers of 128 registers and units of 3 pages a CTA the 48-row step takes 148 us
-// instead of 141.
+// consumers take more than half. With 6 consumers of 128 registers and units of 3 pages a CTA the 48-row step took 148 us
+// when this shape took 141.
 template <int G>
 struct Shape {
     static constexpr int NC = G >= 16 ? 6 : 4;

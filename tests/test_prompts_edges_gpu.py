@@ -70,6 +70,37 @@ def test_prompt_many_tiles_that_end_in_a_first_half(num_sms, hq, hkv):
         check_prompt(q, k, v, cu, out, what=f"call {call}")
 
 
+@pytest.mark.parametrize("variant", [pkv.PKV_VARIANT_WORKQUEUE, pkv.PKV_VARIANT_SPLIT])
+def test_prompt_calls_on_the_workspaces_of_decode_steps(variant):
+    """The prompt calls use a workspace's header alone, and leave it as they found it: on the workspace of an FP16 step, and of
+    a 4-bit one, between steps."""
+    g, hq, hkv, lens = gen(205), 8, 2, [900, 40, 1300]
+    q, k, v, cu = packed(g, lens, hq, hkv, fused=False)
+    bt, pages = table(g, lens)
+    kp, vp = (torch.zeros((pages, PS, hkv, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    pool = torch.zeros((pages, hkv, ref.BLOCK), dtype=torch.uint8, device="cuda")
+    qt, n = normal(g, 3, hq, D), ints(lens)
+    problem = pkv.make_problem(3, hq, hkv, D, PS, pages, bt.shape[1])
+    plan = pkv.pkv_plan_fixed(problem, lens, torch.cuda.get_device_properties(0).multi_processor_count, variant, 8)
+    wide, four = new_ws(plan.ws_bytes), new_ws(pkv.pkv_q4_workspace_bytes(problem))
+    for call in range(3):
+        for ws in (wide, four):
+            out = pkv.prompt_attention(q, k, v, cu, ws=ws)
+            check_prompt(q, k, v, cu, out, what=f"call {call}")
+            pkv.prompt_append(k, v, cu, kp, vp, bt, ws=ws)
+            pkv.q4_prompt_append(k, v, cu, pool, bt, ws=ws)
+        out, out4 = torch.full_like(qt, math.nan), torch.full_like(qt, math.nan)
+        pkv.pkv_decode_step(plan, problem, qt, kp, vp, bt, n, SCALE, wide, out)
+        pkv.q4_decode(qt, pool, bt, n, out=out4, ws=four)
+        assert status(wide) == 0 and status(four) == 0
+        check_q4(qt, pool, bt, lens, out4, what=f"call {call}")
+        at = cu.tolist()
+        for b in range(3):
+            rows = slice(at[b], at[b + 1])
+            w, mag = ref.attend(qt[b:b + 1], k[rows], v[rows], SCALE, lens[b] - 1)
+            ref.check(out[b:b + 1], w, ref.prompt_bound(w, mag, lens[b], qt[b:b + 1], k[rows], v[rows], SCALE), f"row {b}")
+
+
 # ----------------------------------------------------------------------------------------------- small softmax weights
 @pytest.mark.parametrize("n,hq,hkv", [(3000, 8, 2), (16384, 4, 4)])
 @pytest.mark.parametrize("nats", [10.0, 14.0, 16.0, 18.0])
