@@ -787,9 +787,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     ref = *ref_at;
                 }
                 float sum = weights();
-                // (A row without a finite score has no reference, and asks for one when a key has a weight. One whose scores
-                // are NaN, such as those of garbage behind the sequence's end, never does: it would do so in every step.)
-                const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, sum > (ref == -INFINITY ? 0.f : kMost));
+                // (A row without a finite score has no reference yet, and asks for one. One whose scores are NaN, such as those
+                // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
+                const bool ask = ref == -INFINITY ? !isnan(sum) : sum > kMost;
+                const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, ask);
                 if (h == 0 && raise) {
                     // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
                     float f2 = 1.f;

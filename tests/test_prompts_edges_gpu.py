@@ -252,6 +252,28 @@ def test_prompt_rows_computed_again_for_longer_than_a_wait_may_take():
         ref.check(out[a:a + 127], w, ref.prompt_bound(w, mag, a + 127, q[a:a + 127], k[:a + 127], v[:a + 127], SCALE), f"rows {a}..")
 
 
+@pytest.mark.parametrize("near,far", [(-125.5, -130.0), (-140.0, -145.0), (-125.0, -160.0), (-700.0, -701.0), (-3.0, -9.0)])
+def test_prompt_scores_far_below_zero_behind_minus_infinity(near, far):
+    """Behind first keys of -inf the first finite scores (in log2) are the row's reference, however far below 0 they are:
+    2^x of them may be nothing in fp32."""
+    n, first, then = 330, 64, 200
+    q, k, v, cu = packed(gen(252), [n], 8, 2, fused=False)
+    unit = 1.0 / (16.0 * SCALE * math.log2(math.e))
+    q.zero_()
+    k.zero_()
+    q[:, :, 0] = 16.0
+    k[first:then, :, 0], k[then:, :, 0] = far * unit, near * unit
+    kb = k.clone()
+    kb[:first, :, 0] = -math.inf
+    ws = new_ws()
+    out = pkv.prompt_attention(q, kb, v, cu, ws=ws)
+    assert status(ws) == 0
+    assert torch.isnan(out[:first]).all()
+    k, v, q, out = k[first:], v[first:], q[first:], out[first:]
+    w, mag = ref.attend(q, k, v, SCALE, 0)
+    ref.check(out, w, ref.prompt_bound(w, mag, n - first, q, k, v, SCALE))
+
+
 # -------------------------------------------------------------------------------------------- many sequences, other heads
 def mixed(n, seed):
     """Lengths of n sequences, empty ones and of one to a dozen pairs of tiles (at 16 heads to a KV head, a hundred) among
