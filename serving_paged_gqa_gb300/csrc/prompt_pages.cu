@@ -4,10 +4,10 @@
 // quantises: nothing is full there (ALU 56 %, issue 59 %, HBM 60 %), a warp has no load in flight while it quantises, and
 // its longest stall is on its loads. Measured on a GB300, 8 KV heads: FP16 append of 17k tokens 25 us, 5.7 TB/s; 4-bit
 // append of 50k tokens 65 us, 4.0 TB/s (0.60 of the copy bandwidth; 980 instructions for the K or V of a page and KV
-// head); read-back 48 us, 5.4 TB/s; a few tokens 7.5 and 4.7 us. Warps are the unit of work: a token for the FP16 pages, the K or V of a (page, KV head) for
-// the 4-bit append, a (page, KV head) for the read-back. All warps of the grid share the items of all sequences evenly,
-// whatever their lengths: each warp looks at 32 sequences at a time (a lane each), scans their item counts, and takes
-// every W-th item of the running line (W = warps of the grid).
+// head); read-back 48 us, 5.4 TB/s; a few tokens 7.5 and 4.7 us. Warps are the unit of work: a token for the FP16
+// pages, the K or V of a (page, KV head) for the 4-bit append, a (page, KV head) for the read-back. All warps of the
+// grid share the items of all sequences evenly, whatever their lengths: each warp looks at 32 sequences at a time (a
+// lane each), scans their item counts, and takes every W-th item of the running line (W = warps of the grid).
 #include <cuda_fp16.h>
 
 #include <algorithm>
