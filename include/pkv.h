@@ -506,6 +506,35 @@ int pkv_q4_decode_step_append(const pkv_problem* problem, const void* q, const v
                               void* pool, const int32_t* block_table, const int32_t* seq_lens_dev, float scale,
                               int32_t num_sms, void* ws, size_t ws_bytes, void* out, void* stream);
 
+/* ---- chunks, tables and selected pages ------------------------------------------------------------------------------
+ * The paper decodes one token a row over pages that are all read. The calls below serve a cache that grows by chunks of
+ * tokens and is read in part: attention of new tokens over the pages, the tables that say where tokens go, and a decode
+ * step over the pages that promise the greatest scores. Packed new tokens (cu_seqlens, strides) are as for the prompt
+ * calls, and so are num_sms and the rules on workspaces; these calls keep nothing in a workspace between calls but the
+ * status word, so any that is large enough may serve them in turn.
+ */
+
+/* Bytes of the workspace of pkv_chunk_attention on a GPU of num_sms SMs: it depends on nothing else. Host only. */
+int pkv_chunk_workspace_bytes(int32_t num_sms, size_t* bytes);
+
+/*
+ * Attention of packed new tokens over the FP16 pages: token i of sequence s stands at position start[s] + i of row s
+ * (start [num_seqs] int32, NULL = 0), and out = softmax(scale * q . k_j over the positions j <= start[s] + i) V, with k_j and
+ * v_j in slot j % 16 of page block_table[s][j / 16]. The pages hold the new tokens' K and V already (pkv_prompt_append with
+ * the same cu_seqlens and start). One token or many a sequence: a chunk of a long prompt, a prompt behind a cached prefix
+ * (rows may share pages), the verification of proposed tokens. 0 <= scale <= 1e12. problem->batch must equal
+ * prompt->num_seqs and the heads must agree; k_stride and v_stride of prompt do not matter beyond pkv_check_prompt.
+ * Slots behind a row's last token may hold anything. Infinities and NaN of K and V reach the rows that attend to them alone,
+ * as for pkv_prompt_attention. The division of the work over the GPU is worked out on the device: one captured graph
+ * serves every step of a batch. out must not overlap q or the pools (the same address is refused).
+ * A sequence whose bounds are not ordered inside [0, total_tokens], or that would outgrow its block table, raises
+ * PKV_STATUS_BAD_LEN and is skipped; a block-table entry outside the pool raises PKV_STATUS_BAD_PAGE and counts as a page
+ * whose K and V are 0.
+ */
+int pkv_chunk_attention(const pkv_problem* problem, const pkv_prompt* prompt, const void* q, const void* k_pool,
+                        const void* v_pool, const int32_t* cu_seqlens, const int32_t* start, const int32_t* block_table,
+                        float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

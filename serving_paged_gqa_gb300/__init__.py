@@ -22,3 +22,4 @@ from .prompts import (make_prompt, pkv_check_prompt, pkv_prompt_append, pkv_prom
                       pkv_q4_decode_step, pkv_q4_decode_step_append, pkv_q4_pool_bytes, pkv_q4_prompt_append, pkv_q4_read,
                       pkv_q4_workspace_bytes, prompt_append, prompt_attention, q4_decode, q4_problem, q4_prompt_append,
                       q4_read)
+from .paged import chunk_attention, pkv_chunk_attention, pkv_chunk_workspace_bytes  # noqa: F401

@@ -44,6 +44,7 @@ EXPORTS = (
     "pkv_serve_step", "pkv_session_create", "pkv_session_step", "pkv_session_stats", "pkv_session_destroy",
     "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append", "pkv_q4_read",
     "pkv_q4_pool_bytes", "pkv_q4_workspace_bytes", "pkv_q4_decode_step", "pkv_q4_decode_step_append",
+    "pkv_chunk_workspace_bytes", "pkv_chunk_attention",
 )
 
 PKV_SESSION_GRAPHS = 16
@@ -172,7 +173,9 @@ def load(path: str | None = None):
                 ("pkv_q4_pool_bytes", [_P(Problem), _P(size)]),
                 ("pkv_q4_workspace_bytes", [_P(Problem), i32, _P(size)]),
                 ("pkv_q4_decode_step", [_P(Problem), _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
-                ("pkv_q4_decode_step_append", [_P(Problem), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp])):
+                ("pkv_q4_decode_step_append", [_P(Problem), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
+                ("pkv_chunk_workspace_bytes", [i32, _P(size)]),
+                ("pkv_chunk_attention", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = args
         _lib = lib

@@ -1,0 +1,1199 @@
+// Attention of packed new tokens over the FP16 pages that hold them and their sequences' earlier tokens (include/pkv.h,
+// pkv_chunk_attention), and of one token a row over selected pages (pkv_sparse_decode_step).
+//
+// For token i of a sequence (position start + i) and query head hq of KV head h: out = sum_j p_j v_j / sum_j p_j over the
+// positions j <= start + i, p_j = 2^(x_j - ref), x_j = scale * log2(e) * q_i.k_j. Products on the 5th-generation tensor
+// cores, tiles of 128 rows = 128 / G tokens x G heads, two tiles (A, B: a pair) a CTA at a time over 128 keys a step,
+// warp roles, references and precision as in prompt_attention.cu; what differs is where keys come from and who does what.
+//
+// Keys: a step is 8 pages of 16 tokens. A page of one KV head is two TMA boxes (64 dims x 16 tokens) for K and two for V;
+// boxes of consecutive pages lie one behind the other in a stage, which gives the same operand layout as one box of 128
+// rows. Block-table entries are read 32 at a time ahead of their use. An entry outside the pool becomes a coordinate
+// outside the tensor: the copy brings zeros.
+//
+// Division: a pair of tiles of one (sequence, KV head) has as many steps as its last token has keys. Neither one long
+// context with a few new tokens (one pair a KV head) nor a batch of unequal ones fills the GPU pair by pair, so the steps
+// of all pairs form one line, in the order (sequence, KV heads, pair, step), and it is cut into equal pieces wherever the
+// cuts fall. A piece belongs to `lanes` CTAs, one for each of `lanes` neighbouring KV heads, so that they read the same
+// pages at the same time (a token's heads are contiguous in a page). Every CTA finds its piece from a scan of the
+// sequences' lengths; there is no plan, and one captured graph serves every step. A pair that lies in one piece is
+// written out at once. The others leave a state a piece (ref, sum, accumulator, in fp32; a CTA leaves two at most), and a
+// second kernel, launched to overlap this one's end, adds them up in the order of the pieces.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "pkv_internal.h"
+#include "pkv_launch.h"
+#include "pkv_tcgen05.cuh"
+#include "pkv_tensormap.h"
+#include "pkv_wait.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr uint64_t kFinishNs = 32 * 1000;    // a warp's 32 rows, by the key that they are computed from again, at most
+constexpr uint64_t kFinishMostNs = 30000000000ull;  // (a million keys)
+constexpr int kRows = 128;                   // rows of a tile, keys of a step
+constexpr int kStepPages = kRows / kPageSize;
+constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two halves of 64 dims
+constexpr int kBoxBytes = kTileBytes / 2;
+constexpr int kPageBox = kPageSize * 128;    // one page's part of a half
+constexpr int kStages = 4;
+constexpr int kSoftmax = 512;                // threads of the softmax
+constexpr int kThreads = kSoftmax + 128;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96, what the launch has
+constexpr float kMost = 65504.f;             // sum of 64 weights above which the row's reference is raised
+constexpr float kLift = 5.f;                 // the largest weight where the reference was set, in powers of two
+constexpr int kMinSteps = 2;                 // steps a piece has at least
+
+// One sequence: its first packed row, its new tokens, and how many it holds before them.
+struct Seq {
+    int32_t first, n, start;
+};
+
+struct Work {
+    Seq q;
+    int32_t s, t0, h;  // sequence; first new token of tile A; KV head (-1: no more work)
+    int32_t j0, j1;    // steps of this piece
+    int32_t state;     // -1: the whole pair, written to out; else the state that it leaves
+};
+
+// A pair whose states are to be added up: `pieces` of them, the first in slot 2 cta + 1 of the CTA that has this entry, the
+// others in slots 2 (cta + i lanes).
+struct Merge {
+    Seq q;
+    int32_t s, t0, h, pieces, reserved;
+};
+static_assert(sizeof(Merge) == kChunkMergeBytes, "workspace layout");
+
+constexpr int off_q = 0;
+constexpr int off_ring = 2 * kTileBytes;
+constexpr int off_work = off_ring + kStages * kTileBytes;
+constexpr int off_bars = off_work + (int)sizeof(Work) + 8 - sizeof(Work) % 8;
+constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 2 + 1;
+constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
+constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
+constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
+constexpr int off_scan = off_late + 8 * 4;               // int64 [warp]: steps of the sequences of a warp's threads
+constexpr int off_begin = off_scan + kThreads / 32 * 8;  // int64, int32: where the piece begins
+constexpr int off_misc = off_begin + 16;                 // abort flag, TMEM address
+constexpr int kSmem = off_misc + 16 + 1024;              // slack to align the base to 1024 bytes
+static_assert(off_bars % 8 == 0 && off_parts % 8 == 0 && off_scan % 8 == 0, "alignment");
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Params {
+    CUtensorMap q, k, v;
+    ChunkParams p;
+};
+
+// ---- sequences, pairs of tiles and their steps ---------------------------------------------------------------------
+// Sequence s; nothing (n = 0) where its bounds or lengths are not inside the tensors.
+__device__ __forceinline__ Seq load_seq(const ChunkParams& p, int s, bool& bad) {
+    Seq q;
+    if (p.seq_lens) {  // one token a row, behind the keys of its selected pages; the last of them ends with the row
+        const int len = p.seq_lens[s];
+        bad = len < 0 || len > (int64_t)p.max_pages * kPageSize;
+        q.first = s;
+        q.n = bad || len == 0 ? 0 : 1;
+        q.start = (min((len + kPageSize - 1) / kPageSize, p.select) - 1) * kPageSize + (len - 1) % kPageSize;
+    } else {
+        q.first = p.cu_seqlens[s];
+        const int last = p.cu_seqlens[s + 1];
+        q.start = p.start ? p.start[s] : 0;
+        bad = q.first < 0 || last < q.first || last > p.total_tokens || q.start < 0 ||
+              (int64_t)q.start + (last - q.first) > (int64_t)p.max_pages * kPageSize;
+        q.n = bad ? 0 : last - q.first;
+    }
+    if (q.n == 0) q.start = 0;
+    return q;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }
+
+template <int G>
+__device__ __forceinline__ int pairs_of(const Seq& q) {
+    return ceil_div(q.n, 2 * kRows / G);
+}
+
+// Keys of the pair that begins at new token t0: those up to its last token.
+template <int G>
+__device__ __forceinline__ int keys_of(const Seq& q, int t0) {
+    return q.start + (int)min((int64_t)q.n, (int64_t)t0 + 2 * kRows / G);
+}
+
+// Steps of the first m pairs, all of them whole: sum over i = 1..m of ceil((start + i T) / 128), T = 256 / G tokens. For G
+// > 1 that is ceil((c + i) / r) with c = ceil(start / T), r = 128 / T.
+template <int G>
+__device__ __forceinline__ int64_t steps_before(const Seq& q, int m) {
+    constexpr int T = 2 * kRows / G;
+    if constexpr (T > kRows) {
+        return (int64_t)m * ceil_div(q.start, kRows) + (int64_t)m * (m + 1);
+    } else {
+        constexpr int r = kRows / T;
+        const int64_t c = ceil_div(q.start, T);
+        auto upto = [](int64_t x) {  // sum over i = 1..x of ceil(i / r)
+            const int64_t a = x / r, b = x % r;
+            return r * (a * (a + 1) / 2) + b * (a + 1);
+        };
+        return upto(c + m) - upto(c);
+    }
+}
+
+template <int G>
+__device__ __forceinline__ int64_t steps_of(const Seq& q) {  // of one KV head
+    const int m = pairs_of<G>(q);
+    return m == 0 ? 0 : steps_before<G>(q, m - 1) + ceil_div(q.start + q.n, kRows);
+}
+
+// Keys of tile x (0: A, 1: B) of a pair; 0: it has no rows.
+__device__ __forceinline__ int tile_end(const Work& w, int x, int tokens) {
+    const int t = w.t0 + x * tokens;
+    return t < w.q.n ? w.q.start + min(t + tokens, w.q.n) : 0;
+}
+
+// Piece of the line of `total` steps that step u lies in; piece i begins at i * total / pieces.
+__device__ __forceinline__ int piece_of(int64_t u, int64_t total, int pieces) {
+    return (int)(((u + 1) * pieces + total - 1) / total) - 1;
+}
+
+// The pool's page that holds the keys 16 lp .. of row s (for KV head h, where the row's pages are selected ones); num_pages
+// where there is none.
+__device__ __forceinline__ int page_of(const ChunkParams& p, int s, int h, int lp) {
+    if (p.pages) {
+        lp = p.pages[((int64_t)s * p.Hkv + h) * p.select + lp];
+        if (lp < 0 || lp >= p.max_pages) return p.num_pages;
+    }
+    const int e = p.block_table[(int64_t)s * p.max_pages + lp];
+    return e >= 0 && e < p.num_pages ? e : p.num_pages;
+}
+
+// ---- rows on the CUDA cores ----------------------------------------------------------------------------------------
+struct Row4 {
+    float x[4];
+};
+
+__device__ __forceinline__ uint2 load4(const __half* p) { return *reinterpret_cast<const uint2*>(p); }
+
+__device__ __forceinline__ Row4 floats4(const uint2& u) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return Row4{{a.x, a.y, b.x, b.y}};
+}
+
+// The reference for a largest score. Scores of which an fp32 has no fractions are it themselves: nothing is then added to
+// their rounding.
+__device__ __forceinline__ float ref_for(float top) { return fabsf(top) < 16777216.f ? top - kLift : top; }
+
+// One warp, one (token, query head): online softmax over the keys 0..pos of its sequence, 4 at a time; lane l holds dims
+// 4l..4l+3. Stores dims 64 half .. + 63. Factors of the numerator stay at 2^-126 or above, which is nothing to finite values,
+// and keeps infinities of V that no weight is too small for: 0 times one would be NaN.
+__device__ __forceinline__ void row_attention(const ChunkParams& p, const Seq& sq, int s, int t, int hq, int half, int lane) {
+    constexpr int kKeys = 4;
+    constexpr float kLeast = 0x1p-126f;
+    const int h = hq / (p.Hq / p.Hkv), pos = sq.start + t;
+    const int64_t token = (int64_t)p.Hkv * kHeadDim;
+    const int64_t at = h * kHeadDim + lane * 4;
+    const Row4 q = floats4(load4(static_cast<const __half*>(p.q) + (int64_t)(sq.first + t) * p.q_stride + hq * kHeadDim + lane * 4));
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j <= pos; j += kKeys) {
+        const int page = page_of(p, s, h, j / kPageSize);
+        const int64_t row = ((int64_t)page * kPageSize + j % kPageSize) * token + at;
+        uint2 a[kKeys], b[kKeys];
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            a[i] = b[i] = make_uint2(0u, 0u);
+            if (page < p.num_pages && j + i <= pos) {
+                a[i] = load4(static_cast<const __half*>(p.k_pool) + row + i * token);
+                b[i] = load4(static_cast<const __half*>(p.v_pool) + row + i * token);
+            }
+        }
+        float x[kKeys];
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const Row4 y = floats4(a[i]);
+            x[i] = q.x[0] * y.x[0] + q.x[1] * y.x[1] + q.x[2] * y.x[2] + q.x[3] * y.x[3];
+        }
+#pragma unroll
+        for (int z = 16; z > 0; z >>= 1)
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], z);
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            x[i] = j + i <= pos ? x[i] * p.scale_log2 : -INFINITY;
+            mn = fmaxf(mn, x[i]);
+        }
+        const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref);
+        l *= f;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) o[z] *= fmaxf(f, kLeast);
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+            if (j + i <= pos) {
+                const float e = exp2f(x[i] - ref);
+                const Row4 y = floats4(b[i]);
+                l += e;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) o[z] += fmaxf(e, kLeast) * y.x[z];
+            }
+        m = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : NAN;  // NaN: a score is, or all of them are -inf
+    uint2 u;
+    u.x = pack_half2(o[0] * inv, o[1] * inv);
+    u.y = pack_half2(o[2] * inv, o[3] * inv);
+    if (lane >> 4 == half)
+        *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (int64_t)(sq.first + t) * p.out_stride + hq * kHeadDim + lane * 4) = u;
+}
+
+// One warp; rows: a bit for each of its 32 rows (row r is head h * G + r % G of new token t0 + r / G of the sequence) whose
+// tensor-core result, dims 64 half .. + 63 of it in out, is not finite, redo: those among them that are wrong for
+// certain. Lane l looks at dims 2l, 2l + 1. Infinities of V that the row attends to add up to an infinity, of both signs (or
+// with a NaN) to a NaN, whatever their weights; a row that has other dims that are not finite is computed again.
+template <int G>
+__device__ __noinline__ void finish_rows(const ChunkParams& p, const Seq& sq, int s, int t0, int h, int half, uint32_t rows,
+                                         uint32_t redo) {
+    const int lane = threadIdx.x & 31;
+    const int64_t token = (int64_t)p.Hkv * kHeadDim;
+    const __half* v = static_cast<const __half*>(p.v_pool) + h * kHeadDim + half * 64 + lane * 2;
+    __half2 top = __float2half2_rn(0.f), low = top, nan = top;  // of the values of the keys before `keys`
+    int keys = 0;
+    for (; rows; rows &= rows - 1) {  // in the order of their tokens
+        const int r = __ffs(rows) - 1, pos = sq.start + t0 + r / G;
+        if ((redo >> r) & 1) continue;
+        while (keys <= pos) {
+            const int page = page_of(p, s, h, keys / kPageSize), lim = min(pos + 1, (keys | (kPageSize - 1)) + 1);
+            if (page == p.num_pages) {
+                keys = lim;
+                continue;
+            }
+            const __half* at = v + (int64_t)page * kPageSize * token;
+#pragma unroll 16
+            for (; keys < lim; ++keys) {
+                const __half2 x = *reinterpret_cast<const __half2*>(at + (keys % kPageSize) * token);
+                top = __hmax2(top, x);
+                low = __hmin2(low, x);
+                nan = __hmax2_nan(nan, x);
+            }
+        }
+        const uint32_t t = *reinterpret_cast<const uint32_t*>(&top), w = *reinterpret_cast<const uint32_t*>(&low),
+                       n = *reinterpret_cast<const uint32_t*>(&nan);
+        uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<__half*>(p.out) + (int64_t)(sq.first + t0 + r / G) * p.out_stride +
+                                                   (h * G + r % G) * kHeadDim + half * 64 + lane * 2);
+        uint32_t y = *at;
+        bool other = false;
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+            const bool up = ((t >> i) & 0xffffu) == 0x7c00u, down = ((w >> i) & 0xffffu) == 0xfc00u;
+            const bool any = ((n >> i) & 0x7fffu) > 0x7c00u;
+            if (any || up || down)
+                y = (y & ~(0xffffu << i)) | (any || (up && down) ? 0x7fffu : up ? 0x7c00u : 0xfc00u) << i;
+            else
+                other = other || ((y >> i) & 0x7c00u) == 0x7c00u;
+        }
+        *at = y;
+        if (__any_sync(0xffffffffu, other)) redo |= 1u << r;
+    }
+    for (; redo; redo &= redo - 1) {
+        const int r = __ffs(redo) - 1;
+        row_attention(p, sq, s, t0 + r / G, h * G + r % G, half, lane);
+    }
+}
+
+// ---- the tensor-core kernel ---------------------------------------------------------------------------------------
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params prm) {
+    constexpr int kTokens = kRows / G;  // tokens of a tile
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const ChunkParams& p = prm.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + off_bars);
+    uint64_t* kv_empty = kv_full + kStages;
+    uint64_t* w_full = kv_empty + kStages;  // the CTA's next work has been published
+    uint64_t* w_empty = w_full + 1;         // every warp has taken it
+    uint64_t* q_full = w_empty + 1;       // [2], like those below: tile A, tile B
+    uint64_t* q_empty = q_full + 2;
+    uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
+    uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
+    uint64_t* o_full = p_full + 4;        // its accumulator is complete
+    uint64_t* lo_done = o_full + 2;       // the products of a step's first 64 keys are in the accumulator
+    uint64_t* o_free = lo_done + 2;       // the accumulator has been read
+    uint64_t* first_ref = o_free + 2;     // [tile][warp of the half]: the tile's first references are in shared memory
+    uint64_t* half_done = first_ref + 8;  // [tile][warp of the half]: the second half has settled its weights of the step
+    uint64_t* tail_full = half_done + 8;  // [2]: a tile of V with rows behind the pair's last key has come
+    uint64_t* drain = tail_full + 2;
+    Work* work = reinterpret_cast<Work*>(smem + off_work);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + off_scan);
+    int64_t* begin_off = reinterpret_cast<int64_t*>(smem + off_begin);
+    int32_t* begin_seq = reinterpret_cast<int32_t*>(smem + off_begin + 8);
+    const WaitCtx ctx{abort_flag, &p.hdr->status, p.wait_ns};
+
+    grid_launch_dependents();
+    // The line of steps: every thread sums a run of sequences (the first one's bounds are on their way while the barriers are
+    // set up), the CTA scans the sums, and the thread whose run holds the piece's first step finds its sequence.
+    const int per = ceil_div(p.num_seqs, kThreads);
+    const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
+    bool bad = false;
+    Seq sq0{0, 0, 0};
+    if (s0 < s1) sq0 = load_seq(p, s0, bad);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(w_full, 1);
+        mbar_init(w_empty, kSoftmax / 32 + 3);  // and warps 16, 17, 19
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[2 * i], 4);  // one arrival a warp
+            mbar_init(&p_full[2 * i + 1], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&lo_done[i], 1);
+            mbar_init(&o_free[i], 8);
+            mbar_init(&tail_full[i], 1);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&first_ref[i], 1);
+            mbar_init(&half_done[i], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 16) tmem_alloc(tmem_at, 512);
+    int64_t mine = s0 < s1 ? steps_of<G>(sq0) : 0;
+    for (int s = s0 + 1; s < s1; ++s) {
+        bool b;
+        mine += steps_of<G>(load_seq(p, s, b));
+        bad |= b;
+    }
+    if (bad && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
+    const int64_t head_groups = p.Hkv / p.lanes;
+    mine *= head_groups;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+    int64_t before = incl - mine, total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += scan[i];
+        total += scan[i];
+    }
+    const int group = blockIdx.x / p.lanes;
+    const int pieces = (int)min((int64_t)(gridDim.x / p.lanes), (total + kMinSteps - 1) / kMinSteps);
+    const int64_t lo = group < pieces ? group * total / pieces : 0, hi = group < pieces ? (group + 1) * total / pieces : 0;
+    if (lo < hi && before <= lo && lo < before + mine) {
+        int64_t at = before;
+        for (int s = s0; s < s1; ++s) {
+            bool b;
+            const int64_t n = steps_of<G>(s == s0 ? sq0 : load_seq(p, s, b)) * head_groups;
+            if (lo < at + n) {
+                *begin_seq = s;
+                *begin_off = lo - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    if (p.seq_lens) {  // rows without a token get 0
+        for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+            bool b;
+            if (load_seq(p, s, b).n == 0)
+                for (int i = threadIdx.x; i < p.Hq * 16; i += kThreads)
+                    reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + (int64_t)s * p.out_stride)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __syncthreads();
+
+    if (warp >= kSoftmax / 32) {
+        regs_shrink<kOtherRegs>();
+        if (warp == 18) {
+            // ---------------------------------------------------------------------- the piece, pair after pair
+            auto publish = [&](int k, const Work& w) {
+                if (k > 0 && !warp_wait(w_empty, (k - 1) & 1, ctx)) return false;
+                if (lane == 0) {
+                    *work = w;
+                    mbar_arrive(w_full);
+                }
+                __syncwarp();
+                return true;
+            };
+            Merge merge{};
+            int k = 0;
+            bool ok = true;
+            if (lo < hi) {
+                bool b;
+                int s = *begin_seq;
+                Seq q = load_seq(p, s, b);
+                int64_t of_head = steps_of<G>(q);
+                int hg = (int)(*begin_off / of_head);
+                const int64_t rest = *begin_off - hg * of_head;
+                int left = 0, right = pairs_of<G>(q) - 1;  // the last pair that begins at or before `rest`
+                while (left < right) {
+                    const int mid = (left + right + 1) >> 1;
+                    if (steps_before<G>(q, mid) <= rest)
+                        left = mid;
+                    else
+                        right = mid - 1;
+                }
+                int pair = left, j = (int)(rest - steps_before<G>(q, pair));
+                for (int64_t pos = lo; pos < hi; ++k) {
+                    Work w;
+                    w.q = q;
+                    w.s = s;
+                    w.t0 = pair * 2 * kTokens;
+                    w.h = hg * p.lanes + (int)(blockIdx.x % p.lanes);
+                    const int steps = ceil_div(keys_of<G>(q, w.t0), kRows);
+                    w.j0 = j;
+                    w.j1 = (int)min((int64_t)steps, j + (hi - pos));
+                    if (w.j1 <= w.j0) break;  // (only where the lengths change under the kernel, like the one below)
+                    const bool whole = w.j0 == 0 && w.j1 == steps;
+                    w.state = whole ? -1 : 2 * (int)blockIdx.x + (j == 0);
+                    if (!whole && j == 0) merge = Merge{q, s, w.t0, w.h, piece_of(pos + steps - 1, total, pieces) - group + 1, 0};
+                    ok = publish(k, w);
+                    if (!ok) break;
+                    pos += w.j1 - w.j0;
+                    j = 0;
+                    if (++pair == pairs_of<G>(q)) {
+                        pair = 0;
+                        if (++hg == head_groups) {
+                            hg = 0;
+                            do {
+                                if (++s >= p.num_seqs) break;
+                                q = load_seq(p, s, b);
+                            } while (q.n == 0);
+                            if (s >= p.num_seqs) {
+                                ++k;
+                                break;
+                            }
+                        }
+                    }
+                }
+            }
+            if (ok) {
+                Work w{};
+                w.h = -1;
+                publish(k, w);
+            }
+            if (lane == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = merge;
+        } else if (warp == 17) {
+            // ------------------------------------------------------------------------------------- copies
+            if (lane == 0) {
+                prefetch_tensormap(&prm.q);
+                prefetch_tensormap(&prm.k);
+                prefetch_tensormap(&prm.v);
+            }
+            uint64_t ordinary;
+            asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(ordinary));
+            const uint64_t stream = policy_evict_first();
+            int seq = 0, nq[2] = {0, 0}, nc = 0;
+            bool stop = false;
+            for (int k = 0; !stop; ++k) {
+                if (!warp_wait(w_full, k & 1, ctx)) break;
+                const Work w = *work;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_empty);
+                if (w.h < 0) break;
+                const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
+                const int npages = ceil_div(end, kPageSize);
+                auto entries = [&](int lp) {  // a lane's page among 32; where the pair has no more, any
+                    const int page = lp < npages ? page_of(p, w.s, w.h, lp) : 0;
+                    return page;
+                };
+                int next = entries(w.j0 * kStepPages + lane), ent = 0;
+                auto load_q = [&](int x) {
+                    if (tile_end(w, x, kTokens) <= w.j0 * kRows) return true;
+                    if (!warp_wait(&q_empty[x], (nq[x] & 1) ^ 1, ctx)) return false;
+                    if (lane == 0) {
+                        uint8_t* dst = smem + off_q + x * kTileBytes;
+                        mbar_arrive_expect_tx(&q_full[x], kTileBytes);
+                        for (int b = 0; b < 2; ++b)
+                            tma_load_3d(dst + b * kBoxBytes, &prm.q, b * 64, w.h * G, w.q.first + w.t0 + x * kTokens,
+                                        &q_full[x], stream);
+                    }
+                    __syncwarp();
+                    ++nq[x];
+                    return true;
+                };
+                auto load_kv = [&](const CUtensorMap* map, int j, bool tail = false) {  // tail: comes by way of warp 19
+                    const int st = seq % kStages;
+                    uint64_t* bar = tail ? &tail_full[nc & 1] : &kv_full[st];
+                    if (!warp_wait(&kv_empty[st], ((seq / kStages) & 1) ^ 1, ctx)) return false;
+                    const int n = min(kStepPages, npages - j * kStepPages);
+                    // lane 2 i + half: half of the dims of the step's page i
+                    const int page = __shfl_sync(0xffffffffu, ent, ((j - w.j0) & 3) * kStepPages + ((lane >> 1) & 7));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, n * 2 * kPageBox);
+                    __syncwarp();
+                    if (lane < 2 * n)
+                        tma_load_3d(smem + off_ring + st * kTileBytes + (lane & 1) * kBoxBytes + (lane >> 1) * kPageBox, map,
+                                    (lane & 1) * 64, w.h, page * kPageSize, bar, ordinary);
+                    __syncwarp();
+                    ++seq;
+                    nc += tail;
+                    return true;
+                };
+                for (int j = w.j0; j < w.j1 && !stop; ++j) {
+                    if (((j - w.j0) & 3) == 0) {  // 32 entries serve four steps; the next 32 are on their way meanwhile
+                        ent = next;
+                        if (ent == p.num_pages) raise_status(ctx.status, PKV_STATUS_BAD_PAGE);
+                        if (j + 4 < w.j1) next = entries((j + 4) * kStepPages + lane);
+                    }
+                    if (j == w.j0) stop = !load_q(0);
+                    stop = stop || !load_kv(&prm.k, j);
+                    if (j == w.j0) stop = stop || !load_q(1);
+                    stop = stop || !load_kv(&prm.v, j, (j + 1) * kRows >= end && (end & 15));
+                }
+            }
+            // every copy that this warp issued lands before the CTA may end
+            for (int j = max(0, nc - 2); j < nc; ++j) warp_drain(&tail_full[j & 1], (j >> 1) & 1);
+            for (int j = max(0, seq - kStages); j < seq; ++j) warp_drain(&kv_full[j % kStages], (j / kStages) & 1);
+            for (int x = 0; x < 2; ++x)
+                if (nq[x] > 0) warp_drain(&q_full[x], (nq[x] - 1) & 1);
+        } else if (warp == 19) {
+            // ------------------------------------------------------------------------ rows behind the pair's last key
+            // The products' last step of 16 keys reads them, and they may hold anything.
+            int kv = 0, nc = 0;
+            for (int k = 0;; ++k) {
+                if (!warp_wait(w_full, k & 1, ctx)) break;
+                const Work w = *work;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_empty);
+                if (w.h < 0) break;
+                const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
+                kv += 2 * (w.j1 - w.j0);
+                if ((end & 15) == 0 || w.j1 * kRows < end) continue;
+                const int pos = kv - 1;
+                // (Two barriers: the loader may be one such tile ahead, but not two, as it gets a work when every warp has
+                // taken the one before.)
+                if (!warp_wait(&tail_full[nc & 1], (nc >> 1) & 1, ctx)) break;
+                ++nc;
+                uint8_t* v = smem + off_ring + (pos % kStages) * kTileBytes;
+                const int first = end - (w.j1 - 1) * kRows, last = (first + 15) & ~15;
+                for (int i = first * 16 + lane; i < last * 16; i += 32)
+                    *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[pos % kStages]);
+            }
+        } else if (warp == 16) {
+            // ------------------------------------------------------------------------- matrix instructions
+            if (elect_one()) {  // one thread waits for and issues everything
+                int kv = 0;                        // ring position of the next K tile of the current work
+                int nq[2] = {0, 0}, no[2] = {0, 0};  // tiles begun; accumulators begun
+                int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    if (!thread_wait(w_full, k & 1, ctx)) break;
+                    const Work w = *work;
+                    mbar_arrive(w_empty);
+                    if (w.h < 0) break;
+                    // keys from the piece's first on, up to its last
+                    const int most = (w.j1 - w.j0) * kRows;
+                    const int end0 = min(tile_end(w, 0, kTokens) - w.j0 * kRows, most);
+                    const int end1 = min(tile_end(w, 1, kTokens) - w.j0 * kRows, most);
+                    const int steps = w.j1 - w.j0;
+                    // ring positions: K_j at kv + 2j, V_j one behind it
+                    const uint32_t ring = smem_addr(smem + off_ring);
+                    auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
+                    auto wait_stage = [&](int pos) { return thread_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
+                    // keys of the piece's step j that tile x needs (0: none)
+                    auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
+                    auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
+                        const int n = (keys(x, j) + 15) & ~15;
+                        if (n == 0) return;
+                        const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
+                        const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
+                        const uint32_t idesc = mma_idesc(n, false);
+                        const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
+                        mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, idesc);
+                        mma_commit(&s_full[x]);
+                        if (last) mma_commit(&q_empty[x]);
+                    };
+                    auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
+                        const int n = (keys(x, j) + 15) >> 4;
+                        if (n == 0) return true;
+                        constexpr uint32_t idesc = mma_idesc(kHeadDim, true);
+                        const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
+                        const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
+                        const bool last = keys(x, j + 1) == 0;
+                        if (j == 0) {  // the previous tile's rows have been read
+                            if (!thread_wait(&o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
+                            ++no[x];
+                        }
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {  // 64 keys each
+                            const int c = min(4, n - 4 * half);  // steps of 16 keys
+                            if (c <= 0) break;
+                            if (!thread_wait(&p_full[2 * x + half], np[x][half] & 1, ctx)) return false;
+                            ++np[x][half];
+                            tc_fence_after();
+                            if (c == 4)
+                                mma_ts_64(o, pw + 64 * half, v + 512 * half, idesc, j > 0 || half > 0);
+                            else
+                                for (int i = 0; i < c; ++i)
+                                    mma_ts(o, pw + 64 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
+                            if (half == 0) mma_commit(&lo_done[x]);
+                            if (last && n - 4 * half <= 4) mma_commit(&o_full[x]);
+                        }
+                        return true;
+                    };
+                    auto release = [&](int pos) { mma_commit(&kv_empty[pos % kStages]); };
+                    ok = wait_stage(kv);
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (keys(x, 0) == 0) continue;
+                        ok = thread_wait(&q_full[x], nq[x] & 1, ctx);
+                        ++nq[x];
+                        tc_fence_after();
+                        if (ok) scores(x, 0);
+                    }
+                    if (!ok) break;
+                    release(kv);
+                    for (int j = 0; j < steps && ok; ++j) {
+                        ok = wait_stage(kv + 2 * j + 1) && values(0, j);
+                        if (ok && j + 1 < steps) {
+                            ok = wait_stage(kv + 2 * j + 2);
+                            if (ok) scores(0, j + 1);
+                        }
+                        ok = ok && values(1, j);
+                        if (!ok) break;
+                        release(kv + 2 * j + 1);
+                        if (j + 1 < steps) {
+                            scores(1, j + 1);
+                            release(kv + 2 * j + 2);
+                        }
+                    }
+                    kv += 2 * steps;
+                }
+                mma_commit(drain);
+            }
+            __syncwarp();
+            // every matrix instruction has completed before the TMEM is freed and the CTA ends
+            warp_drain(drain, 0);
+        }
+    } else {
+        // ---------------------------------------------------------------------------- softmax and output rows
+        regs_grow<kSoftmaxRegs>();
+        const int x = warp >> 3, h = (warp >> 2) & 1;  // tile, half of the keys (and of the output's dims)
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + x * 128 + h * 64;  // this half's scores, and its weights over the first 32
+        const uint32_t o_at = tmem + lanes + 256 + x * 128;
+        volatile float* ref_at = reinterpret_cast<volatile float*>(smem + off_ref) + x * kRows + row;
+        float2* parts = reinterpret_cast<float2*>(smem + off_parts) + x * 2 * kRows + row;  // + buffer * 4 kRows + half * kRows
+        uint64_t* settled = &first_ref[x * 4 + (warp & 3)];
+        uint64_t* second = &half_done[x * 4 + (warp & 3)];
+        volatile int* late_at = reinterpret_cast<volatile int*>(smem + off_late) + x * 4 + (warp & 3);
+        const float sl2 = p.scale_log2;
+        const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
+        int ns = 0, no = 0;  // steps, tiles taken
+        int step2 = 0;       // steps with keys in the second half, as the first half counts them
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!warp_wait(w_full, k & 1, ctx)) break;
+            const Work w = *work;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w_empty);
+            if (w.h < 0) break;
+            const int end = tile_end(w, x, kTokens);
+            const int j1 = min(w.j1, ceil_div(end, kRows));  // the tile's steps of this piece: j0 .. j1 - 1
+            const int token = w.t0 + x * kTokens + row / G;
+            const bool mine = token < w.q.n;
+            float2* state_ml = p.ml + ((int64_t)w.state * 2 + x) * kRows + row;
+            if (j1 <= w.j0) {  // tile A may end before the piece begins
+                if (w.state >= 0 && h == 0 && mine) *state_ml = make_float2(-INFINITY, 0.f);
+                continue;
+            }
+            const bool idle = w.t0 + x * kTokens + (row & ~31) / G >= w.q.n;  // none of the warp's rows is one
+            float ref = -INFINITY, l = 0.f;
+            for (int j = w.j0; j < j1; ++j) {
+                const int step = ns++;
+                const int last = end - j * kRows - h * 64;  // keys of this half, counted from its first
+                // The tile's last step ends in the first half: the second does not wait for its scores (nothing would keep
+                // the next tile's from coming before it looks, and a parity two phases on does not pass). They have come
+                // when the tile's accumulator is complete, for which it waits below.
+                if (last <= 0) continue;
+                if (!warp_wait(&s_full[x], step & 1, ctx)) {
+                    ok = false;
+                    break;
+                }
+                if (idle) {  // it keeps the count of arrivals; nothing reads its rows of the accumulator
+                    if (last > 64) ++step2;
+                    if (lane == 0) {
+                        if (h == 0 && j == w.j0) mbar_arrive(settled);
+                        if (h == 1) mbar_arrive(second);
+                        mbar_arrive(&p_full[2 * x + h]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                tc_fence_after();
+                // Steps with keys behind the tile's first token are masked; the others are whole.
+                const bool tail = (j + 1) * kRows > w.q.start + w.t0 + x * kTokens;
+                const int lim = tail ? min(w.q.start + token, end - 1) - j * kRows - h * 64 : 64;
+                auto fetch = [&](int c, uint32_t* r) {  // 32 of the row's scores
+                    tmem_ld32(s_at + c * 32, r);
+                    tmem_wait_ld();
+                    tmem_use32(r);
+                    if (tail) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i > lim) r[i] = 0xff800000u;  // -inf
+                    }
+                };
+                auto greatest = [&]() {
+                    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (c * 32 < last) {
+                            uint32_t r[32];
+                            fetch(c, r);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                m0 = fmaxf(m0, __uint_as_float(r[i]));
+                                m1 = fmaxf(m1, __uint_as_float(r[i + 1]));
+                            }
+                        }
+                    }
+                    return fmaxf(m0, m1);
+                };
+                uint32_t ph[32];  // the weights, in fp16
+                auto weights = [&]() {  // returns their sum
+                    const float nref = ref == -INFINITY ? 0.f : -ref;
+                    const uint64_t refx2 = pack_f32x2(nref, nref);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (c * 32 < last) {
+                            uint32_t r[32];
+                            fetch(c, r);
+                            const float* f = reinterpret_cast<const float*>(r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float a, b;
+                                unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
+                                a = fast_exp2(a);
+                                b = fast_exp2(b);
+                                if (i & 1)
+                                    sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+                                else
+                                    sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+                                ph[c * 16 + i] = pack_half2(a, b);
+                            }
+                        }
+                    }
+                    float a, b;
+                    unpack_f32x2(add_f32x2(sum0, sum1), a, b);
+                    return a + b;
+                };
+                // Scales what has been accumulated up to now (this thread's sum; the row's accumulator).
+                auto scale_sum = [&](float to) {
+                    if (to != ref) {
+                        const float f = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                        l = l == INFINITY && f == 0.f ? 0.f : l * f;  // NaN only where a score is
+                    }
+                };
+                auto scale_acc = [&](float f) {
+                    const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t t[32];
+                        tmem_ld32(o_at + c * 32, t);
+                        tmem_wait_ld();
+                        tmem_use32(t);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
+                            t[i] = __float_as_uint(a);
+                            t[i + 1] = __float_as_uint(b);
+                        }
+                        tmem_st32(o_at + c * 32, t);
+                    }
+                };
+                // The reference that this half's keys ask for: above the present one by a whole number.
+                auto raised = [&]() {
+                    const float to = ref_for(greatest() * sl2);
+                    return ref == -INFINITY ? to : to > ref ? ref + ceilf(to - ref) : ref;
+                };
+                if (j > w.j0) {  // the other half may have raised it in the step before
+                    const float r = *ref_at;
+                    scale_sum(r);
+                    ref = r;
+                } else if (h == 0) {
+                    ref = ref_for(greatest() * sl2);
+                    *ref_at = ref;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(settled);
+                } else {
+                    if (!warp_wait(settled, no & 1, ctx)) {
+                        ok = false;
+                        break;
+                    }
+                    ref = *ref_at;
+                }
+                float sum = weights();
+                // (A row without a finite score has no reference yet, and asks for one. One whose scores are NaN, such as those
+                // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
+                const bool ask = ref == -INFINITY ? !isnan(sum) : sum > kMost;
+                const bool raise = (j > w.j0 || h == 1) && __any_sync(0xffffffffu, ask);
+                if (h == 0 && raise) {
+                    // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
+                    float f2 = 1.f;
+                    const float to = raised();
+                    const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                    if (last > 64) {
+                        if (!warp_wait(second, step2 & 1, ctx)) {
+                            ok = false;
+                            break;
+                        }
+                        if (*late_at == 0) f2 = f;
+                    }
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, f2 != 1.f)) {
+                        uint32_t t[32];
+                        tmem_ld32(s_at + 64, t);
+                        tmem_wait_ld();
+                        tmem_use32(t);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
+                            t[i] = pack_half2(v.x * f2, v.y * f2);
+                        }
+                        tmem_st32(s_at + 64, t);
+                    }
+                    scale_sum(to);
+                    ref = to;
+                    *ref_at = ref;
+                    scale_acc(f);
+                    sum = weights();
+                } else if (h == 1) {
+                    if (raise) {
+                        if (lane == 0) *late_at = 1;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(second);
+                        // the first half's products must be in the accumulator before it is scaled
+                        if (!warp_wait(&lo_done[x], step & 1, ctx)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float r = *ref_at;  // the first half may have raised it in this step
+                        scale_sum(r);
+                        ref = r;
+                        const float to = raised();
+                        const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                        scale_sum(to);
+                        ref = to;
+                        *ref_at = ref;
+                        scale_acc(f);
+                        sum = weights();
+                    } else if (lane == 0) {
+                        *late_at = 0;
+                    }
+                }
+                if (last > 64) ++step2;
+                l += sum;
+                parts[(no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
+                tmem_st32(s_at, ph);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (h == 1 && !raise) mbar_arrive(second);  // before the one that lets the first half's next step begin
+                    mbar_arrive(&p_full[2 * x + h]);
+                }
+            }
+            if (!ok) break;
+            if (!warp_wait(&o_full[x], no & 1, ctx)) break;
+            if (idle) {
+                if (lane == 0) mbar_arrive(&o_free[x]);
+                __syncwarp();
+                ++no;
+                continue;
+            }
+            tc_fence_after();
+            // the row's sum: both halves', relative to the last reference (they only rise)
+            const float2 lo = parts[(no & 1) * 4 * kRows], hi = parts[(no & 1) * 4 * kRows + kRows];
+            float total = lo.y;
+            if (end - w.j0 * kRows > 64) {
+                const float top = fmaxf(lo.x, hi.x);
+                auto part = [&](const float2& x) {
+                    const float f = x.x == top ? 1.f : fast_exp2(x.x - top);
+                    return x.y == INFINITY && f == 0.f ? 0.f : x.y * f;
+                };
+                total = part(lo) + part(hi);
+            }
+            if (w.state >= 0) {  // columns in fours, rows side by side
+                float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)w.state * 2 + x) * 32 + h * 16) * kRows + row;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + h * 64 + c * 32, o);
+                    tmem_wait_ld();
+                    tmem_use32(o);
+                    if (c == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&o_free[x]);
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[(c * 8 + i) * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+                if (h == 0 && mine) *state_ml = make_float2(end - w.j0 * kRows > 64 ? fmaxf(lo.x, hi.x) : lo.x, total);
+                ++no;
+                continue;
+            }
+            const float inv = 1.f / total;
+            __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
+            const __half2 zero = probe;
+            // Four lanes exchange 16-byte pieces of their rows, so that they store 64 consecutive bytes of one row at a time
+            // (16 bytes of 32 rows an instruction took 1.7 us a tile).
+            const int q4 = lane & 3;
+            __half* dst[4];
+            bool in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (row & ~3) + i, t = w.t0 + x * kTokens + r / G;
+                in[i] = t < w.q.n;
+                dst[i] = static_cast<__half*>(p.out) + (int64_t)(w.q.first + t) * p.out_stride + (w.h * G + r % G) * kHeadDim +
+                         h * 64 + q4 * 8;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[32], y[4][4];
+                tmem_ld32(o_at + h * 64 + c * 32, o);
+                tmem_wait_ld();
+                tmem_use32(o);
+                if (c == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[x]);  // the next tile's products may overwrite it
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
+                    const uint32_t u = pack_half2(a, b);
+                    probe = __hfma2(*reinterpret_cast<const __half2*>(&u), zero, probe);
+                    y[i >> 2][i & 3] = u;
+                }
+#pragma unroll
+                for (int s = 1; s < 4; s <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!(i & s))
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, q4 & s ? y[i][e] : y[i + s][e], s);
+                                (q4 & s ? y[i][e] : y[i + s][e]) = got;
+                            }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            }
+            ++no;
+            // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
+            // themselves 1, or above 1/2.
+            const bool low_sum = !(total >= 0.25f);
+            const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
+            const unsigned again = __ballot_sync(0xffffffffu, mine && odd && !isnan(total));
+            if (again) {
+                const unsigned redo = __ballot_sync(0xffffffffu, low_sum) & again;
+                __syncwarp();  // the rows were stored by other lanes
+                finish_rows<G>(p, w.q, w.s, w.t0 + x * kTokens + (row & ~31) / G, w.h, h, again, redo);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---- adding up the states of pairs that were cut ---------------------------------------------------------------------
+// A block: 32 rows of the pair that began in CTA blockIdx.x and went on in the pieces behind it. Warp w takes dims 16 w ..
+// + 15. Where few rows are valid, the lanes of the others take every 2nd, 4th, .. state of them, and the sums are added
+// over the lanes.
+constexpr int kMergeWarps = 8;
+
+template <int G>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkParams p) {
+    constexpr int kTokens = kRows / G;
+    __shared__ uint32_t s_bad[2], s_redo;  // rows with a value that is not finite, by half of the dims; wrong for certain
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    const Merge m = static_cast<const Merge*>(p.merges)[blockIdx.x];
+    const int r0 = (int)blockIdx.y * 32;  // of the pair's 256 rows
+    const int valid = min(32, (min(m.q.n, m.t0 + 2 * kTokens) - m.t0) * G - r0);
+    if (m.pieces <= 1 || valid <= 0) return;
+    if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
+    if (threadIdx.x == 2) s_redo = 0;
+    __syncthreads();
+    int span = 1;  // lanes a row takes: a power of two
+    while (32 / (2 * span) >= valid) span *= 2;
+    const int rows = 32 / span, row = r0 + lane % rows, turn = lane / rows;
+    const float2* ml = p.ml + row;
+    const float4* acc = reinterpret_cast<const float4*>(p.acc) + ((row >> 7) * 32 + warp * 4) * kRows + (row & 127);
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i * p.lanes)); };
+    float top = -INFINITY;
+    bool nan = false;
+    for (int i = turn; i < m.pieces; i += span) {
+        const float2 x = __ldcg(ml + slot(i) * 2 * kRows);
+        nan |= isnan(x.y);
+        if (x.y > 0.f) top = fmaxf(top, x.x);
+    }
+    for (int o = rows; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float total = 0.f;
+    float4 sum[4] = {};
+#pragma unroll 2
+    for (int i = turn; i < m.pieces; i += span) {
+        const float2 x = __ldcg(ml + slot(i) * 2 * kRows);
+        float4 a[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = __ldcg(acc + slot(i) * 2 * 32 * kRows + c * kRows);
+        if (x.y > 0.f) {  // a piece whose keys come behind the row's token has none
+            const float f = x.x == top ? 1.f : fast_exp2(x.x - top);
+            total += x.y == INFINITY && f == 0.f ? 0.f : x.y * f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sum[c].x += a[c].x * f;
+                sum[c].y += a[c].y * f;
+                sum[c].z += a[c].z * f;
+                sum[c].w += a[c].w * f;
+            }
+        }
+    }
+    if (nan) total = NAN;
+    for (int o = rows; o < 32; o *= 2) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            sum[c].x += __shfl_xor_sync(0xffffffffu, sum[c].x, o);
+            sum[c].y += __shfl_xor_sync(0xffffffffu, sum[c].y, o);
+            sum[c].z += __shfl_xor_sync(0xffffffffu, sum[c].z, o);
+            sum[c].w += __shfl_xor_sync(0xffffffffu, sum[c].w, o);
+        }
+    }
+    const int t = m.t0 + row / G;
+    const bool mine = turn == 0 && row - r0 < valid;
+    const float inv = 1.f / total;
+    uint32_t y[8];
+    __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
+    const __half2 zero = probe;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        y[2 * c] = pack_half2(sum[c].x * inv, sum[c].y * inv);
+        y[2 * c + 1] = pack_half2(sum[c].z * inv, sum[c].w * inv);
+        probe = __hfma2(*reinterpret_cast<const __half2*>(&y[2 * c]), zero, probe);
+        probe = __hfma2(*reinterpret_cast<const __half2*>(&y[2 * c + 1]), zero, probe);
+    }
+    if (mine) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + (int64_t)(m.q.first + t) * p.out_stride +
+                                              (m.h * G + row % G) * kHeadDim + warp * 16);
+        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        const bool low_sum = !(total >= 0.25f);
+        if ((__low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum) && !isnan(total)) {
+            atomicOr(&s_bad[warp >> 2], 1u << (row - r0));
+            if (low_sum) atomicOr(&s_redo, 1u << (row - r0));
+        }
+    }
+    __syncthreads();
+    if (warp < 2 && s_bad[warp]) finish_rows<G>(p, m.q, m.s, m.t0 + r0 / G, m.h, warp, s_bad[warp], s_redo & s_bad[warp]);
+}
+
+template <int G>
+int launch(const Params& prm, cudaStream_t stream) {
+    static int configured_mask = 0;  // one bit per device ordinal (< 32)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 32 || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+        cudaFuncAttributes a{};
+        cudaError_t e = cudaFuncGetAttributes(&a, chunk_kernel<G>);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares come out of what the launch gives them
+        if (a.numRegs * kThreads < kSoftmax * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(chunk_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
+    }
+    const cudaError_t e = launch_kernel(chunk_kernel<G>, prm.p.grid, kThreads, kSmem, stream, prm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)prm.p.grid, 2 * kRows / 32);
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel<G>, prm.p);
+}
+
+// KV heads whose CTAs read the same pages at the same time: of the divisors of Hkv up to 8 (a token's K of 8 heads are 2 KB
+// of a page) the one that leaves the fewest SMs without a piece, the largest of these.
+int head_lanes(int hkv, int num_sms) {
+    int best = 1;
+    for (int d = 2; d <= 8; ++d)
+        if (hkv % d == 0 && d <= num_sms && num_sms / d * d >= num_sms / best * best) best = d;
+    return best;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(int num_sms) {
+    const size_t merges = ((size_t)num_sms * kChunkMergeBytes + kWsAlign - 1) / kWsAlign * kWsAlign;
+    return sizeof(pkv_ws_header) + merges + (size_t)num_sms * 2 * 2 * kRows * (sizeof(float2) + kRowBytes * 2);
+}
+
+int launch_chunk_attention(const ChunkParams& in, int num_sms, void* stream) {
+    Params prm;
+    ChunkParams& p = prm.p;
+    p = in;
+    p.lanes = head_lanes(p.Hkv, num_sms);
+    p.grid = num_sms / p.lanes * p.lanes;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(p.hdr);
+    const size_t merges = ((size_t)num_sms * kChunkMergeBytes + kWsAlign - 1) / kWsAlign * kWsAlign;
+    p.merges = ws + sizeof(pkv_ws_header);
+    p.ml = reinterpret_cast<float2*>(ws + sizeof(pkv_ws_header) + merges);
+    p.acc = reinterpret_cast<float*>(p.ml + (size_t)num_sms * 2 * 2 * kRows);
+    p.wait_ns = kWaitLimitNs + std::min(kFinishMostNs, kFinishNs * kPageSize * (uint64_t)p.max_pages);
+    const int g = p.Hq / p.Hkv;
+    const int64_t token = (int64_t)p.Hkv * kHeadDim;
+    if (!encode_rows(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g, kRows / g) ||
+        !encode_rows(&prm.k, p.k_pool, p.Hkv, (int64_t)p.num_pages * kPageSize, token, 1, kPageSize) ||
+        !encode_rows(&prm.v, p.v_pool, p.Hkv, (int64_t)p.num_pages * kPageSize, token, 1, kPageSize))
+        return cudaErrorInvalidValue;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (g) {
+        case 1: return launch<1>(prm, s);
+        case 2: return launch<2>(prm, s);
+        case 4: return launch<4>(prm, s);
+        case 8: return launch<8>(prm, s);
+        case 16: return launch<16>(prm, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkv

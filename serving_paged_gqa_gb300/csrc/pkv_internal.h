@@ -114,6 +114,31 @@ struct Q4Params {
     float scale_log2;
 };
 
+// Arguments of the chunk attention (chunk_attention.cu): packed new tokens over the FP16 pages, or, with seq_lens and pages
+// instead of cu_seqlens and start, one token a row over selected pages.
+struct ChunkParams {
+    const void* q;
+    const void* k_pool;
+    const void* v_pool;
+    void* out;
+    const int32_t* cu_seqlens;
+    const int32_t* start;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* pages;  // [num_seqs][Hkv][select]: logical pages
+    pkv_ws_header* hdr;
+    int64_t q_stride, out_stride;  // elements between tokens
+    int32_t num_seqs, total_tokens, Hq, Hkv, num_pages, max_pages, select;
+    float scale_log2;
+    // set by the launcher
+    int32_t lanes, grid;  // KV heads side by side, CTAs
+    void* merges;         // a kChunkMergeBytes entry a CTA
+    float2* ml;           // [state][256]: (reference, sum) of a row
+    float* acc;           // [state][tile][32][128][4]: its accumulator
+    uint64_t wait_ns;     // limit of a wait
+};
+constexpr int kChunkMergeBytes = 32;
+
 // Kernel launchers (defined in the .cu files). They return the CUDA error of the launch.
 int launch_decode(const DecodeParams& p, int group, int grid, bool pdl, void* stream);
 int launch_build(const BuildParams& p, int grid, void* stream);
@@ -126,9 +151,13 @@ int launch_prompt_append(const PagesParams& p, int num_sms, void* stream);
 int launch_q4_append(const PagesParams& p, int num_sms, void* stream);
 int launch_q4_read(const PagesParams& p, int num_sms, void* stream);
 int launch_q4_decode(const Q4Params& p, int num_sms, void* stream);
+int launch_chunk_attention(const ChunkParams& p, int num_sms, void* stream);
 
 // Workspace of a 4-bit decode step on a GPU of num_sms SMs.
 size_t q4_workspace_bytes(const pkv_problem& pr, int num_sms);
+
+// Workspace of the chunk attention on a GPU of num_sms SMs.
+size_t chunk_workspace_bytes(int num_sms);
 
 // Validation shared by pkv_decode and the step entry points (PKV_OK or a PKV_E_* code; enqueues nothing).
 int check_decode_args(const pkv_plan_t* plan, const pkv_problem* pr, const void* q, const void* k_pool,

@@ -62,15 +62,14 @@
 // Every wait is bounded (pkv_wait.cuh): on a time-out the kernel sets PKV_STATUS_TIMEOUT, the warps drain what they
 // have in flight, and the CTA frees its TMEM and returns. The limit grows with the prompt: a warp may finish 32 rows from
 // all keys before them (0.16 us a key), while the others wait for it.
-#include <cuda.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 
 #include "pkv_internal.h"
 #include "pkv_launch.h"
 #include "pkv_tcgen05.cuh"
+#include "pkv_tensormap.h"
 #include "pkv_wait.cuh"
 
 namespace pkv {
@@ -941,32 +940,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
-// Packed rows [tokens][heads][128] at `stride` elements a token as the 3-D tensor (d, heads, tokens), box (64, heads of
-// the box, tokens of the box), 128-byte swizzle: one box is half of a tile's dims.
-bool encode(CUtensorMap* map, const void* rows, int heads, int64_t tokens, int64_t stride, int box_heads) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)kRowBytes, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)(kRows / box_heads)};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(rows), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int G>
 int launch(const Params& prm, int num_sms, cudaStream_t stream) {
     static int configured_mask = 0;  // one bit per device ordinal (< 32)
@@ -996,9 +969,10 @@ int launch_prompt_attention(const PromptParams& p, int num_sms, void* stream) {
     prm.p = p;
     prm.p.wait_ns = kWaitLimitNs + kFinishNs * p.total_tokens;
     const int g = p.Hq / p.Hkv;
-    if (!encode(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g) ||
-        !encode(&prm.k, p.k, p.Hkv, p.total_tokens, p.k_stride, 1) ||
-        !encode(&prm.v, p.v, p.Hkv, p.total_tokens, p.v_stride, 1))
+    // one box is half of a tile's dims
+    if (!encode_rows(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g, kRows / g) ||
+        !encode_rows(&prm.k, p.k, p.Hkv, p.total_tokens, p.k_stride, 1, kRows) ||
+        !encode_rows(&prm.v, p.v, p.Hkv, p.total_tokens, p.v_stride, 1, kRows))
         return cudaErrorInvalidValue;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (g) {
