@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_internal.h"
 #include "pkv_launch.h"
@@ -45,7 +46,10 @@ constexpr int kThreads = kSoftmax + 128;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96, what the launch has
 constexpr float kMost = 65504.f;             // sum of 64 weights above which the row's reference is raised
 constexpr float kLift = 5.f;                 // the largest weight where the reference was set, in powers of two
-constexpr int kMinSteps = 2;                 // steps a piece has at least
+// What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps.
+constexpr int kPairCost = 2;
+constexpr int kMinCost = 2;                  // of a piece, at least
+constexpr int kWhole = 10;                   // cost of a pair that is not cut where a piece has no more
 
 // One sequence: its first packed row, its new tokens, and how many it holds before them.
 struct Seq {
@@ -70,8 +74,8 @@ static_assert(sizeof(Merge) == kChunkMergeBytes, "workspace layout");
 constexpr int off_q = 0;
 constexpr int off_ring = 2 * kTileBytes;
 constexpr int off_work = off_ring + kStages * kTileBytes;
-constexpr int off_bars = off_work + (int)sizeof(Work) + 8 - sizeof(Work) % 8;
-constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 8 + 8 + 2 + 1;
+constexpr int off_bars = off_work + 2 * (int)sizeof(Work);
+constexpr int kBars = 2 * kStages + 38;
 constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
 constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
 constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
@@ -79,7 +83,7 @@ constexpr int off_scan = off_late + 8 * 4;               // int64 [warp]: steps 
 constexpr int off_begin = off_scan + kThreads / 32 * 8;  // int64, int32: where the piece begins
 constexpr int off_misc = off_begin + 16;                 // abort flag, TMEM address
 constexpr int kSmem = off_misc + 16 + 1024;              // slack to align the base to 1024 bytes
-static_assert(off_bars % 8 == 0 && off_parts % 8 == 0 && off_scan % 8 == 0, "alignment");
+static_assert(sizeof(Work) % 4 == 0 && off_bars % 8 == 0 && off_parts % 8 == 0 && off_scan % 8 == 0, "alignment");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Params {
@@ -122,13 +126,13 @@ __device__ __forceinline__ int keys_of(const Seq& q, int t0) {
     return q.start + (int)min((int64_t)q.n, (int64_t)t0 + 2 * kRows / G);
 }
 
-// Steps of the first m pairs, all of them whole: sum over i = 1..m of ceil((start + i T) / 128), T = 256 / G tokens. For G
-// > 1 that is ceil((c + i) / r) with c = ceil(start / T), r = 128 / T.
+// Cost of the first m pairs, all of them whole: sum over i = 1..m of ceil((start + i T) / 128) + kPairCost, T = 256 / G tokens.
+// For G > 1 the quotient is ceil((c + i) / r) with c = ceil(start / T), r = 128 / T.
 template <int G>
-__device__ __forceinline__ int64_t steps_before(const Seq& q, int m) {
+__device__ __forceinline__ int64_t cost_before(const Seq& q, int m) {
     constexpr int T = 2 * kRows / G;
     if constexpr (T > kRows) {
-        return (int64_t)m * ceil_div(q.start, kRows) + (int64_t)m * (m + 1);
+        return (int64_t)m * (ceil_div(q.start, kRows) + kPairCost) + (int64_t)m * (m + 1);
     } else {
         constexpr int r = kRows / T;
         const int64_t c = ceil_div(q.start, T);
@@ -136,23 +140,30 @@ __device__ __forceinline__ int64_t steps_before(const Seq& q, int m) {
             const int64_t a = x / r, b = x % r;
             return r * (a * (a + 1) / 2) + b * (a + 1);
         };
-        return upto(c + m) - upto(c);
+        return upto(c + m) - upto(c) + (int64_t)m * kPairCost;
     }
 }
 
 template <int G>
-__device__ __forceinline__ int64_t steps_of(const Seq& q) {  // of one KV head
+__device__ __forceinline__ int64_t cost_of(const Seq& q) {  // of one KV head
     const int m = pairs_of<G>(q);
-    return m == 0 ? 0 : steps_before<G>(q, m - 1) + ceil_div(q.start + q.n, kRows);
+    return m == 0 ? 0 : cost_before<G>(q, m - 1) + kPairCost + ceil_div(q.start + q.n, kRows);
 }
 
 // Keys of tile x (0: A, 1: B) of a pair; 0: it has no rows.
-__device__ __forceinline__ int tile_end(const Work& w, int x, int tokens) {
-    const int t = w.t0 + x * tokens;
-    return t < w.q.n ? w.q.start + min(t + tokens, w.q.n) : 0;
+template <typename W>
+__device__ __forceinline__ int tile_end(const W& w, int x, int tokens) {
+    const int t = w.t0 + x * tokens, n = w.q.n;
+    return t < n ? w.q.start + min(t + tokens, n) : 0;
 }
 
-// Piece of the line of `total` steps that step u lies in; piece i begins at i * total / pieces.
+// Whether the pair has a tile B.
+template <typename W>
+__device__ __forceinline__ bool tile_b(const W& w, int tokens) {
+    return w.t0 + tokens < w.q.n;
+}
+
+// Piece of the line of cost `total` that its unit u lies in; piece i begins at i * total / pieces.
 __device__ __forceinline__ int piece_of(int64_t u, int64_t total, int pieces) {
     return (int)(((u + 1) * pieces + total - 1) / total) - 1;
 }
@@ -301,6 +312,440 @@ __device__ __noinline__ void finish_rows(const ChunkParams& p, const Seq& sq, in
     }
 }
 
+// ---- softmax and output rows -----------------------------------------------------------------------------------------
+// Barriers of the CTA, in shared memory.
+struct Bars {
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t w_full[2], w_empty[2];  // a work has been published; every warp is done with what it needs of it
+    uint64_t q_full[2], q_empty[2];  // like those below: tile A, tile B
+    uint64_t s_full[2];              // the tile's scores are in TMEM
+    uint64_t p_full[2][2];           // its weights of the step's first, second 64 keys are
+    uint64_t o_full[2];              // its accumulator is complete
+    uint64_t lo_done[2];             // the products of a step's first 64 keys are in the accumulator
+    uint64_t o_free[2];              // the accumulator has been read
+    uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
+    uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
+    uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
+    uint64_t drain;
+};
+static_assert(sizeof(Bars) == kBars * 8, "layout");
+
+// What a warp of the softmax has counted: the tile's steps; tiles taken; those of B; steps with keys in the second half, as the
+// first half counts them.
+struct Counts {
+    int ns, no, nb, step2;
+};
+
+// The tile of one work. Alone: there is no tile B, and A's rows are worked on by both tiles' warps, which take its odd and
+// even steps and the accumulators of B and A (few rows wait for K and V, and for one step's scores, weights and products
+// after the other: at 1.8 us a step, in turn, an SM takes half of its share of the memory's bandwidth). Weights are
+// then two fp16 parts, for which such pairs leave the tensor core the time: the relative error is that of the output's
+// rounding, 2.1e-4 (with one part 2.9e-4).
+template <int G, bool alone>
+__device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w,
+                                             const WaitCtx& ctx, Counts& cnt) {
+    constexpr int kTokens = kRows / G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Bars& bars = *reinterpret_cast<Bars*>(smem + off_bars);
+    const int x = warp >> 3, h = (warp >> 2) & 1;  // tile, half of the keys (and of the output's dims)
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + x * 128 + h * 64;  // this half's scores, and its weights over the first 32
+    const uint32_t o_at = tmem + lanes + 256 + x * 128;
+    volatile float* ref_at = reinterpret_cast<volatile float*>(smem + off_ref) + x * kRows + row;
+    float2* parts = reinterpret_cast<float2*>(smem + off_parts) + x * 2 * kRows + row;  // + buffer * 4 kRows + half * kRows
+    uint64_t* settled = &bars.first_ref[x][warp & 3];
+    uint64_t* second = &bars.half_done[x][warp & 3];
+    volatile int* late_at = reinterpret_cast<volatile int*>(smem + off_late) + x * 4 + (warp & 3);
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
+    constexpr int kNext = alone ? 2 * kRows : kRows;  // from one of the tile's steps to the next
+    const bool both = !alone || w.j1 - w.j0 > 1;      // B's warps have something to do
+    const int skip = alone ? x * kRows : 0;
+    // Positions are counted from the tile's first key of the piece.
+    const int end = tile_end(w, alone ? 0 : x, kTokens) - w.j0 * kRows - skip;
+    const int all = min(w.j1 - w.j0, ceil_div(max(end + skip, 0), kRows));
+    const int steps = alone ? (all + 1 - x) >> 1 : all;
+    auto first_token = [&]() { return w.q.start - w.j0 * kRows + w.t0 + (alone ? 0 : x * kTokens) - skip; };
+    if (steps == 0) {  // tile A may end before the piece begins
+        if (!alone && w.state >= 0 && h == 0 && first_token() + row / G < end)
+            p.ml[((int64_t)w.state * 2 + x) * kRows + row] = make_float2(-INFINITY, 0.f);
+        if (!alone || x == 0) cnt.nb += both;
+        return true;
+    }
+    // The accumulators are complete; then they have been read: A's warps read B's, too, where A is alone.
+    auto complete = [&]() {
+        return warp_wait(&bars.o_full[x], cnt.no & 1, ctx) && (!alone || x == 1 || !both || warp_wait(&bars.o_full[1], cnt.nb & 1, ctx));
+    };
+    auto have_read = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bars.o_free[x]);
+            if (alone && both) mbar_arrive(&bars.o_free[1]);
+        }
+    };
+    if (first_token() + (row & ~31) / G >= end) {
+        // None of the warp's rows is one, and nothing reads their weights or accumulators: it keeps the count of arrivals.
+        // (In the loop below this test costs every step of full tiles 80 cycles.)
+        for (int j = 0; j < steps; ++j) {
+            const int step = cnt.ns++, last = end - j * kNext - h * 64;
+            if (last <= 0) continue;
+            if (!warp_wait(&bars.s_full[x], step & 1, ctx)) return false;
+            if (last > 64) ++cnt.step2;
+            if (lane == 0) {
+                if (h == 0 && j == 0) mbar_arrive(settled);
+                if (h == 1) mbar_arrive(second);
+                mbar_arrive(&bars.p_full[x][h]);
+            }
+            __syncwarp();
+        }
+        if (!complete()) return false;
+        if (!alone || x == 0) have_read();
+        ++cnt.no;
+        cnt.nb += both;
+        return true;
+    }
+    // Keys from `masked` on are in steps with keys behind the tile's first token; the others are whole. (It may begin before the
+    // piece.)
+    const int masked = max(first_token(), 0) / kRows * kRows;
+    const int seen = min(first_token() + row / G, end - 1) - h * 64;  // the row's last key, from the half's first on
+    float ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < steps; ++j) {
+        const int step = cnt.ns++;
+        const int last = end - j * kNext - h * 64;  // keys of this half, counted from its first
+        // The tile's last step ends in the first half: the second does not wait for its scores (nothing would keep
+        // the next tile's from coming before it looks, and a parity two phases on does not pass). They have come
+        // when the tile's accumulator is complete, for which it waits below.
+        if (last <= 0) continue;
+        if (!warp_wait(&bars.s_full[x], step & 1, ctx)) return false;
+        tc_fence_after();
+        // Keys behind the row's token: -inf in TMEM, before anything reads the scores. (Masked as they are read, which unmasked steps
+        // skip, every step takes 7 % longer.)
+        if (j * kNext >= masked) {
+            const int lim = seen - j * kNext;
+#pragma unroll 1
+            for (int c = 0; c < 2 && c * 32 < last; ++c) {
+                uint32_t r[32];
+                tmem_ld32(s_at + c * 32, r);
+                tmem_wait_ld();
+                tmem_use32(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c * 32 + i > lim) r[i] = 0xff800000u;
+                tmem_st32(s_at + c * 32, r);
+            }
+            tmem_wait_st();
+        }
+        auto fetch = [&](int c, uint32_t* r) {  // 32 of the row's scores
+            tmem_ld32(s_at + c * 32, r);
+            tmem_wait_ld();
+            tmem_use32(r);
+        };
+        auto greatest = [&]() {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (c * 32 < last) {
+                    uint32_t r[32];
+                    fetch(c, r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        m0 = fmaxf(m0, __uint_as_float(r[i]));
+                        m1 = fmaxf(m1, __uint_as_float(r[i + 1]));
+                    }
+                }
+            }
+            return fmaxf(m0, m1);
+        };
+        uint32_t ph[alone ? 16 : 32];  // the weights, in fp16
+        auto weights = [&]() {  // returns their sum
+            const float nref = ref == -INFINITY ? 0.f : -ref;
+            const uint64_t refx2 = pack_f32x2(nref, nref);
+            uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (c * 32 < last) {
+                    uint32_t r[32];
+                    fetch(c, r);
+                    const float* f = reinterpret_cast<const float*>(r);
+                    uint32_t pl[alone ? 16 : 1];  // what they leave of them
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float a, b;
+                        unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
+                        if (i & 1)
+                            sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+                        else
+                            sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+                        const uint32_t y = pack_half2(a, b);
+                        if constexpr (alone) {
+                            const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                            ph[i] = y;
+                            pl[i] = pack_half2(a - hi.x, b - hi.y);
+                        } else {
+                            ph[c * 16 + i] = y;
+                        }
+                    }
+                    if constexpr (alone) {
+                        tmem_st16(s_at + c * 32, ph);
+                        tmem_st16(s_at + c * 32 + 16, pl);
+                    }
+                }
+            }
+            float a, b;
+            unpack_f32x2(add_f32x2(sum0, sum1), a, b);
+            return a + b;
+        };
+        // Scales what has been accumulated up to now (this thread's sum; the row's accumulator).
+        auto scale_sum = [&](float to) {
+            if (to != ref) {
+                const float f = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                l = l == INFINITY && f == 0.f ? 0.f : l * f;  // NaN only where a score is
+            }
+        };
+        auto scale_acc = [&](float f) {
+            const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t t[32];
+                tmem_ld32(o_at + c * 32, t);
+                tmem_wait_ld();
+                tmem_use32(t);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float a, b;
+                    unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
+                    t[i] = __float_as_uint(a);
+                    t[i + 1] = __float_as_uint(b);
+                }
+                tmem_st32(o_at + c * 32, t);
+            }
+        };
+        // The reference that this half's keys ask for: above the present one by a whole number.
+        float top = 0.f;  // alone: the half's largest score
+        auto raised = [&]() {
+            const float to = ref_for(alone ? top : greatest() * sl2);
+            return ref == -INFINITY ? to : to > ref ? ref + ceilf(to - ref) : ref;
+        };
+        if (j > 0) {  // the other half may have raised it in the step before
+            const float r = *ref_at;
+            scale_sum(r);
+            ref = r;
+        } else if (h == 0) {
+            ref = ref_for(greatest() * sl2);
+            *ref_at = ref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(settled);
+        } else {
+            if (!warp_wait(settled, cnt.no & 1, ctx)) return false;
+            ref = *ref_at;
+        }
+        // (Where A is alone both parts of the weights take the scores' place, so the largest score decides before they are made:
+        // a weight of 2^15 fits fp16.)
+        float sum = 0.f;
+        if constexpr (alone)
+            top = greatest() * sl2;
+        else
+            sum = weights();
+        // (A row without a finite score has cnt.no reference yet, and asks for one. One whose scores are NaN, such as those
+        // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
+        const bool ask = alone ? top > ref + 15.f : ref == -INFINITY ? !isnan(sum) : sum > kMost;
+        const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, ask);
+        if (h == 0 && raise) {
+            // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
+            float f2 = 1.f;
+            const float to = raised();
+            const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+            if (last > 64) {
+                if (!warp_wait(second, cnt.step2 & 1, ctx)) return false;
+                if (*late_at == 0) f2 = f;
+            }
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, f2 != 1.f)) {
+#pragma unroll 1
+                for (int part = 0; part < (alone ? 2 : 1); ++part) {
+                    uint32_t t[32];
+                    tmem_ld32(s_at + 64 + 32 * part, t);
+                    tmem_wait_ld();
+                    tmem_use32(t);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
+                        t[i] = pack_half2(v.x * f2, v.y * f2);
+                    }
+                    tmem_st32(s_at + 64 + 32 * part, t);
+                }
+            }
+            scale_sum(to);
+            ref = to;
+            *ref_at = ref;
+            scale_acc(f);
+            if constexpr (!alone) sum = weights();
+        } else if (h == 1) {
+            if (raise) {
+                if (lane == 0) *late_at = 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(second);
+                // the first half's products must be in the accumulator before it is scaled
+                if (!warp_wait(&bars.lo_done[x], step & 1, ctx)) return false;
+                tc_fence_after();
+                const float r = *ref_at;  // the first half may have raised it in this step
+                scale_sum(r);
+                ref = r;
+                const float to = raised();
+                const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                scale_sum(to);
+                ref = to;
+                *ref_at = ref;
+                scale_acc(f);
+                if constexpr (!alone) sum = weights();
+            } else if (lane == 0) {
+                *late_at = 0;
+            }
+        }
+        if constexpr (alone) sum = weights();
+        if (last > 64) ++cnt.step2;
+        l += sum;
+        parts[(cnt.no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
+        if constexpr (!alone) tmem_st32(s_at, ph);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (h == 1 && !raise) mbar_arrive(second);  // before the one that lets the first half's next step begin
+            mbar_arrive(&bars.p_full[x][h]);
+        }
+    }
+    if (!complete()) return false;
+    if (alone && x == 1) {  // A's warps read the accumulator
+        ++cnt.no;
+        return true;
+    }
+    tc_fence_after();
+    // The row's reference and sum: both halves', relative to the last reference (they only rise); those of both accumulators,
+    // of which one without a key that the row attends to counts for nothing.
+    auto scaled = [](float y, float f) { return y == INFINITY && f == 0.f ? 0.f : y * f; };  // NaN only where a score is
+    auto sum_of = [&](const float2* at, bool second_half) {
+        const float2 lo = at[0], hi = at[kRows];
+        if (!second_half) return lo;
+        const float top = fmaxf(lo.x, hi.x);
+        return make_float2(top, scaled(lo.y, lo.x == top ? 1.f : fast_exp2(lo.x - top)) +
+                                    scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
+    };
+    float2 y = sum_of(parts + (cnt.no & 1) * 4 * kRows, end > 64);
+    float fa = 1.f, fb = 0.f;  // factors of the accumulators
+    if (alone && both) {
+        const float2 yb = sum_of(parts + (cnt.nb & 1) * 4 * kRows + 2 * kRows, end - kRows > 64);
+        const bool some_a = y.y != 0.f, some_b = yb.y != 0.f;
+        const float top = some_b && (!some_a || yb.x > y.x) ? yb.x : y.x;
+        fa = !some_a ? 0.f : y.x == top ? 1.f : fast_exp2(y.x - top);
+        fb = !some_b ? 0.f : yb.x == top ? 1.f : fast_exp2(yb.x - top);
+        y = make_float2(top, (some_a ? scaled(y.y, fa) : 0.f) + (some_b ? scaled(yb.y, fb) : 0.f));
+        if (!some_a) fa = -1.f;
+        if (!some_b) fb = -1.f;
+    }
+    const float total = y.y;
+    auto fetch_o = [&](int c, uint32_t* o) {  // 32 of this half's dims
+        tmem_ld32(o_at + h * 64 + c * 32, o);
+        tmem_wait_ld();
+        tmem_use32(o);
+        if (alone && both) {
+            uint32_t ob[32];
+            tmem_ld32(o_at + 128 + h * 64 + c * 32, ob);
+            tmem_wait_ld();
+            tmem_use32(ob);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint((fa < 0.f ? 0.f : __uint_as_float(o[i]) * fa) +
+                                       (fb < 0.f ? 0.f : __uint_as_float(ob[i]) * fb));
+        }
+        if (c == 1) have_read();  // the next tiles' products may overwrite them
+    };
+    const bool mine = first_token() + row / G < end;
+    const int state = w.state;
+    if (state >= 0) {  // columns in fours, rows side by side
+        float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)state * 2 + x) * 32 + h * 16) * kRows + row;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            fetch_o(c, o);
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[(c * 8 + i) * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+        }
+        if (h == 0 && mine) p.ml[((int64_t)state * 2 + x) * kRows + row] = y;
+        ++cnt.no;
+        cnt.nb += both;
+        return true;
+    }
+    const float inv = 1.f / total;
+    __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
+    const __half2 zero = probe;
+    // Four lanes exchange 16-byte pieces of their rows, so that they store 64 consecutive bytes of one row at a time
+    // (16 bytes of 32 rows an instruction took 1.7 us a tile).
+    const int q4 = lane & 3;
+    __half* dst[4];
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (row & ~3) + i, t = w.t0 + x * kTokens + r / G;
+        in[i] = first_token() + r / G < end;
+        dst[i] = static_cast<__half*>(p.out) + (int64_t)(w.q.first + t) * p.out_stride + (w.h * G + r % G) * kHeadDim +
+                 h * 64 + q4 * 8;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t o[32], y[4][4];
+        fetch_o(c, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
+            const uint32_t u = pack_half2(a, b);
+            probe = __hfma2(*reinterpret_cast<const __half2*>(&u), zero, probe);
+            y[i >> 2][i & 3] = u;
+        }
+#pragma unroll
+        for (int s = 1; s < 4; s <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!(i & s))
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, q4 & s ? y[i][e] : y[i + s][e], s);
+                        (q4 & s ? y[i][e] : y[i + s][e]) = got;
+                    }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+    }
+    ++cnt.no;
+    cnt.nb += both;
+    // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
+    // themselves 1, or above 1/2.
+    const bool low_sum = !(total >= 0.25f);
+    const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
+    const unsigned again = __ballot_sync(0xffffffffu, mine && odd && !isnan(total));
+    if (again) {
+        const unsigned redo = __ballot_sync(0xffffffffu, low_sum) & again;
+        __syncwarp();  // the rows were stored by other lanes
+        finish_rows<G>(p, Seq{w.q.first, w.q.n, w.q.start}, w.s, w.t0 + x * kTokens + (row & ~31) / G, w.h, h, again, redo);
+    }
+    return true;
+}
+
+// A call of its own: inlined next to the other, it takes registers from it (8192 tokens 370 -> 396 us).
+template <int G>
+__device__ __noinline__ bool softmax_alone(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w, WaitCtx ctx,
+                                           Counts& cnt) {
+    return softmax_tile<G, true>(p, smem, tmem, w, ctx, cnt);
+}
+
 // ---- the tensor-core kernel ---------------------------------------------------------------------------------------
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params prm) {
@@ -310,22 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const ChunkParams& p = prm.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + off_bars);
-    uint64_t* kv_empty = kv_full + kStages;
-    uint64_t* w_full = kv_empty + kStages;  // the CTA's next work has been published
-    uint64_t* w_empty = w_full + 1;         // every warp has taken it
-    uint64_t* q_full = w_empty + 1;       // [2], like those below: tile A, tile B
-    uint64_t* q_empty = q_full + 2;
-    uint64_t* s_full = q_empty + 2;       // the tile's scores are in TMEM
-    uint64_t* p_full = s_full + 2;        // [2][2]: its weights of the step's first, second 64 keys are
-    uint64_t* o_full = p_full + 4;        // its accumulator is complete
-    uint64_t* lo_done = o_full + 2;       // the products of a step's first 64 keys are in the accumulator
-    uint64_t* o_free = lo_done + 2;       // the accumulator has been read
-    uint64_t* first_ref = o_free + 2;     // [tile][warp of the half]: the tile's first references are in shared memory
-    uint64_t* half_done = first_ref + 8;  // [tile][warp of the half]: the second half has settled its weights of the step
-    uint64_t* tail_full = half_done + 8;  // [2]: a tile of V with rows behind the pair's last key has come
-    uint64_t* drain = tail_full + 2;
-    Work* work = reinterpret_cast<Work*>(smem + off_work);
+    Bars& bars = *reinterpret_cast<Bars*>(smem + off_bars);
+    const Work* work = reinterpret_cast<const Work*>(smem + off_work);  // [2]
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
     int64_t* scan = reinterpret_cast<int64_t*>(smem + off_scan);
@@ -334,48 +765,51 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const WaitCtx ctx{abort_flag, &p.hdr->status, p.wait_ns};
 
     grid_launch_dependents();
-    // The line of steps: every thread sums a run of sequences (the first one's bounds are on their way while the barriers are
-    // set up), the CTA scans the sums, and the thread whose run holds the piece's first step finds its sequence.
-    const int per = ceil_div(p.num_seqs, kThreads);
-    const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
+    // The line: up to 32 sequences are scanned by the warp that walks the piece, a lane each. Of more, every thread sums a run
+    // (the first one's bounds are on their way while the barriers are set up), the CTA scans the sums, and the thread whose
+    // run holds the piece's first unit finds its sequence.
+    const bool few = p.num_seqs <= 32;
+    const int per = few ? 1 : ceil_div(p.num_seqs, kThreads);
+    const int self = few ? (warp == 18 ? lane : p.num_seqs) : (int)threadIdx.x * per;
+    const int s0 = min(p.num_seqs, self), s1 = min(p.num_seqs, s0 + per);
     bool bad = false;
     Seq sq0{0, 0, 0};
     if (s0 < s1) sq0 = load_seq(p, s0, bad);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&bars.kv_full[i], 1);
+            mbar_init(&bars.kv_empty[i], 1);
         }
-        mbar_init(w_full, 1);
-        mbar_init(w_empty, kSoftmax / 32 + 3);  // and warps 16, 17, 19
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[2 * i], 4);  // one arrival a warp
-            mbar_init(&p_full[2 * i + 1], 4);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&lo_done[i], 1);
-            mbar_init(&o_free[i], 8);
-            mbar_init(&tail_full[i], 1);
+            mbar_init(&bars.w_full[i], 1);
+            mbar_init(&bars.w_empty[i], kSoftmax / 32 + 3);  // and warps 16, 17, 19
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i][0], 4);  // one arrival a warp
+            mbar_init(&bars.p_full[i][1], 4);
+            mbar_init(&bars.o_full[i], 1);
+            mbar_init(&bars.lo_done[i], 1);
+            mbar_init(&bars.o_free[i], 8);
         }
         for (int i = 0; i < 8; ++i) {
-            mbar_init(&first_ref[i], 1);
-            mbar_init(&half_done[i], 1);
+            mbar_init(&bars.first_ref[0][i], 1);
+            mbar_init(&bars.half_done[0][i], 1);
         }
-        mbar_init(drain, 1);
+        mbar_init(&bars.tail_full, 1);
+        mbar_init(&bars.drain, 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
     if (warp == 16) tmem_alloc(tmem_at, 512);
-    int64_t mine = s0 < s1 ? steps_of<G>(sq0) : 0;
+    int64_t mine = s0 < s1 ? cost_of<G>(sq0) : 0;
     for (int s = s0 + 1; s < s1; ++s) {
         bool b;
-        mine += steps_of<G>(load_seq(p, s, b));
+        mine += cost_of<G>(load_seq(p, s, b));
         bad |= b;
     }
     if (bad && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
-    const int64_t head_groups = p.Hkv / p.lanes;
+    const int head_groups = p.Hkv / p.lanes, group = blockIdx.x / p.lanes;
     mine *= head_groups;
     int64_t incl = mine;
 #pragma unroll
@@ -389,25 +823,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
     int64_t before = incl - mine, total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = few ? 18 : 0; i < (few ? 19 : kThreads / 32); ++i) {
         if (i < warp) before += scan[i];
         total += scan[i];
     }
-    const int group = blockIdx.x / p.lanes;
-    const int pieces = (int)min((int64_t)(gridDim.x / p.lanes), (total + kMinSteps - 1) / kMinSteps);
+    const int pieces = (int)min((int64_t)(gridDim.x / p.lanes), (total + kMinCost - 1) / kMinCost);
     const int64_t lo = group < pieces ? group * total / pieces : 0, hi = group < pieces ? (group + 1) * total / pieces : 0;
-    if (lo < hi && before <= lo && lo < before + mine) {
-        int64_t at = before;
-        for (int s = s0; s < s1; ++s) {
-            bool b;
-            const int64_t n = steps_of<G>(s == s0 ? sq0 : load_seq(p, s, b)) * head_groups;
-            if (lo < at + n) {
-                *begin_seq = s;
-                *begin_off = lo - at;
-                break;
+    if (!few) {
+        if (lo < hi && before <= lo && lo < before + mine) {
+            int64_t at = before;
+            for (int s = s0; s < s1; ++s) {
+                bool b;
+                const int64_t n = cost_of<G>(s == s0 ? sq0 : load_seq(p, s, b)) * head_groups;
+                if (lo < at + n) {
+                    *begin_seq = s;
+                    *begin_off = lo - at;
+                    break;
+                }
+                at += n;
             }
-            at += n;
         }
+        __syncthreads();
     }
     if (p.seq_lens) {  // rows without a token get 0
         for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
@@ -417,69 +853,96 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + (int64_t)s * p.out_stride)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    __syncthreads();
 
     if (warp >= kSoftmax / 32) {
         regs_shrink<kOtherRegs>();
         if (warp == 18) {
             // ---------------------------------------------------------------------- the piece, pair after pair
             auto publish = [&](int k, const Work& w) {
-                if (k > 0 && !warp_wait(w_empty, (k - 1) & 1, ctx)) return false;
+                if (!warp_wait(&bars.w_empty[k & 1], ((k >> 1) & 1) ^ 1, ctx)) return false;
                 if (lane == 0) {
-                    *work = w;
-                    mbar_arrive(w_full);
+                    const_cast<Work*>(work)[k & 1] = w;
+                    mbar_arrive(&bars.w_full[k & 1]);
                 }
                 __syncwarp();
                 return true;
+            };
+            // Where a cut at `u` of a pair of cost `len` goes: to the pair's beginning or end where it is next to one (or where pieces
+            // are no more than a short pair).
+            const int near = total <= (int64_t)kWhole * pieces ? kWhole : 0;
+            auto snap = [&](int u, int len) {
+                if (len <= near) return 2 * u <= len ? 0 : len;
+                return u <= kPairCost ? 0 : u >= len - 1 ? len : u;
             };
             Merge merge{};
             int k = 0;
             bool ok = true;
             if (lo < hi) {
                 bool b;
-                int s = *begin_seq;
-                Seq q = load_seq(p, s, b);
-                int64_t of_head = steps_of<G>(q);
-                int hg = (int)(*begin_off / of_head);
-                const int64_t rest = *begin_off - hg * of_head;
+                int s;
+                int64_t rest;
+                auto take = [&](int i) {  // sequence i
+                    if (!few) return load_seq(p, i, b);
+                    return Seq{__shfl_sync(0xffffffffu, sq0.first, i), __shfl_sync(0xffffffffu, sq0.n, i),
+                               __shfl_sync(0xffffffffu, sq0.start, i)};
+                };
+                if (few) {
+                    s = __ffs(__ballot_sync(0xffffffffu, before <= lo && lo < before + mine)) - 1;
+                    rest = lo - __shfl_sync(0xffffffffu, before, s);
+                } else {
+                    s = *begin_seq;
+                    rest = *begin_off;
+                }
+                Seq q = take(s);
+                int hg = 0;
+                if (head_groups > 1) {
+                    const int64_t of_head = cost_of<G>(q);
+                    hg = (int)(rest / of_head);
+                    rest -= hg * of_head;
+                }
                 int left = 0, right = pairs_of<G>(q) - 1;  // the last pair that begins at or before `rest`
                 while (left < right) {
                     const int mid = (left + right + 1) >> 1;
-                    if (steps_before<G>(q, mid) <= rest)
+                    if (cost_before<G>(q, mid) <= rest)
                         left = mid;
                     else
                         right = mid - 1;
                 }
-                int pair = left, j = (int)(rest - steps_before<G>(q, pair));
-                for (int64_t pos = lo; pos < hi; ++k) {
+                int pair = left, u = (int)(rest - cost_before<G>(q, pair));
+                bool first = true;
+                for (int64_t at = lo - u; ok; first = false) {  // where the pair begins
                     Work w;
                     w.q = q;
                     w.s = s;
                     w.t0 = pair * 2 * kTokens;
                     w.h = hg * p.lanes + (int)(blockIdx.x % p.lanes);
-                    const int steps = ceil_div(keys_of<G>(q, w.t0), kRows);
-                    w.j0 = j;
-                    w.j1 = (int)min((int64_t)steps, j + (hi - pos));
-                    if (w.j1 <= w.j0) break;  // (only where the lengths change under the kernel, like the one below)
-                    const bool whole = w.j0 == 0 && w.j1 == steps;
-                    w.state = whole ? -1 : 2 * (int)blockIdx.x + (j == 0);
-                    if (!whole && j == 0) merge = Merge{q, s, w.t0, w.h, piece_of(pos + steps - 1, total, pieces) - group + 1, 0};
-                    ok = publish(k, w);
-                    if (!ok) break;
-                    pos += w.j1 - w.j0;
-                    j = 0;
+                    const int steps = ceil_div(keys_of<G>(q, w.t0), kRows), len = steps + kPairCost;
+                    if (first) u = snap(u, len);
+                    const int end = at + len <= hi ? len : snap((int)(hi - at), len);
+                    if (end > u) {
+                        w.j0 = max(0, u - kPairCost);  // (a cut leaves the pair's own cost to its first piece)
+                        w.j1 = end - kPairCost;
+                        const bool whole = w.j0 == 0 && w.j1 == steps;
+                        w.state = whole ? -1 : 2 * (int)blockIdx.x + (w.j0 == 0);
+                        if (!whole && w.j0 == 0) {
+                            int e = piece_of(at + len - 1, total, pieces);
+                            while (e > group && snap((int)((int64_t)e * total / pieces - at), len) == len) --e;
+                            merge = Merge{q, s, w.t0, w.h, e - group + 1, 0};
+                        }
+                        ok = publish(k++, w);
+                    }
+                    at += len;
+                    u = 0;
+                    if (at >= hi) break;
                     if (++pair == pairs_of<G>(q)) {
                         pair = 0;
                         if (++hg == head_groups) {
                             hg = 0;
                             do {
                                 if (++s >= p.num_seqs) break;
-                                q = load_seq(p, s, b);
+                                q = take(s);
                             } while (q.n == 0);
-                            if (s >= p.num_seqs) {
-                                ++k;
-                                break;
-                            }
+                            if (s >= p.num_seqs) break;  // (only where the lengths change under the kernel)
                         }
                     }
                 }
@@ -490,106 +953,91 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 publish(k, w);
             }
             if (lane == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = merge;
-        } else if (warp == 17) {
-            // ------------------------------------------------------------------------------------- copies
+        } else if (warp == 17 || warp == 19) {
+            // ----------------------------------------------- copies: of queries and K (warp 17), of V (warp 19)
+            // (A page is four boxes, and a warp issues the boxes of its lanes one after the other: one warp for all of them leaves
+            // the tensor core waiting.)
+            const bool of_v = warp == 19;
+            const CUtensorMap* map = of_v ? &prm.v : &prm.k;
             if (lane == 0) {
-                prefetch_tensormap(&prm.q);
-                prefetch_tensormap(&prm.k);
-                prefetch_tensormap(&prm.v);
+                prefetch_tensormap(map);
+                if (!of_v) prefetch_tensormap(&prm.q);
             }
             uint64_t ordinary;
             asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(ordinary));
             const uint64_t stream = policy_evict_first();
-            int seq = 0, nq[2] = {0, 0}, nc = 0;
+            int seq = of_v ? 1 : 0, nq[2] = {0, 0}, nc = 0;  // ring position; tiles of queries; tiles that were cleared
+            const int seq0 = seq;
             bool stop = false;
             for (int k = 0; !stop; ++k) {
-                if (!warp_wait(w_full, k & 1, ctx)) break;
-                const Work w = *work;
+                if (!warp_wait(&bars.w_full[k & 1], (k >> 1) & 1, ctx)) break;
+                const Work w = work[k & 1];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_empty);
+                if (lane == 0) mbar_arrive(&bars.w_empty[k & 1]);
                 if (w.h < 0) break;
                 const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
                 const int npages = ceil_div(end, kPageSize);
-                auto entries = [&](int lp) {  // a lane's page among 32; where the pair has no more, any
-                    const int page = lp < npages ? page_of(p, w.s, w.h, lp) : 0;
-                    return page;
-                };
+                auto entries = [&](int lp) { return lp < npages ? page_of(p, w.s, w.h, lp) : 0; };
                 int next = entries(w.j0 * kStepPages + lane), ent = 0;
                 auto load_q = [&](int x) {
                     if (tile_end(w, x, kTokens) <= w.j0 * kRows) return true;
-                    if (!warp_wait(&q_empty[x], (nq[x] & 1) ^ 1, ctx)) return false;
+                    if (!warp_wait(&bars.q_empty[x], (nq[x] & 1) ^ 1, ctx)) return false;
                     if (lane == 0) {
                         uint8_t* dst = smem + off_q + x * kTileBytes;
-                        mbar_arrive_expect_tx(&q_full[x], kTileBytes);
+                        mbar_arrive_expect_tx(&bars.q_full[x], kTileBytes);
                         for (int b = 0; b < 2; ++b)
                             tma_load_3d(dst + b * kBoxBytes, &prm.q, b * 64, w.h * G, w.q.first + w.t0 + x * kTokens,
-                                        &q_full[x], stream);
+                                        &bars.q_full[x], stream);
                     }
                     __syncwarp();
                     ++nq[x];
                     return true;
                 };
-                auto load_kv = [&](const CUtensorMap* map, int j, bool tail = false) {  // tail: comes by way of warp 19
-                    const int st = seq % kStages;
-                    uint64_t* bar = tail ? &tail_full[nc & 1] : &kv_full[st];
-                    if (!warp_wait(&kv_empty[st], ((seq / kStages) & 1) ^ 1, ctx)) return false;
-                    const int n = min(kStepPages, npages - j * kStepPages);
-                    // lane 2 i + half: half of the dims of the step's page i
-                    const int page = __shfl_sync(0xffffffffu, ent, ((j - w.j0) & 3) * kStepPages + ((lane >> 1) & 7));
-                    if (lane == 0) mbar_arrive_expect_tx(bar, n * 2 * kPageBox);
-                    __syncwarp();
-                    if (lane < 2 * n)
-                        tma_load_3d(smem + off_ring + st * kTileBytes + (lane & 1) * kBoxBytes + (lane >> 1) * kPageBox, map,
-                                    (lane & 1) * 64, w.h, page * kPageSize, bar, ordinary);
-                    __syncwarp();
-                    ++seq;
-                    nc += tail;
-                    return true;
-                };
-                for (int j = w.j0; j < w.j1 && !stop; ++j) {
+                for (int j = w.j0; j < w.j1; ++j) {
                     if (((j - w.j0) & 3) == 0) {  // 32 entries serve four steps; the next 32 are on their way meanwhile
                         ent = next;
                         if (ent == p.num_pages) raise_status(ctx.status, PKV_STATUS_BAD_PAGE);
                         if (j + 4 < w.j1) next = entries((j + 4) * kStepPages + lane);
                     }
-                    if (j == w.j0) stop = !load_q(0);
-                    stop = stop || !load_kv(&prm.k, j);
-                    if (j == w.j0) stop = stop || !load_q(1);
-                    stop = stop || !load_kv(&prm.v, j, (j + 1) * kRows >= end && (end & 15));
+                    stop = !of_v && j == w.j0 && !load_q(0);
+                    const int st = seq % kStages, n = min(kStepPages, npages - j * kStepPages);
+                    stop = stop || !warp_wait(&bars.kv_empty[st], ((seq / kStages) & 1) ^ 1, ctx);
+                    if (stop) break;
+                    // The products' last step of 16 keys reads rows behind the pair's last key, which may hold anything: in V they are
+                    // cleared before the tile counts as loaded.
+                    const bool tail = of_v && (j + 1) * kRows >= end && (end & 15);
+                    uint64_t* bar = tail ? &bars.tail_full : &bars.kv_full[st];
+                    uint8_t* dst = smem + off_ring + st * kTileBytes;
+                    // lane 2 i + half: half of the dims of the step's page i
+                    const int page = __shfl_sync(0xffffffffu, ent, ((j - w.j0) & 3) * kStepPages + ((lane >> 1) & 7));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, n * 2 * kPageBox);
+                    __syncwarp();
+                    if (lane < 2 * n)
+                        tma_load_3d(dst + (lane & 1) * kBoxBytes + (lane >> 1) * kPageBox, map, (lane & 1) * 64, w.h, page * kPageSize,
+                                    bar, ordinary);
+                    __syncwarp();
+                    seq += 2;
+                    if (tail) {
+                        nc += 1;
+                        stop = !warp_wait(&bars.tail_full, (nc - 1) & 1, ctx);
+                        if (stop) break;
+                        const int first = end - j * kRows, last = (first + 15) & ~15;
+                        for (int i = first * 16 + lane; i < last * 16; i += 32)
+                            *reinterpret_cast<uint4*>(dst + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.kv_full[st]);
+                    }
+                    stop = !of_v && j == w.j0 && !load_q(1);
+                    if (stop) break;
                 }
             }
             // every copy that this warp issued lands before the CTA may end
-            for (int j = max(0, nc - 2); j < nc; ++j) warp_drain(&tail_full[j & 1], (j >> 1) & 1);
-            for (int j = max(0, seq - kStages); j < seq; ++j) warp_drain(&kv_full[j % kStages], (j / kStages) & 1);
+            if (nc > 0) warp_drain(&bars.tail_full, (nc - 1) & 1);
+            for (int j = max(seq0, seq - kStages); j < seq; j += 2) warp_drain(&bars.kv_full[j % kStages], (j / kStages) & 1);
             for (int x = 0; x < 2; ++x)
-                if (nq[x] > 0) warp_drain(&q_full[x], (nq[x] - 1) & 1);
-        } else if (warp == 19) {
-            // ------------------------------------------------------------------------ rows behind the pair's last key
-            // The products' last step of 16 keys reads them, and they may hold anything.
-            int kv = 0, nc = 0;
-            for (int k = 0;; ++k) {
-                if (!warp_wait(w_full, k & 1, ctx)) break;
-                const Work w = *work;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(w_empty);
-                if (w.h < 0) break;
-                const int end = max(tile_end(w, 0, kTokens), tile_end(w, 1, kTokens));
-                kv += 2 * (w.j1 - w.j0);
-                if ((end & 15) == 0 || w.j1 * kRows < end) continue;
-                const int pos = kv - 1;
-                // (Two barriers: the loader may be one such tile ahead, but not two, as it gets a work when every warp has
-                // taken the one before.)
-                if (!warp_wait(&tail_full[nc & 1], (nc >> 1) & 1, ctx)) break;
-                ++nc;
-                uint8_t* v = smem + off_ring + (pos % kStages) * kTileBytes;
-                const int first = end - (w.j1 - 1) * kRows, last = (first + 15) & ~15;
-                for (int i = first * 16 + lane; i < last * 16; i += 32)
-                    *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kBoxBytes + (i >> 4) * 128 + (i & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kv_full[pos % kStages]);
-            }
+                if (nq[x] > 0) warp_drain(&bars.q_full[x], (nq[x] - 1) & 1);
         } else if (warp == 16) {
             // ------------------------------------------------------------------------- matrix instructions
             if (elect_one()) {  // one thread waits for and issues everything
@@ -598,427 +1046,154 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 int np[2][2] = {{0, 0}, {0, 0}};     // halves of steps taken
                 bool ok = true;
                 for (int k = 0; ok; ++k) {
-                    if (!thread_wait(w_full, k & 1, ctx)) break;
-                    const Work w = *work;
-                    mbar_arrive(w_empty);
+                    if (!thread_wait(&bars.w_full[k & 1], (k >> 1) & 1, ctx)) break;
+                    const Work w = work[k & 1];
+                    mbar_arrive(&bars.w_empty[k & 1]);
                     if (w.h < 0) break;
                     // keys from the piece's first on, up to its last
-                    const int most = (w.j1 - w.j0) * kRows;
+                    const int steps = w.j1 - w.j0, most = steps * kRows;
                     const int end0 = min(tile_end(w, 0, kTokens) - w.j0 * kRows, most);
                     const int end1 = min(tile_end(w, 1, kTokens) - w.j0 * kRows, most);
-                    const int steps = w.j1 - w.j0;
                     // ring positions: K_j at kv + 2j, V_j one behind it
                     const uint32_t ring = smem_addr(smem + off_ring);
                     auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
-                    auto wait_stage = [&](int pos) { return thread_wait(&kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
-                    // keys of the piece's step j that tile x needs (0: none)
-                    auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
-                    auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
-                        const int n = (keys(x, j) + 15) & ~15;
-                        if (n == 0) return;
-                        const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
-                        const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
-                        const uint32_t idesc = mma_idesc(n, false);
-                        const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
-                        mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, idesc);
-                        mma_commit(&s_full[x]);
-                        if (last) mma_commit(&q_empty[x]);
-                    };
-                    auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
-                        const int n = (keys(x, j) + 15) >> 4;
-                        if (n == 0) return true;
-                        constexpr uint32_t idesc = mma_idesc(kHeadDim, true);
-                        const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
-                        const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
-                        const bool last = keys(x, j + 1) == 0;
-                        if (j == 0) {  // the previous tile's rows have been read
-                            if (!thread_wait(&o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
-                            ++no[x];
-                        }
+                    auto wait_stage = [&](int pos) { return thread_wait(&bars.kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
+                    auto release = [&](int pos) { mma_commit(&bars.kv_empty[pos % kStages]); };
+                    constexpr uint32_t idesc_v = mma_idesc(kHeadDim, true);
+                    if (tile_b(w, kTokens)) {
+                        // keys of the piece's step j that tile x needs (0: none)
+                        auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
+                        auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
+                            const int n = (keys(x, j) + 15) & ~15;
+                            if (n == 0) return;
+                            const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
+                            const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
+                            const uint32_t idesc = mma_idesc(n, false);
+                            const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
+                            mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, idesc);
+                            mma_commit(&bars.s_full[x]);
+                            if (last) mma_commit(&bars.q_empty[x]);
+                        };
+                        auto values = [&](int x, int j) {  // O_x += P_x(j) V_j
+                            const int n = (keys(x, j) + 15) >> 4;
+                            if (n == 0) return true;
+                            const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
+                            const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128;
+                            const bool last = keys(x, j + 1) == 0;
+                            if (j == 0) {  // the previous tile's rows have been read
+                                if (!thread_wait(&bars.o_free[x], (no[x] & 1) ^ 1, ctx)) return false;
+                                ++no[x];
+                            }
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {  // 64 keys each
-                            const int c = min(4, n - 4 * half);  // steps of 16 keys
-                            if (c <= 0) break;
-                            if (!thread_wait(&p_full[2 * x + half], np[x][half] & 1, ctx)) return false;
-                            ++np[x][half];
+                            for (int half = 0; half < 2; ++half) {  // 64 keys each
+                                const int c = min(4, n - 4 * half);  // steps of 16 keys
+                                if (c <= 0) break;
+                                if (!thread_wait(&bars.p_full[x][half], np[x][half] & 1, ctx)) return false;
+                                ++np[x][half];
+                                tc_fence_after();
+                                if (c == 4)
+                                    mma_ts_64(o, pw + 64 * half, v + 512 * half, idesc_v, j > 0 || half > 0);
+                                else
+                                    for (int i = 0; i < c; ++i)
+                                        mma_ts(o, pw + 64 * half + 8 * i, v + 512 * half + 128 * i, idesc_v, j > 0 || half > 0 || i > 0);
+                                if (half == 0) mma_commit(&bars.lo_done[x]);
+                                if (last && n - 4 * half <= 4) mma_commit(&bars.o_full[x]);
+                            }
+                            return true;
+                        };
+                        ok = wait_stage(kv);
+                        for (int x = 0; x < 2 && ok; ++x) {
+                            if (keys(x, 0) == 0) continue;
+                            ok = thread_wait(&bars.q_full[x], nq[x] & 1, ctx);
+                            ++nq[x];
                             tc_fence_after();
-                            if (c == 4)
-                                mma_ts_64(o, pw + 64 * half, v + 512 * half, idesc, j > 0 || half > 0);
-                            else
-                                for (int i = 0; i < c; ++i)
-                                    mma_ts(o, pw + 64 * half + 8 * i, v + 512 * half + 128 * i, idesc, j > 0 || half > 0 || i > 0);
-                            if (half == 0) mma_commit(&lo_done[x]);
-                            if (last && n - 4 * half <= 4) mma_commit(&o_full[x]);
+                            if (ok) scores(x, 0);
                         }
-                        return true;
-                    };
-                    auto release = [&](int pos) { mma_commit(&kv_empty[pos % kStages]); };
-                    ok = wait_stage(kv);
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (keys(x, 0) == 0) continue;
-                        ok = thread_wait(&q_full[x], nq[x] & 1, ctx);
-                        ++nq[x];
-                        tc_fence_after();
-                        if (ok) scores(x, 0);
-                    }
-                    if (!ok) break;
-                    release(kv);
-                    for (int j = 0; j < steps && ok; ++j) {
-                        ok = wait_stage(kv + 2 * j + 1) && values(0, j);
-                        if (ok && j + 1 < steps) {
-                            ok = wait_stage(kv + 2 * j + 2);
-                            if (ok) scores(0, j + 1);
-                        }
-                        ok = ok && values(1, j);
                         if (!ok) break;
-                        release(kv + 2 * j + 1);
-                        if (j + 1 < steps) {
-                            scores(1, j + 1);
-                            release(kv + 2 * j + 2);
+                        release(kv);
+                        for (int j = 0; j < steps && ok; ++j) {
+                            ok = wait_stage(kv + 2 * j + 1) && values(0, j);
+                            if (ok && j + 1 < steps) {
+                                ok = wait_stage(kv + 2 * j + 2);
+                                if (ok) scores(0, j + 1);
+                            }
+                            ok = ok && values(1, j);
+                            if (!ok) break;
+                            release(kv + 2 * j + 1);
+                            if (j + 1 < steps) {
+                                scores(1, j + 1);
+                                release(kv + 2 * j + 2);
+                            }
+                        }
+                    } else {
+                        // A alone: its odd steps are B's. (The same in general terms for both: its operands leave the uniform registers, and
+                        // pairs take 7 % longer.)
+                        ok = thread_wait(&bars.q_full[0], nq[0] & 1, ctx);
+                        ++nq[0];
+                        tc_fence_after();
+                        const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q));
+                        for (int i = 0; i < steps + 2 && ok; ++i) {  // values of step i - 2, scores of step i
+                            const int x = i & 1, j = i - 2;
+                            if (j >= 0) {
+                                const int n = (min(kRows, end0 - j * kRows) + 15) >> 4;
+                                ok = wait_stage(kv + 2 * j + 1);
+                                if (ok && j < 2) {
+                                    ok = thread_wait(&bars.o_free[x], (no[x] & 1) ^ 1, ctx);
+                                    ++no[x];
+                                }
+                                const uint64_t v = smem_desc_mn_major(stage_addr(kv + 2 * j + 1), kBoxBytes);
+                                for (int half = 0; half < 2 && 4 * half < n && ok; ++half) {
+                                    ok = thread_wait(&bars.p_full[x][half], np[x][half] & 1, ctx);
+                                    ++np[x][half];
+                                    tc_fence_after();
+                                    for (int k16 = 0; k16 < min(4, n - 4 * half); ++k16) {  // 32 keys: 16 columns of first parts, 16 of second
+                                        const uint32_t at = tmem + x * 128 + 64 * half + 32 * (k16 >> 1) + 8 * (k16 & 1);
+                                        const uint64_t vk = v + 512 * half + 128 * k16;
+                                        mma_ts(tmem + 256 + x * 128, at, vk, idesc_v, j > 1 || half > 0 || k16 > 0);
+                                        mma_ts(tmem + 256 + x * 128, at + 16, vk, idesc_v, true);
+                                    }
+                                    if (half == 0) mma_commit(&bars.lo_done[x]);
+                                    if (j + 2 >= steps && n - 4 * half <= 4) mma_commit(&bars.o_full[x]);
+                                }
+                                if (!ok) break;
+                                release(kv + 2 * j + 1);
+                            }
+                            if (i < steps) {
+                                ok = wait_stage(kv + 2 * i);
+                                const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * i));
+                                mma_ss_128<kBoxBytes / 16>(tmem + x * 128, q, kd, mma_idesc((min(kRows, end0 - i * kRows) + 15) & ~15, false));
+                                mma_commit(&bars.s_full[x]);
+                                release(kv + 2 * i);
+                                if (i + 1 == steps) mma_commit(&bars.q_empty[0]);
+                            }
                         }
                     }
                     kv += 2 * steps;
                 }
-                mma_commit(drain);
+                mma_commit(&bars.drain);
             }
             __syncwarp();
             // every matrix instruction has completed before the TMEM is freed and the CTA ends
-            warp_drain(drain, 0);
+            warp_drain(&bars.drain, 0);
         }
     } else {
         // ---------------------------------------------------------------------------- softmax and output rows
         regs_grow<kSoftmaxRegs>();
-        const int x = warp >> 3, h = (warp >> 2) & 1;  // tile, half of the keys (and of the output's dims)
-        const int row = threadIdx.x & 127;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + x * 128 + h * 64;  // this half's scores, and its weights over the first 32
-        const uint32_t o_at = tmem + lanes + 256 + x * 128;
-        volatile float* ref_at = reinterpret_cast<volatile float*>(smem + off_ref) + x * kRows + row;
-        float2* parts = reinterpret_cast<float2*>(smem + off_parts) + x * 2 * kRows + row;  // + buffer * 4 kRows + half * kRows
-        uint64_t* settled = &first_ref[x * 4 + (warp & 3)];
-        uint64_t* second = &half_done[x * 4 + (warp & 3)];
-        volatile int* late_at = reinterpret_cast<volatile int*>(smem + off_late) + x * 4 + (warp & 3);
-        const float sl2 = p.scale_log2;
-        const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
-        int ns = 0, no = 0;  // steps, tiles taken
-        int step2 = 0;       // steps with keys in the second half, as the first half counts them
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            if (!warp_wait(w_full, k & 1, ctx)) break;
-            const Work w = *work;
+        Counts counts{0, 0, 0, 0};
+        for (int k = 0;; ++k) {
+            // The slot is kept while it is worked on: what a step does not need is not kept in registers.
             __syncwarp();
-            if (lane == 0) mbar_arrive(w_empty);
+            if (k > 0 && lane == 0) mbar_arrive(&bars.w_empty[(k - 1) & 1]);
+            if (!warp_wait(&bars.w_full[k & 1], (k >> 1) & 1, ctx)) break;
+            const volatile Work& w = reinterpret_cast<const volatile Work*>(work)[k & 1];
             if (w.h < 0) break;
-            const int end = tile_end(w, x, kTokens);
-            const int j1 = min(w.j1, ceil_div(end, kRows));  // the tile's steps of this piece: j0 .. j1 - 1
-            const int token = w.t0 + x * kTokens + row / G;
-            const bool mine = token < w.q.n;
-            float2* state_ml = p.ml + ((int64_t)w.state * 2 + x) * kRows + row;
-            if (j1 <= w.j0) {  // tile A may end before the piece begins
-                if (w.state >= 0 && h == 0 && mine) *state_ml = make_float2(-INFINITY, 0.f);
-                continue;
-            }
-            const bool idle = w.t0 + x * kTokens + (row & ~31) / G >= w.q.n;  // none of the warp's rows is one
-            float ref = -INFINITY, l = 0.f;
-            for (int j = w.j0; j < j1; ++j) {
-                const int step = ns++;
-                const int last = end - j * kRows - h * 64;  // keys of this half, counted from its first
-                // The tile's last step ends in the first half: the second does not wait for its scores (nothing would keep
-                // the next tile's from coming before it looks, and a parity two phases on does not pass). They have come
-                // when the tile's accumulator is complete, for which it waits below.
-                if (last <= 0) continue;
-                if (!warp_wait(&s_full[x], step & 1, ctx)) {
-                    ok = false;
-                    break;
-                }
-                if (idle) {  // it keeps the count of arrivals; nothing reads its rows of the accumulator
-                    if (last > 64) ++step2;
-                    if (lane == 0) {
-                        if (h == 0 && j == w.j0) mbar_arrive(settled);
-                        if (h == 1) mbar_arrive(second);
-                        mbar_arrive(&p_full[2 * x + h]);
-                    }
-                    __syncwarp();
-                    continue;
-                }
-                tc_fence_after();
-                // Steps with keys behind the tile's first token are masked; the others are whole.
-                const bool tail = (j + 1) * kRows > w.q.start + w.t0 + x * kTokens;
-                const int lim = tail ? min(w.q.start + token, end - 1) - j * kRows - h * 64 : 64;
-                auto fetch = [&](int c, uint32_t* r) {  // 32 of the row's scores
-                    tmem_ld32(s_at + c * 32, r);
-                    tmem_wait_ld();
-                    tmem_use32(r);
-                    if (tail) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i > lim) r[i] = 0xff800000u;  // -inf
-                    }
-                };
-                auto greatest = [&]() {
-                    float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (c * 32 < last) {
-                            uint32_t r[32];
-                            fetch(c, r);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                m0 = fmaxf(m0, __uint_as_float(r[i]));
-                                m1 = fmaxf(m1, __uint_as_float(r[i + 1]));
-                            }
-                        }
-                    }
-                    return fmaxf(m0, m1);
-                };
-                uint32_t ph[32];  // the weights, in fp16
-                auto weights = [&]() {  // returns their sum
-                    const float nref = ref == -INFINITY ? 0.f : -ref;
-                    const uint64_t refx2 = pack_f32x2(nref, nref);
-                    uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (c * 32 < last) {
-                            uint32_t r[32];
-                            fetch(c, r);
-                            const float* f = reinterpret_cast<const float*>(r);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float a, b;
-                                unpack_f32x2(fma_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), sl2x2, refx2), a, b);
-                                a = fast_exp2(a);
-                                b = fast_exp2(b);
-                                if (i & 1)
-                                    sum1 = add_f32x2(sum1, pack_f32x2(a, b));
-                                else
-                                    sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-                                ph[c * 16 + i] = pack_half2(a, b);
-                            }
-                        }
-                    }
-                    float a, b;
-                    unpack_f32x2(add_f32x2(sum0, sum1), a, b);
-                    return a + b;
-                };
-                // Scales what has been accumulated up to now (this thread's sum; the row's accumulator).
-                auto scale_sum = [&](float to) {
-                    if (to != ref) {
-                        const float f = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
-                        l = l == INFINITY && f == 0.f ? 0.f : l * f;  // NaN only where a score is
-                    }
-                };
-                auto scale_acc = [&](float f) {
-                    const uint64_t ff = pack_f32x2(f, f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t t[32];
-                        tmem_ld32(o_at + c * 32, t);
-                        tmem_wait_ld();
-                        tmem_use32(t);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a, b;
-                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), ff), a, b);
-                            t[i] = __float_as_uint(a);
-                            t[i + 1] = __float_as_uint(b);
-                        }
-                        tmem_st32(o_at + c * 32, t);
-                    }
-                };
-                // The reference that this half's keys ask for: above the present one by a whole number.
-                auto raised = [&]() {
-                    const float to = ref_for(greatest() * sl2);
-                    return ref == -INFINITY ? to : to > ref ? ref + ceilf(to - ref) : ref;
-                };
-                if (j > w.j0) {  // the other half may have raised it in the step before
-                    const float r = *ref_at;
-                    scale_sum(r);
-                    ref = r;
-                } else if (h == 0) {
-                    ref = ref_for(greatest() * sl2);
-                    *ref_at = ref;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(settled);
-                } else {
-                    if (!warp_wait(settled, no & 1, ctx)) {
-                        ok = false;
-                        break;
-                    }
-                    ref = *ref_at;
-                }
-                float sum = weights();
-                // (A row without a finite score has no reference yet, and asks for one. One whose scores are NaN, such as those
-                // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
-                const bool ask = ref == -INFINITY ? !isnan(sum) : sum > kMost;
-                const bool raise = (j > w.j0 || h == 1) && __any_sync(0xffffffffu, ask);
-                if (h == 0 && raise) {
-                    // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
-                    float f2 = 1.f;
-                    const float to = raised();
-                    const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
-                    if (last > 64) {
-                        if (!warp_wait(second, step2 & 1, ctx)) {
-                            ok = false;
-                            break;
-                        }
-                        if (*late_at == 0) f2 = f;
-                    }
-                    tc_fence_after();
-                    if (__any_sync(0xffffffffu, f2 != 1.f)) {
-                        uint32_t t[32];
-                        tmem_ld32(s_at + 64, t);
-                        tmem_wait_ld();
-                        tmem_use32(t);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
-                            t[i] = pack_half2(v.x * f2, v.y * f2);
-                        }
-                        tmem_st32(s_at + 64, t);
-                    }
-                    scale_sum(to);
-                    ref = to;
-                    *ref_at = ref;
-                    scale_acc(f);
-                    sum = weights();
-                } else if (h == 1) {
-                    if (raise) {
-                        if (lane == 0) *late_at = 1;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(second);
-                        // the first half's products must be in the accumulator before it is scaled
-                        if (!warp_wait(&lo_done[x], step & 1, ctx)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const float r = *ref_at;  // the first half may have raised it in this step
-                        scale_sum(r);
-                        ref = r;
-                        const float to = raised();
-                        const float f = to == ref ? 1.f : ref == -INFINITY ? 0.f : fast_exp2(ref - to);
-                        scale_sum(to);
-                        ref = to;
-                        *ref_at = ref;
-                        scale_acc(f);
-                        sum = weights();
-                    } else if (lane == 0) {
-                        *late_at = 0;
-                    }
-                }
-                if (last > 64) ++step2;
-                l += sum;
-                parts[(no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
-                tmem_st32(s_at, ph);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (h == 1 && !raise) mbar_arrive(second);  // before the one that lets the first half's next step begin
-                    mbar_arrive(&p_full[2 * x + h]);
-                }
-            }
-            if (!ok) break;
-            if (!warp_wait(&o_full[x], no & 1, ctx)) break;
-            if (idle) {
-                if (lane == 0) mbar_arrive(&o_free[x]);
-                __syncwarp();
-                ++no;
-                continue;
-            }
-            tc_fence_after();
-            // the row's sum: both halves', relative to the last reference (they only rise)
-            const float2 lo = parts[(no & 1) * 4 * kRows], hi = parts[(no & 1) * 4 * kRows + kRows];
-            float total = lo.y;
-            if (end - w.j0 * kRows > 64) {
-                const float top = fmaxf(lo.x, hi.x);
-                auto part = [&](const float2& x) {
-                    const float f = x.x == top ? 1.f : fast_exp2(x.x - top);
-                    return x.y == INFINITY && f == 0.f ? 0.f : x.y * f;
-                };
-                total = part(lo) + part(hi);
-            }
-            if (w.state >= 0) {  // columns in fours, rows side by side
-                float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)w.state * 2 + x) * 32 + h * 16) * kRows + row;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + h * 64 + c * 32, o);
-                    tmem_wait_ld();
-                    tmem_use32(o);
-                    if (c == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&o_free[x]);
-                    }
-                    if (mine) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[(c * 8 + i) * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-                    }
-                }
-                if (h == 0 && mine) *state_ml = make_float2(end - w.j0 * kRows > 64 ? fmaxf(lo.x, hi.x) : lo.x, total);
-                ++no;
-                continue;
-            }
-            const float inv = 1.f / total;
-            __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
-            const __half2 zero = probe;
-            // Four lanes exchange 16-byte pieces of their rows, so that they store 64 consecutive bytes of one row at a time
-            // (16 bytes of 32 rows an instruction took 1.7 us a tile).
-            const int q4 = lane & 3;
-            __half* dst[4];
-            bool in[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = (row & ~3) + i, t = w.t0 + x * kTokens + r / G;
-                in[i] = t < w.q.n;
-                dst[i] = static_cast<__half*>(p.out) + (int64_t)(w.q.first + t) * p.out_stride + (w.h * G + r % G) * kHeadDim +
-                         h * 64 + q4 * 8;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t o[32], y[4][4];
-                tmem_ld32(o_at + h * 64 + c * 32, o);
-                tmem_wait_ld();
-                tmem_use32(o);
-                if (c == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_free[x]);  // the next tile's products may overwrite it
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
-                    const uint32_t u = pack_half2(a, b);
-                    probe = __hfma2(*reinterpret_cast<const __half2*>(&u), zero, probe);
-                    y[i >> 2][i & 3] = u;
-                }
-#pragma unroll
-                for (int s = 1; s < 4; s <<= 1)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!(i & s))
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, q4 & s ? y[i][e] : y[i + s][e], s);
-                                (q4 & s ? y[i][e] : y[i + s][e]) = got;
-                            }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
-            }
-            ++no;
-            // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
-            // themselves 1, or above 1/2.
-            const bool low_sum = !(total >= 0.25f);
-            const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
-            const unsigned again = __ballot_sync(0xffffffffu, mine && odd && !isnan(total));
-            if (again) {
-                const unsigned redo = __ballot_sync(0xffffffffu, low_sum) & again;
-                __syncwarp();  // the rows were stored by other lanes
-                finish_rows<G>(p, w.q, w.s, w.t0 + x * kTokens + (row & ~31) / G, w.h, h, again, redo);
+            if (tile_b(w, kTokens)) {
+                if (!softmax_tile<G, false>(p, smem, tmem, w, ctx, counts)) break;
+            } else {
+                Counts c = counts;  // (of which the call takes the address)
+                const bool ok = softmax_alone<G>(p, smem, tmem, w, ctx, c);
+                counts = c;
+                if (!ok) break;
             }
         }
     }
@@ -1055,34 +1230,51 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
     const float2* ml = p.ml + row;
     const float4* acc = reinterpret_cast<const float4*>(p.acc) + ((row >> 7) * 32 + warp * 4) * kRows + (row & 127);
     auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i * p.lanes)); };
-    float top = -INFINITY;
-    bool nan = false;
-    for (int i = turn; i < m.pieces; i += span) {
-        const float2 x = __ldcg(ml + slot(i) * 2 * kRows);
-        nan |= isnan(x.y);
-        if (x.y > 0.f) top = fmaxf(top, x.x);
-    }
-    for (int o = rows; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float total = 0.f;
+    // Four states at a time, all of their loads in flight together.
+    constexpr int kBatch = 4;
+    float top = -INFINITY, total = 0.f;
     float4 sum[4] = {};
-#pragma unroll 2
-    for (int i = turn; i < m.pieces; i += span) {
-        const float2 x = __ldcg(ml + slot(i) * 2 * kRows);
-        float4 a[4];
+    bool nan = false;
+    auto scaled = [](float l, float f) { return l == INFINITY && f == 0.f ? 0.f : l * f; };  // NaN only where a score is
+    auto rescale = [&](float to) {
+        const float f = top == to ? 1.f : fast_exp2(top - to);
+        top = to;
+        total = scaled(total, f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) a[c] = __ldcg(acc + slot(i) * 2 * 32 * kRows + c * kRows);
-        if (x.y > 0.f) {  // a piece whose keys come behind the row's token has none
-            const float f = x.x == top ? 1.f : fast_exp2(x.x - top);
-            total += x.y == INFINITY && f == 0.f ? 0.f : x.y * f;
+        for (int c = 0; c < 4; ++c) sum[c] = make_float4(sum[c].x * f, sum[c].y * f, sum[c].z * f, sum[c].w * f);
+    };
+    for (int i0 = turn; i0 < m.pieces; i0 += kBatch * span) {
+        float2 x[kBatch];
+        float4 a[kBatch][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                sum[c].x += a[c].x * f;
-                sum[c].y += a[c].y * f;
-                sum[c].z += a[c].z * f;
-                sum[c].w += a[c].w * f;
-            }
+        for (int e = 0; e < kBatch; ++e) {
+            const int i = min(i0 + e * span, m.pieces - 1);
+            x[e] = __ldcg(ml + slot(i) * 2 * kRows);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[e][c] = __ldcg(acc + slot(i) * 2 * 32 * kRows + c * kRows);
         }
+        float to = top;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            if (i0 + e * span >= m.pieces) x[e].y = 0.f;
+            nan |= isnan(x[e].y);
+            if (x[e].y > 0.f) to = fmaxf(to, x[e].x);
+        }
+        rescale(to);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+            if (x[e].y > 0.f) {  // 0: keys behind the row's token alone
+                const float f = x[e].x == top ? 1.f : fast_exp2(x[e].x - top);
+                total += scaled(x[e].y, f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    sum[c] = make_float4(sum[c].x + a[e][c].x * f, sum[c].y + a[e][c].y * f, sum[c].z + a[e][c].z * f,
+                                         sum[c].w + a[e][c].w * f);
+            }
     }
+    float to = top;
+    for (int o = rows; o < 32; o *= 2) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+    rescale(to);
     if (nan) total = NAN;
     for (int o = rows; o < 32; o *= 2) {
         total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -1140,7 +1332,9 @@ int launch(const Params& prm, cudaStream_t stream) {
     const cudaError_t e = launch_kernel(chunk_kernel<G>, prm.p.grid, kThreads, kSmem, stream, prm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)prm.p.grid, 2 * kRows / 32);
+    // 32 rows a block, of the most that a pair may have
+    const int64_t rows = prm.p.seq_lens ? G : std::min<int64_t>(2 * kRows, (int64_t)prm.p.total_tokens * G);
+    cfg.gridDim = dim3((unsigned)prm.p.grid, (unsigned)((rows + 31) / 32));
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
