@@ -67,6 +67,8 @@ extern "C" {
                                      between pkv_plan and the launch; extra tasks were dropped), or a task or
                                      row range in the workspace did not belong to the plan (it was skipped) */
 
+#define PKV_STATUS_NO_PAGES 0x10u /* pkv_tables_grow: a row got nothing, as the pages of the stack or the slots ran out */
+
 #define PKV_MAX_BATCH 4096
 #define PKV_MAX_ROWS_IN_DECODE 256 /* largest B for which the decode kernel can derive the workqueue itself */
 
@@ -534,6 +536,83 @@ int pkv_chunk_workspace_bytes(int32_t num_sms, size_t* bytes);
 int pkv_chunk_attention(const pkv_problem* problem, const pkv_prompt* prompt, const void* q, const void* k_pool,
                         const void* v_pool, const int32_t* cu_seqlens, const int32_t* start, const int32_t* block_table,
                         float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out, void* stream);
+
+/*
+ * The tables of a step from its rows' lengths: row b (b < problem->batch) holds seq_lens[b] tokens and gets new_tokens[b]
+ * more (both int32 [B]; 0 allowed). Pages come from a stack: free_pages [num_pages] int32, of which the first *free_count are
+ * free, taken from the top (index *free_count - 1) down, row by row and within a row by position. Written:
+ *   block_table     the entries of new pages (behind those that the row's tokens have already), in place
+ *   cu_seqlens      [B + 1] packed rows of each row's new tokens, as pkv_prompt_append and pkv_chunk_attention take them
+ *   start           [B] the lengths before, as they take them
+ *   slots           [capacity] int64: page * page_size + slot of each packed new token
+ *   positions       [capacity] int32: its position in its row
+ *   seq_lens_out    [B] the lengths afterwards (may be seq_lens)
+ *   free_count_out  [1] the stack's height afterwards (may be free_count)
+ * cu_seqlens, start, slots and positions may be NULL; entries of slots and positions behind the last new token keep their
+ * values. Apart from the two pairs named, no output may be an input or another output (the same address is refused).
+ * A row with a negative length or number, or that would outgrow its block table, raises PKV_STATUS_BAD_LEN and gets nothing (as
+ * if its new_tokens were 0). Rows are served in order: one whose new tokens, with those of the rows before it, exceed capacity
+ * (with slots or positions), or that needs pages which, with those that the rows before it need, exceed *free_count, raises
+ * PKV_STATUS_NO_PAGES and gets nothing. ws: PKV_PROMPT_WS_BYTES, zeroed once. 0 <= capacity < 2^31. Of problem, the heads do
+ * not matter beyond pkv_check_problem.
+ */
+int pkv_tables_grow(const pkv_problem* problem, const int32_t* new_tokens, const int32_t* seq_lens, int32_t* block_table,
+                    const int32_t* free_pages, const int32_t* free_count, int32_t* cu_seqlens, int32_t* start,
+                    int64_t* slots, int32_t* positions, int64_t capacity, int32_t* seq_lens_out, int32_t* free_count_out,
+                    int32_t num_sms, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The pages of rows that end, back on the stack: for each row b with released[b] != 0 (int32 [B]), in order, the pages of its
+ * seq_lens[b] tokens go to free_pages[*free_count ...] by position, and its length becomes 0. Rows that share pages must not
+ * be released with this call (a page goes on the stack once for each). A released row with a length outside its table raises
+ * PKV_STATUS_BAD_LEN and keeps it; a stack that would outgrow num_pages raises PKV_STATUS_BAD_LEN, and nothing is released.
+ * seq_lens_out and free_count_out may be seq_lens and free_count; nothing else may be the same memory. The block table
+ * keeps its entries. ws: PKV_PROMPT_WS_BYTES, zeroed once.
+ */
+int pkv_tables_release(const pkv_problem* problem, const int32_t* released, const int32_t* seq_lens,
+                       const int32_t* block_table, int32_t* free_pages, const int32_t* free_count, int32_t* seq_lens_out,
+                       int32_t* free_count_out, int32_t num_sms, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Bounds of pages: bounds [num_pages][Hkv][2][d] fp16, 16-byte aligned, gets for every page that the new tokens (cu_seqlens,
+ * start, as for pkv_prompt_append, which wrote them) lie in the least and the greatest K of the row's tokens in that page,
+ * dim by dim, earlier tokens of the page included; a NaN among them is both. Other pages keep theirs. problem and prompt as
+ * for pkv_prompt_append (k_stride and v_stride do not matter). Rows and pages that are not in order are skipped with the same
+ * status bits. ws: PKV_PROMPT_WS_BYTES. bounds must not overlap the pool (the same address is refused).
+ */
+int pkv_page_bounds(const pkv_problem* problem, const pkv_prompt* prompt, const int32_t* cu_seqlens, const int32_t* start,
+                    const void* k_pool, const int32_t* block_table, void* bounds, int32_t num_sms, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* Bytes of the workspace of pkv_select_pages and pkv_sparse_decode_step for a problem, on a GPU of num_sms SMs. Host only. */
+int pkv_sparse_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size_t* bytes);
+
+/*
+ * The pages that a decode step attends to: for row b and KV head h, of the P pages of the row's seq_lens[b] tokens the last one
+ * and the select - 1 others of the greatest score (all of them where P <= select), in ascending order, to
+ * pages [B][Hkv][select] int32 (logical pages of the row; -1 behind them). The score of a page is the greatest, over the G
+ * query heads of h (q [B][Hq][d] fp16), of sum_d max(q_d lo_d, q_d hi_d) with the page's bounds (pkv_page_bounds): an upper
+ * bound of q.k over its tokens. Scores are compared as sums of exact products in 64 bits; equal ones go to the lowest
+ * page, and a score whose bounds or whose queries (of any of the G heads) are not all finite counts as +inf. select >= 1.
+ * A length that is negative or exceeds the table raises PKV_STATUS_BAD_LEN (no pages); a block-table entry outside the pool
+ * raises PKV_STATUS_BAD_PAGE and counts as bounds of 0 (entries of rows with P <= select are not looked at). ws:
+ * pkv_sparse_workspace_bytes.
+ */
+int pkv_select_pages(const pkv_problem* problem, const void* q, const void* bounds, const int32_t* block_table,
+                     const int32_t* seq_lens_dev, int32_t select, int32_t num_sms, void* ws, size_t ws_bytes, int32_t* pages,
+                     void* stream);
+
+/*
+ * One decode step over selected pages: as pkv_decode_step, where row b's query heads of KV head h attend to the tokens of the
+ * first min(select, P) pages of pages[b][h] alone, of which the last entry is the row's last page (pages as pkv_select_pages
+ * leaves them; others of the same form will do). 0 <= scale <= 1e12; ws: pkv_sparse_workspace_bytes. A row of length 0 gets 0.
+ * out must not overlap q or the pools (the same address is refused). Infinities and NaN of K and V as for
+ * pkv_chunk_attention. A bad length raises PKV_STATUS_BAD_LEN (the row counts as empty); a page outside the row's table or
+ * the pool raises PKV_STATUS_BAD_PAGE and counts as one whose K and V are 0.
+ */
+int pkv_sparse_decode_step(const pkv_problem* problem, const void* q, const void* k_pool, const void* v_pool,
+                           const int32_t* block_table, const int32_t* seq_lens_dev, const int32_t* pages, int32_t select,
+                           float scale, int32_t num_sms, void* ws, size_t ws_bytes, void* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,7 @@ from ._lib import (EXPORTS, LIB_PATH, PKV_MAX_BATCH, PKV_MAX_ROWS_IN_DECODE, PKV
                    PKV_PLAN_INPUTS_AFTER_PREV,
                    PKV_PLAN_OVERLAP_PREV, PKV_PROMPT_WS_BYTES, PKV_Q4_BLOCK_BYTES, Prompt,
                    PKV_SESSION_GRAPHS, PKV_STATIC_SCRATCH_BYTES,
-                   PKV_STATUS_BAD_LEN, PKV_STATUS_BAD_PAGE, PKV_STATUS_TASKS, PKV_STATUS_TIMEOUT, PKV_VARIANT_SINGLE,
+                   PKV_STATUS_BAD_LEN, PKV_STATUS_BAD_PAGE, PKV_STATUS_NO_PAGES, PKV_STATUS_TASKS, PKV_STATUS_TIMEOUT, PKV_VARIANT_SINGLE,
                    PKV_VARIANT_SPLIT, PKV_VARIANT_WORKQUEUE, VARIANT_NAMES, PkvError, load)
 from .binding import (Plan, Policy, Problem, alloc_workspace, decode, make_problem, pkv_build_worklist,  # noqa: F401
                       pkv_check_problem, pkv_decode, pkv_decode_step, pkv_decode_step_append, pkv_decode_step_static,
@@ -22,4 +22,6 @@ from .prompts import (make_prompt, pkv_check_prompt, pkv_prompt_append, pkv_prom
                       pkv_q4_decode_step, pkv_q4_decode_step_append, pkv_q4_pool_bytes, pkv_q4_prompt_append, pkv_q4_read,
                       pkv_q4_workspace_bytes, prompt_append, prompt_attention, q4_decode, q4_problem, q4_prompt_append,
                       q4_read)
-from .paged import chunk_attention, pkv_chunk_attention, pkv_chunk_workspace_bytes  # noqa: F401
+from .paged import (chunk_attention, page_bounds, pkv_chunk_attention, pkv_chunk_workspace_bytes,  # noqa: F401
+                    pkv_page_bounds, pkv_select_pages, pkv_sparse_decode_step, pkv_sparse_workspace_bytes, pkv_tables_grow,
+                    pkv_tables_release, select_pages, sparse_decode, sparse_problem, tables_grow, tables_release)

@@ -24,6 +24,7 @@ PKV_STATUS_BAD_PAGE = 0x1
 PKV_STATUS_BAD_LEN = 0x2
 PKV_STATUS_TIMEOUT = 0x4
 PKV_STATUS_TASKS = 0x8
+PKV_STATUS_NO_PAGES = 0x10
 
 PKV_MAX_BATCH = 4096
 PKV_MAX_ROWS_IN_DECODE = 256
@@ -44,7 +45,8 @@ EXPORTS = (
     "pkv_serve_step", "pkv_session_create", "pkv_session_step", "pkv_session_stats", "pkv_session_destroy",
     "pkv_check_prompt", "pkv_prompt_attention", "pkv_prompt_append", "pkv_q4_prompt_append", "pkv_q4_read",
     "pkv_q4_pool_bytes", "pkv_q4_workspace_bytes", "pkv_q4_decode_step", "pkv_q4_decode_step_append",
-    "pkv_chunk_workspace_bytes", "pkv_chunk_attention",
+    "pkv_chunk_workspace_bytes", "pkv_chunk_attention", "pkv_tables_grow", "pkv_tables_release", "pkv_page_bounds",
+    "pkv_sparse_workspace_bytes", "pkv_select_pages", "pkv_sparse_decode_step",
 )
 
 PKV_SESSION_GRAPHS = 16
@@ -175,7 +177,13 @@ def load(path: str | None = None):
                 ("pkv_q4_decode_step", [_P(Problem), _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
                 ("pkv_q4_decode_step_append", [_P(Problem), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
                 ("pkv_chunk_workspace_bytes", [i32, _P(size)]),
-                ("pkv_chunk_attention", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp])):
+                ("pkv_chunk_attention", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, _vp, f32, i32, _vp, size, _vp, _vp]),
+                ("pkv_tables_grow", [_P(Problem)] + [_vp] * 9 + [ctypes.c_int64, _vp, _vp, i32, _vp, size, _vp]),
+                ("pkv_tables_release", [_P(Problem)] + [_vp] * 7 + [i32, _vp, size, _vp]),
+                ("pkv_page_bounds", [_P(Problem), _P(Prompt), _vp, _vp, _vp, _vp, _vp, i32, _vp, size, _vp]),
+                ("pkv_sparse_workspace_bytes", [_P(Problem), i32, _P(size)]),
+                ("pkv_select_pages", [_P(Problem), _vp, _vp, _vp, _vp, i32, i32, _vp, size, _vp, _vp]),
+                ("pkv_sparse_decode_step", [_P(Problem), _vp, _vp, _vp, _vp, _vp, _vp, i32, f32, i32, _vp, size, _vp, _vp])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = args
         _lib = lib

@@ -17,7 +17,8 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpkv.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "build_worklist.cu", "decode.cu", "merge.cu", "static_scratch.cu", "stage.cu",
-           "prompt.cpp", "prompt_attention.cu", "prompt_pages.cu", "q4_decode.cu", "paged.cpp", "chunk_attention.cu"]
+           "prompt.cpp", "prompt_attention.cu", "prompt_pages.cu", "q4_decode.cu", "paged.cpp", "chunk_attention.cu",
+           "tables.cu", "page_select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -139,6 +139,40 @@ struct ChunkParams {
 };
 constexpr int kChunkMergeBytes = 32;
 
+// Arguments of the table calls (tables.cu).
+struct TablesParams {
+    const int32_t* new_tokens;  // grow
+    const int32_t* released;    // release
+    const int32_t* seq_lens;
+    int32_t* block_table;
+    const int32_t* free_pages;  // grow: the stack
+    int32_t* free_out;          // release: the same
+    const int32_t* free_count;
+    int32_t* cu_seqlens;        // the next four may be NULL
+    int32_t* start;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* seq_lens_out;      // may be seq_lens
+    int32_t* free_count_out;    // may be free_count
+    pkv_ws_header* hdr;
+    int64_t capacity;           // entries of slots and positions
+    int32_t B, num_pages, max_pages;
+};
+
+// Arguments of the page selection (page_select.cu).
+struct SelectParams {
+    const void* q;
+    const void* bounds;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    int32_t* pages;
+    pkv_ws_header* hdr;
+    float* scores;   // [B][Hkv][max_pages]; turned into keys where they are near the border
+    double* exact;   // the same, of pages near the border
+    float* tops;     // [B][Hkv][ceil(max_pages / 16)]: largest magnitude of 16 pages' finite bounds
+    int32_t B, Hq, Hkv, num_pages, max_pages, select;
+};
+
 // Kernel launchers (defined in the .cu files). They return the CUDA error of the launch.
 int launch_decode(const DecodeParams& p, int group, int grid, bool pdl, void* stream);
 int launch_build(const BuildParams& p, int grid, void* stream);
@@ -152,12 +186,22 @@ int launch_q4_append(const PagesParams& p, int num_sms, void* stream);
 int launch_q4_read(const PagesParams& p, int num_sms, void* stream);
 int launch_q4_decode(const Q4Params& p, int num_sms, void* stream);
 int launch_chunk_attention(const ChunkParams& p, int num_sms, void* stream);
+int launch_tables_grow(const TablesParams& p, int num_sms, void* stream);
+int launch_tables_release(const TablesParams& p, int num_sms, void* stream);
+int launch_page_bounds(const PagesParams& p, int num_sms, void* stream);
+int launch_select_pages(const SelectParams& p, int num_sms, void* stream);
 
 // Workspace of a 4-bit decode step on a GPU of num_sms SMs.
 size_t q4_workspace_bytes(const pkv_problem& pr, int num_sms);
 
 // Workspace of the chunk attention on a GPU of num_sms SMs.
 size_t chunk_workspace_bytes(int num_sms);
+
+// Offsets of the page selection's scores, exact scores and magnitudes in its workspace, and its size.
+struct SelectLayout {
+    size_t scores, exact, tops, bytes;
+};
+SelectLayout select_layout(const pkv_problem& pr);
 
 // Validation shared by pkv_decode and the step entry points (PKV_OK or a PKV_E_* code; enqueues nothing).
 int check_decode_args(const pkv_plan_t* plan, const pkv_problem* pr, const void* q, const void* k_pool,

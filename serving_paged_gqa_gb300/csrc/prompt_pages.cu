@@ -117,6 +117,40 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const PagesParams p) {
         });
 }
 
+// Bounds of pages: a warp per (page, 32 pieces of 16 bytes of a token's K), a lane per piece, all 16 tokens in flight. Bound:
+// HBM (the pages' K is read once, 512 bytes a (page, KV head) written).
+__global__ void __launch_bounds__(kThreads) bounds_kernel(const PagesParams p) {
+    const int lane = threadIdx.x & 31;
+    const int per = p.Hkv * 16, parts = (per + 31) / 32;
+    for_items(
+        p, [&](const Seq& q) { return (int64_t)page_count(q) * parts; },
+        [&](const Seq& q, uint32_t i) {
+            const int lp = first_page(q) + (int)(i / (uint32_t)parts), c = (int)(i % (uint32_t)parts) * 32 + lane;
+            const int64_t page = page_of(p, q.s, lp);
+            if (page < 0 || c >= per) return;
+            const int n = min(kPageSize, q.start + q.n - lp * kPageSize);
+            const uint4* k = static_cast<const uint4*>(p.k_pool) + page * kPageSize * per + c;
+            uint4 x[kPageSize];
+#pragma unroll
+            for (int t = 0; t < kPageSize; ++t) x[t] = __ldcs(k + min(t, n - 1) * per);
+            __half2 lo[4], hi[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lo[j] = hi[j] = reinterpret_cast<const __half2*>(&x[0])[j];
+#pragma unroll
+            for (int t = 1; t < kPageSize; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 y = reinterpret_cast<const __half2*>(&x[t])[j];
+                    lo[j] = __hmin2_nan(lo[j], y);
+                    hi[j] = __hmax2_nan(hi[j], y);
+                }
+            // [page][head][least, greatest][16 pieces]
+            uint4* out = static_cast<uint4*>(p.pool) + (page * p.Hkv + c / 16) * 32 + c % 16;
+            out[0] = *reinterpret_cast<const uint4*>(lo);
+            out[16] = *reinterpret_cast<const uint4*>(hi);
+        });
+}
+
 // ---- quantising a whole (page, KV head) ----------------------------------------------------------------------------
 // Lane l holds dims 8 c .. 8 c + 7 (c = l % 16) of tokens 2 i + l / 16, i < 8: coalesced rows. A group is 8 lanes.
 
@@ -404,6 +438,13 @@ int64_t page_items(const PagesParams& p) { return ((int64_t)p.total_tokens / kPa
 
 int launch_prompt_append(const PagesParams& p, int num_sms, void* stream) {
     return launch_kernel(append_kernel, grid_for(num_sms, p.total_tokens), kThreads, 0, static_cast<cudaStream_t>(stream), p);
+}
+
+int launch_page_bounds(const PagesParams& p, int num_sms, void* stream) {
+    // (the number of new tokens is not known here, so more CTAs than are resident would start to find nothing)
+    const int64_t items = page_items(p) / p.Hkv * ((p.Hkv + 1) / 2);
+    return launch_kernel(bounds_kernel, std::min(grid_for(num_sms, items), 2 * num_sms), kThreads, 0,
+                         static_cast<cudaStream_t>(stream), p);
 }
 
 int launch_q4_append(const PagesParams& p, int num_sms, void* stream) {

@@ -12,10 +12,14 @@ import math
 
 import torch
 
-from ._lib import Problem, Prompt, check, load
+from ._lib import PKV_PROMPT_WS_BYTES, Problem, Prompt, check, load
 from .prompts import _addr, _byref, _call, _device, _fits, _handle, _new, _num_sms, _pool, _rows, _scratch, _seqs, _start, _table
 
-__all__ = ["pkv_chunk_workspace_bytes", "pkv_chunk_attention", "chunk_attention"]
+__all__ = [
+    "pkv_chunk_workspace_bytes", "pkv_chunk_attention", "pkv_tables_grow", "pkv_tables_release", "pkv_page_bounds",
+    "pkv_sparse_workspace_bytes", "pkv_select_pages", "pkv_sparse_decode_step",
+    "chunk_attention", "tables_grow", "tables_release", "page_bounds", "sparse_problem", "select_pages", "sparse_decode",
+]
 
 
 def pkv_chunk_workspace_bytes(num_sms: int | None = None) -> int:
@@ -42,6 +46,94 @@ def pkv_chunk_attention(problem: Problem, prompt: Prompt, q, k_pool, v_pool, cu_
     _pool(k_pool, "k_pool", problem, prompt)
     _pool(v_pool, "v_pool", problem, prompt)
     _chunk(dev, problem, prompt, q, k_pool, v_pool, cu_seqlens, start, block_table, scale, ws, out, stream)
+
+
+def _ints(t, name: str, n: int, dtype=torch.int32) -> int | None:
+    """The address of a tensor of n integers (None: not given)."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return _addr(t, dtype, name)
+
+
+def pkv_tables_grow(problem: Problem, new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots,
+                    positions, seq_lens_out, free_count_out, ws, stream=None) -> None:
+    dev = _device(new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots, positions, seq_lens_out,
+                  free_count_out, ws)
+    b = problem.batch
+    cap = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
+    _call(dev, "pkv_tables_grow", _byref(problem), _ints(new_tokens, "new_tokens", b), _ints(seq_lens, "seq_lens", b),
+          _table(block_table, problem), _ints(free_pages, "free_pages", problem.num_pages), _ints(free_count, "free_count", 1),
+          _ints(cu_seqlens, "cu_seqlens", b + 1), _ints(start, "start", b), _ints(slots, "slots", cap, torch.int64),
+          _ints(positions, "positions", cap), cap, _ints(seq_lens_out, "seq_lens_out", b),
+          _ints(free_count_out, "free_count_out", 1), _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
+def pkv_tables_release(problem: Problem, released, seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out,
+                       ws, stream=None) -> None:
+    dev = _device(released, seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out, ws)
+    b = problem.batch
+    _call(dev, "pkv_tables_release", _byref(problem), _ints(released, "released", b), _ints(seq_lens, "seq_lens", b),
+          _table(block_table, problem), _ints(free_pages, "free_pages", problem.num_pages), _ints(free_count, "free_count", 1),
+          _ints(seq_lens_out, "seq_lens_out", b), _ints(free_count_out, "free_count_out", 1), _num_sms(dev),
+          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
+def _bounds(t: torch.Tensor, problem: Problem) -> int:
+    want = (problem.num_pages, problem.num_kv_heads, 2, problem.head_dim)
+    if t.shape != want:
+        raise ValueError(f"bounds must have shape {want}, got {tuple(t.shape)}")
+    return _addr(t, torch.float16, "bounds")
+
+
+def pkv_page_bounds(problem: Problem, prompt: Prompt, cu_seqlens, start, k_pool, block_table, bounds, ws, stream=None) -> None:
+    dev = _device(k_pool, cu_seqlens, start, block_table, bounds, ws)
+    n = prompt.num_seqs
+    _pool(k_pool, "k_pool", problem, prompt)
+    _call(dev, "pkv_page_bounds", _byref(problem), _byref(prompt), _seqs(cu_seqlens, n), _start(start, n),
+          _addr(k_pool, torch.float16, "k_pool"), _table(block_table, problem), _bounds(bounds, problem), _num_sms(dev),
+          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+
+
+def pkv_sparse_workspace_bytes(problem: Problem, num_sms: int | None = None) -> int:
+    """Bytes of the workspace of a page selection and the step over its pages (num_sms None: that of the current device)."""
+    if num_sms is None:
+        num_sms = _num_sms(torch.cuda.current_device())
+    n = ctypes.c_size_t(0)
+    check(load().pkv_sparse_workspace_bytes(_byref(problem), int(num_sms), _byref(n)), "pkv_sparse_workspace_bytes")
+    return int(n.value)
+
+
+def _queries(t: torch.Tensor, name: str, problem: Problem) -> int:
+    want = (problem.batch, problem.num_q_heads, problem.head_dim)
+    if t.shape != want:
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    return _addr(t, torch.float16, name)
+
+
+def _selected(pages: torch.Tensor, problem: Problem) -> int:
+    if pages.dim() != 3 or pages.shape[:2] != (problem.batch, problem.num_kv_heads):
+        raise ValueError(f"pages must be [{problem.batch}, {problem.num_kv_heads}, select]")
+    return _addr(pages, torch.int32, "pages")
+
+
+def pkv_select_pages(problem: Problem, q, bounds, block_table, seq_lens, pages, ws, stream=None) -> None:
+    dev = _device(q, bounds, block_table, seq_lens, pages, ws)
+    _call(dev, "pkv_select_pages", _byref(problem), _queries(q, "q", problem), _bounds(bounds, problem),
+          _table(block_table, problem), _ints(seq_lens, "seq_lens", problem.batch), pages.shape[-1], _num_sms(dev),
+          _addr(ws, torch.uint8, "ws"), ws.numel(), _selected(pages, problem), _handle(stream, dev))
+
+
+def pkv_sparse_decode_step(problem: Problem, q, k_pool, v_pool, block_table, seq_lens, pages, scale, ws, out,
+                           stream=None) -> None:
+    dev = _device(q, k_pool, v_pool, block_table, seq_lens, pages, ws, out)
+    want = (problem.num_pages, problem.page_size, problem.num_kv_heads, problem.head_dim)
+    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t.shape != want:
+            raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    _call(dev, "pkv_sparse_decode_step", _byref(problem), _queries(q, "q", problem), _addr(k_pool, torch.float16, "k_pool"),
+          _addr(v_pool, torch.float16, "v_pool"), _table(block_table, problem), _ints(seq_lens, "seq_lens", problem.batch),
+          _selected(pages, problem), pages.shape[-1], scale, _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(),
+          _queries(out, "out", problem), _handle(stream, dev))
 
 
 # ------------------------------------------------------------------------------- the same, described by the tensors
@@ -79,4 +171,113 @@ def chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
         ws = _scratch(pkv_chunk_workspace_bytes(_num_sms(dev)), None, dev, stream)
     _chunk(dev, problem, prompt, q, k_pool, v_pool, cu_seqlens, start, block_table,
            1.0 / math.sqrt(d) if scale is None else scale, ws, out, stream)
+    return out
+
+
+def tables_grow(new_tokens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                free_count: torch.Tensor, cu_seqlens: torch.Tensor | None = None, start: torch.Tensor | None = None,
+                slots: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                seq_lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None, stream=None):
+    """Pages and packed rows for the rows' new tokens (include/pkv.h, pkv_tables_grow). Returns cu_seqlens, start.
+
+    new_tokens, seq_lens [B], block_table [B, max_pages], free_pages [num_pages], free_count [1] int32 on the device: row b
+    holds seq_lens[b] tokens and gets new_tokens[b] more; the first free_count entries of free_pages are the stack of free
+    pages. block_table gets the new pages' entries; seq_lens_out and free_count_out (None: seq_lens and free_count themselves)
+    the lengths and the stack's height afterwards; cu_seqlens [B + 1] and start [B] (made here where they are not given) what
+    prompt_append and chunk_attention take; slots (int64) and positions (int32), one entry for each packed new token, where
+    they are given, the token's page * 16 + slot and its position.
+    """
+    b = new_tokens.numel()
+    dev = _device(new_tokens)
+    if cu_seqlens is None:
+        cu_seqlens = _new((b + 1,), dev, stream, torch.int32)
+    if start is None:
+        start = _new((b,), dev, stream, torch.int32)
+    problem = Problem(b, 1, 1, 128, 16, free_pages.numel(), block_table.shape[1])
+    pkv_tables_grow(problem, new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots, positions,
+                    seq_lens if seq_lens_out is None else seq_lens_out, free_count if free_count_out is None else free_count_out,
+                    _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    return cu_seqlens, start
+
+
+def tables_release(released: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                   free_count: torch.Tensor, seq_lens_out: torch.Tensor | None = None,
+                   free_count_out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> None:
+    """The pages of the rows with released != 0 back on the stack (include/pkv.h, pkv_tables_release); released [B] int32, the
+    others as for tables_grow."""
+    b = released.numel()
+    dev = _device(released)
+    problem = Problem(b, 1, 1, 128, 16, free_pages.numel(), block_table.shape[1])
+    pkv_tables_release(problem, released, seq_lens, block_table, free_pages, free_count,
+                       seq_lens if seq_lens_out is None else seq_lens_out,
+                       free_count if free_count_out is None else free_count_out,
+                       _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+
+
+def page_bounds(k_pool: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor, bounds: torch.Tensor,
+                start: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Bounds of the pages that packed new tokens went to (include/pkv.h, pkv_page_bounds). Returns bounds.
+
+    k_pool [num_pages, 16, Hkv, d]; bounds [num_pages, Hkv, 2, d] fp16, the least and the greatest key of each page; cu_seqlens,
+    start and block_table as for the prompt_append that wrote the tokens. (Nothing here knows how many new tokens there are but
+    the device: the work is bounded by the pages of the table.)
+    """
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_pages, page_size, Hkv, d]")
+    pages, ps, hkv, d = k_pool.shape
+    b, width = block_table.shape
+    dev = _device(k_pool, cu_seqlens, start, block_table, bounds, ws)
+    problem = Problem(b, hkv, hkv, d, ps, pages, width)
+    prompt = Prompt(cu_seqlens.numel() - 1, min(b * width * ps, 0x7fffffff), hkv, hkv, d, 0, hkv * d, hkv * d, hkv * d, hkv * d)
+    pkv_page_bounds(problem, prompt, cu_seqlens, start, k_pool, block_table, bounds,
+                    _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    return bounds
+
+
+def sparse_problem(q: torch.Tensor, k_pool: torch.Tensor, block_table: torch.Tensor) -> Problem:
+    """The problem of a step over selected pages: q [B, Hq, d], k_pool [num_pages, 16, Hkv, d], block_table [B, max_pages]."""
+    b, hq, d = q.shape
+    return Problem(b, hq, k_pool.shape[2], d, k_pool.shape[1], k_pool.shape[0], block_table.shape[1])
+
+
+def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, select: int,
+                 pages: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The pages that a decode step attends to (include/pkv.h, pkv_select_pages). Returns pages [B, Hkv, select] int32.
+
+    q [B, Hq, d] fp16; bounds [num_pages, Hkv, 2, d] (page_bounds); block_table [B, max_pages], seq_lens [B] int32. Keep ws
+    (pkv_sparse_workspace_bytes, alloc_workspace) over the steps of a loop; sparse_decode takes the same.
+    """
+    if bounds.dim() != 4:
+        raise ValueError("bounds must be [num_pages, Hkv, 2, d]")
+    b, hq, d = q.shape
+    problem = Problem(b, hq, bounds.shape[1], d, 16, bounds.shape[0], block_table.shape[1])
+    dev = _device(q)
+    if pages is None:
+        pages = _new((b, bounds.shape[1], int(select)), dev, stream, torch.int32)
+    elif pages.shape[-1] != select:
+        raise ValueError(f"pages has room for {pages.shape[-1]} pages, select is {select}")
+    if ws is None:
+        ws = _scratch(pkv_sparse_workspace_bytes(problem, _num_sms(dev)), None, dev, stream)
+    pkv_select_pages(problem, q, bounds, block_table, seq_lens, pages, ws, stream)
+    return pages
+
+
+def sparse_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                  seq_lens: torch.Tensor, pages: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One decode step over the pages that select_pages chose (include/pkv.h, pkv_sparse_decode_step). Returns out [B, Hq, d].
+
+    q [B, Hq, d] fp16; k_pool, v_pool [num_pages, 16, Hkv, d]; block_table [B, max_pages], seq_lens [B], pages [B, Hkv,
+    select] int32 on the device.
+    """
+    _pools(k_pool, v_pool, q.shape[-1])
+    problem = sparse_problem(q, k_pool, block_table)
+    dev = _device(q)
+    if out is None:
+        out = _new(tuple(q.shape), dev, stream)
+    if ws is None:
+        ws = _scratch(pkv_sparse_workspace_bytes(problem, _num_sms(dev)), None, dev, stream)
+    pkv_sparse_decode_step(problem, q, k_pool, v_pool, block_table, seq_lens, pages,
+                           1.0 / math.sqrt(q.shape[2]) if scale is None else scale, ws, out, stream)
     return out

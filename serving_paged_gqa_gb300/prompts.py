@@ -278,8 +278,8 @@ def _scratch(nbytes: int, ws, device: int, stream):
             return alloc_workspace(nbytes, device)
 
 
-def _new(shape, device: int, stream) -> torch.Tensor:
-    out = torch.empty(shape, dtype=torch.float16, device=device)
+def _new(shape, device: int, stream, dtype=torch.float16) -> torch.Tensor:
+    out = torch.empty(shape, dtype=dtype, device=device)
     other = _other(stream, device)
     if other is not None:
         other.wait_stream(torch.cuda.current_stream(device))  # the memory may still be read on the current stream
