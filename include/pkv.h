@@ -592,8 +592,8 @@ int pkv_sparse_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size
  * and the select - 1 others of the greatest score (all of them where P <= select), in ascending order, to
  * pages [B][Hkv][select] int32 (logical pages of the row; -1 behind them). The score of a page is the greatest, over the G
  * query heads of h (q [B][Hq][d] fp16), of sum_d max(q_d lo_d, q_d hi_d) with the page's bounds (pkv_page_bounds): an upper
- * bound of q.k over its tokens. Scores are compared as sums of exact products in 64 bits; equal ones go to the lowest
- * page, and a score whose bounds or whose queries (of any of the G heads) are not all finite counts as +inf. select >= 1.
+ * bound of q.k over its tokens. Scores are compared as exact sums (rounded to 64 bits where more than 256 pages are within
+ * fp32's error of the last selected one); equal ones go to the lowest page, and a score whose bounds or whose queries (of any of the G heads) are not all finite counts as +inf. select >= 1.
  * A length that is negative or exceeds the table raises PKV_STATUS_BAD_LEN (no pages); a block-table entry outside the pool
  * raises PKV_STATUS_BAD_PAGE and counts as bounds of 0 (entries of rows with P <= select are not looked at). ws:
  * pkv_sparse_workspace_bytes.

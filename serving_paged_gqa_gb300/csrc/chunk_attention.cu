@@ -40,7 +40,7 @@ constexpr int kStepPages = kRows / kPageSize;
 constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two halves of 64 dims
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kPageBox = kPageSize * 128;    // one page's part of a half
-constexpr int kStages = 4;
+constexpr int kMostStages = 5;
 constexpr int kSoftmax = 512;                // threads of the softmax
 constexpr int kThreads = kSoftmax + 128;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96, what the launch has
@@ -49,7 +49,7 @@ constexpr float kLift = 5.f;                 // the largest weight where the ref
 // What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps.
 constexpr int kPairCost = 2;
 constexpr int kMinCost = 2;                  // of a piece, at least
-constexpr int kWhole = 10;                   // cost of a pair that is not cut where a piece has no more
+constexpr int kWhole = 5;                    // cost of a pair that is not cut where a piece has no more
 
 // One sequence: its first packed row, its new tokens, and how many it holds before them.
 struct Seq {
@@ -71,23 +71,44 @@ struct Merge {
 };
 static_assert(sizeof(Merge) == kChunkMergeBytes, "workspace layout");
 
-constexpr int off_q = 0;
-constexpr int off_ring = 2 * kTileBytes;
-constexpr int off_work = off_ring + kStages * kTileBytes;
-constexpr int off_bars = off_work + 2 * (int)sizeof(Work);
-constexpr int kBars = 2 * kStages + 38;
-constexpr int off_ref = off_bars + kBars * 8;            // float [tile][row]: ref
-constexpr int off_parts = off_ref + 2 * kRows * 4;       // float2 (ref, l) [work & 1][tile][half][row]
-constexpr int off_late = off_parts + 2 * 2 * 2 * kRows * 8;  // int [tile][warp of the half]: the second half raises
-constexpr int off_scan = off_late + 8 * 4;               // int64 [warp]: steps of the sequences of a warp's threads
-constexpr int off_begin = off_scan + kThreads / 32 * 8;  // int64, int32: where the piece begins
-constexpr int off_misc = off_begin + 16;                 // abort flag, TMEM address
-constexpr int kSmem = off_misc + 16 + 1024;              // slack to align the base to 1024 bytes
-static_assert(sizeof(Work) % 4 == 0 && off_bars % 8 == 0 && off_parts % 8 == 0 && off_scan % 8 == 0, "alignment");
-static_assert(kSmem <= 227 * 1024, "shared memory");
+// Barriers of the CTA, in shared memory.
+struct Bars {
+    uint64_t kv_full[kMostStages], kv_empty[kMostStages];
+    uint64_t w_full[2], w_empty[2];  // a work has been published; every warp is done with what it needs of it
+    uint64_t q_full[2], q_empty[2];  // like those below: tile A, tile B
+    uint64_t s_full[2];              // the tile's scores are in TMEM
+    uint64_t p_full[2][2];           // its weights of the step's first, second 64 keys are
+    uint64_t o_full[2];              // its accumulator is complete
+    uint64_t lo_done[2];             // the products of a step's first 64 keys are in the accumulator
+    uint64_t o_free[2];              // the accumulator has been read
+    uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
+    uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
+    uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
+    uint64_t drain;
+};
+
+// Shared memory. Few: the kernel of sequences whose new tokens are one tile.
+template <bool kFew>
+struct Layout {
+    static constexpr int kStages = kFew ? 5 : 4;  // K and V tiles in flight
+    static constexpr int q = 0;
+    static constexpr int ring = (kFew ? 1 : 2) * kTileBytes;
+    static constexpr int work = ring + kStages * kTileBytes;
+    static constexpr int bars = work + 2 * (int)sizeof(Work);
+    static constexpr int ref = bars + (int)sizeof(Bars);         // float [tile][row]: ref
+    static constexpr int parts = ref + 2 * kRows * 4;            // float2 (ref, l) [work & 1][tile][half][row]
+    static constexpr int late = parts + 2 * 2 * 2 * kRows * 8;   // int [tile][warp of the half]: the second half raises
+    static constexpr int scan = late + 8 * 4;                    // int64 [warp]: cost of the sequences of a warp's threads
+    static constexpr int begin = scan + kThreads / 32 * 8;       // int64, int32: where the piece begins
+    static constexpr int low = begin + 16;                       // few: float [half][64][33]: second parts' accumulators
+    static constexpr int misc = low + (kFew ? 2 * 64 * 33 * 4 : 0);  // abort flag, TMEM address
+    static constexpr int bytes = misc + 16 + 1024;               // slack to align the base to 1024 bytes
+    static_assert(sizeof(Work) % 4 == 0 && bars % 8 == 0 && parts % 8 == 0 && scan % 8 == 0, "alignment");
+    static_assert(kStages <= kMostStages && bytes <= 227 * 1024, "shared memory");
+};
 
 struct Params {
-    CUtensorMap q, k, v;
+    CUtensorMap q, q64, k, v;  // q: 128 rows a box; q64: 64
     ChunkParams p;
 };
 
@@ -110,6 +131,14 @@ __device__ __forceinline__ Seq load_seq(const ChunkParams& p, int s, bool& bad) 
         q.n = bad ? 0 : last - q.first;
     }
     if (q.n == 0) q.start = 0;
+    return q;
+}
+
+// The same for a kernel: nothing where the sequence is the other one's.
+template <int G, bool kFew>
+__device__ __forceinline__ Seq own_seq(const ChunkParams& p, int s, bool& bad) {
+    Seq q = load_seq(p, s, bad);
+    if (p.split && (q.n <= kRows / G) != kFew) q = Seq{0, 0, 0};
     return q;
 }
 
@@ -155,12 +184,6 @@ template <typename W>
 __device__ __forceinline__ int tile_end(const W& w, int x, int tokens) {
     const int t = w.t0 + x * tokens, n = w.q.n;
     return t < n ? w.q.start + min(t + tokens, n) : 0;
-}
-
-// Whether the pair has a tile B.
-template <typename W>
-__device__ __forceinline__ bool tile_b(const W& w, int tokens) {
-    return w.t0 + tokens < w.q.n;
 }
 
 // Piece of the line of cost `total` that its unit u lies in; piece i begins at i * total / pieces.
@@ -313,76 +336,62 @@ __device__ __noinline__ void finish_rows(const ChunkParams& p, const Seq& sq, in
 }
 
 // ---- softmax and output rows -----------------------------------------------------------------------------------------
-// Barriers of the CTA, in shared memory.
-struct Bars {
-    uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t w_full[2], w_empty[2];  // a work has been published; every warp is done with what it needs of it
-    uint64_t q_full[2], q_empty[2];  // like those below: tile A, tile B
-    uint64_t s_full[2];              // the tile's scores are in TMEM
-    uint64_t p_full[2][2];           // its weights of the step's first, second 64 keys are
-    uint64_t o_full[2];              // its accumulator is complete
-    uint64_t lo_done[2];             // the products of a step's first 64 keys are in the accumulator
-    uint64_t o_free[2];              // the accumulator has been read
-    uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
-    uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
-    uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
-    uint64_t drain;
-};
-static_assert(sizeof(Bars) == kBars * 8, "layout");
-
 // What a warp of the softmax has counted: the tile's steps; tiles taken; those of B; steps with keys in the second half, as the
 // first half counts them.
 struct Counts {
     int ns, no, nb, step2;
 };
 
-// The tile of one work. Alone: there is no tile B, and A's rows are worked on by both tiles' warps, which take its odd and
-// even steps and the accumulators of B and A (few rows wait for K and V, and for one step's scores, weights and products
-// after the other: at 1.8 us a step, in turn, an SM takes half of its share of the memory's bandwidth). Weights are
-// then two fp16 parts, for which such pairs leave the tensor core the time: the relative error is that of the output's
-// rounding, 2.1e-4 (with one part 2.9e-4).
-template <int G, bool alone>
+// The tile of one work. Few: the tile is alone, and its rows are worked on by both tiles' warps, which take its even and odd steps
+// and the accumulators of A and B (few rows wait for K and V, and for one step's scores, weights and products after the
+// other). Where it has at most 64 rows, lanes 64-127 hold the same queries again: their warps make the same weights and store
+// what the rounding to fp16 left of them, so that one product takes both parts, and the two halves of the accumulators are added
+// in the end. The relative error is then that of the output's rounding, 2.1e-4 (with one part 2.9e-4).
+template <int G, bool kFew>
 __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w,
                                              const WaitCtx& ctx, Counts& cnt) {
-    constexpr int kTokens = kRows / G;
+    constexpr int kTokens = kRows / G, kTiles = kFew ? 1 : 2;
+    using L = Layout<kFew>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Bars& bars = *reinterpret_cast<Bars*>(smem + off_bars);
+    Bars& bars = *reinterpret_cast<Bars*>(smem + L::bars);
     const int x = warp >> 3, h = (warp >> 2) & 1;  // tile, half of the keys (and of the output's dims)
-    const int row = threadIdx.x & 127;
+    const int lane_row = threadIdx.x & 127;
+    const bool dup = kFew && w.q.n <= kRows / 2 / G, low = dup && lane_row >= 64;
+    const int row = dup ? lane_row & 63 : lane_row;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + x * 128 + h * 64;  // this half's scores, and its weights over the first 32
     const uint32_t o_at = tmem + lanes + 256 + x * 128;
-    volatile float* ref_at = reinterpret_cast<volatile float*>(smem + off_ref) + x * kRows + row;
-    float2* parts = reinterpret_cast<float2*>(smem + off_parts) + x * 2 * kRows + row;  // + buffer * 4 kRows + half * kRows
+    volatile float* ref_at = reinterpret_cast<volatile float*>(smem + L::ref) + x * kRows + lane_row;
+    float2* parts = reinterpret_cast<float2*>(smem + L::parts) + x * 2 * kRows + lane_row;  // + buffer * 4 kRows + half * kRows
     uint64_t* settled = &bars.first_ref[x][warp & 3];
     uint64_t* second = &bars.half_done[x][warp & 3];
-    volatile int* late_at = reinterpret_cast<volatile int*>(smem + off_late) + x * 4 + (warp & 3);
+    volatile int* late_at = reinterpret_cast<volatile int*>(smem + L::late) + x * 4 + (warp & 3);
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
-    constexpr int kNext = alone ? 2 * kRows : kRows;  // from one of the tile's steps to the next
-    const bool both = !alone || w.j1 - w.j0 > 1;      // B's warps have something to do
-    const int skip = alone ? x * kRows : 0;
+    constexpr int kNext = kFew ? 2 * kRows : kRows;  // from one of the tile's steps to the next
+    const bool both = !kFew || w.j1 - w.j0 > 1;      // B's warps have something to do
+    const int skip = kFew ? x * kRows : 0;
     // Positions are counted from the tile's first key of the piece.
-    const int end = tile_end(w, alone ? 0 : x, kTokens) - w.j0 * kRows - skip;
+    const int end = tile_end(w, kFew ? 0 : x, kTokens) - w.j0 * kRows - skip;
     const int all = min(w.j1 - w.j0, ceil_div(max(end + skip, 0), kRows));
-    const int steps = alone ? (all + 1 - x) >> 1 : all;
-    auto first_token = [&]() { return w.q.start - w.j0 * kRows + w.t0 + (alone ? 0 : x * kTokens) - skip; };
+    const int steps = kFew ? (all + 1 - x) >> 1 : all;
+    auto first_token = [&]() { return w.q.start - w.j0 * kRows + w.t0 + (kFew ? 0 : x * kTokens) - skip; };
     if (steps == 0) {  // tile A may end before the piece begins
-        if (!alone && w.state >= 0 && h == 0 && first_token() + row / G < end)
-            p.ml[((int64_t)w.state * 2 + x) * kRows + row] = make_float2(-INFINITY, 0.f);
-        if (!alone || x == 0) cnt.nb += both;
+        if (!kFew && w.state >= 0 && h == 0 && first_token() + row / G < end)
+            p.ml[((int64_t)w.state * kTiles + x) * kRows + row] = make_float2(-INFINITY, 0.f);
+        cnt.nb += kFew && both;
         return true;
     }
-    // The accumulators are complete; then they have been read: A's warps read B's, too, where A is alone.
+    // The accumulators are complete; then they have been read: A's warps read B's, too, where A is kFew.
     auto complete = [&]() {
-        return warp_wait(&bars.o_full[x], cnt.no & 1, ctx) && (!alone || x == 1 || !both || warp_wait(&bars.o_full[1], cnt.nb & 1, ctx));
+        return warp_wait(&bars.o_full[x], cnt.no & 1, ctx) && (!kFew || x == 1 || !both || warp_wait(&bars.o_full[1], cnt.nb & 1, ctx));
     };
     auto have_read = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&bars.o_free[x]);
-            if (alone && both) mbar_arrive(&bars.o_free[1]);
+            if (kFew && both) mbar_arrive(&bars.o_free[1]);
         }
     };
     if (first_token() + (row & ~31) / G >= end) {
@@ -401,9 +410,9 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             __syncwarp();
         }
         if (!complete()) return false;
-        if (!alone || x == 0) have_read();
+        if (!kFew || x == 0) have_read();
         ++cnt.no;
-        cnt.nb += both;
+        cnt.nb += kFew && both;
         return true;
     }
     // Keys from `masked` on are in steps with keys behind the tile's first token; the others are whole. (It may begin before the
@@ -458,7 +467,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             }
             return fmaxf(m0, m1);
         };
-        uint32_t ph[alone ? 16 : 32];  // the weights, in fp16
+        uint32_t ph[32];  // the weights, in fp16
         auto weights = [&]() {  // returns their sum
             const float nref = ref == -INFINITY ? 0.f : -ref;
             const uint64_t refx2 = pack_f32x2(nref, nref);
@@ -469,7 +478,6 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
                     uint32_t r[32];
                     fetch(c, r);
                     const float* f = reinterpret_cast<const float*>(r);
-                    uint32_t pl[alone ? 16 : 1];  // what they leave of them
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float a, b;
@@ -480,18 +488,12 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
                             sum1 = add_f32x2(sum1, pack_f32x2(a, b));
                         else
                             sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-                        const uint32_t y = pack_half2(a, b);
-                        if constexpr (alone) {
+                        uint32_t y = pack_half2(a, b);
+                        if (kFew && low) {
                             const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&y));
-                            ph[i] = y;
-                            pl[i] = pack_half2(a - hi.x, b - hi.y);
-                        } else {
-                            ph[c * 16 + i] = y;
+                            y = pack_half2(a - hi.x, b - hi.y);
                         }
-                    }
-                    if constexpr (alone) {
-                        tmem_st16(s_at + c * 32, ph);
-                        tmem_st16(s_at + c * 32 + 16, pl);
+                        ph[c * 16 + i] = y;
                     }
                 }
             }
@@ -525,9 +527,8 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             }
         };
         // The reference that this half's keys ask for: above the present one by a whole number.
-        float top = 0.f;  // alone: the half's largest score
         auto raised = [&]() {
-            const float to = ref_for(alone ? top : greatest() * sl2);
+            const float to = ref_for(greatest() * sl2);
             return ref == -INFINITY ? to : to > ref ? ref + ceilf(to - ref) : ref;
         };
         if (j > 0) {  // the other half may have raised it in the step before
@@ -543,16 +544,10 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             if (!warp_wait(settled, cnt.no & 1, ctx)) return false;
             ref = *ref_at;
         }
-        // (Where A is alone both parts of the weights take the scores' place, so the largest score decides before they are made:
-        // a weight of 2^15 fits fp16.)
-        float sum = 0.f;
-        if constexpr (alone)
-            top = greatest() * sl2;
-        else
-            sum = weights();
+        float sum = weights();
         // (A row without a finite score has cnt.no reference yet, and asks for one. One whose scores are NaN, such as those
         // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
-        const bool ask = alone ? top > ref + 15.f : ref == -INFINITY ? !isnan(sum) : sum > kMost;
+        const bool ask = ref == -INFINITY ? !isnan(sum) : sum > kMost;
         const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, ask);
         if (h == 0 && raise) {
             // The second half's weights of this step are in TMEM already, unless it raises, too, after this.
@@ -565,25 +560,22 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             }
             tc_fence_after();
             if (__any_sync(0xffffffffu, f2 != 1.f)) {
-#pragma unroll 1
-                for (int part = 0; part < (alone ? 2 : 1); ++part) {
-                    uint32_t t[32];
-                    tmem_ld32(s_at + 64 + 32 * part, t);
-                    tmem_wait_ld();
-                    tmem_use32(t);
+                uint32_t t[32];
+                tmem_ld32(s_at + 64, t);
+                tmem_wait_ld();
+                tmem_use32(t);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
-                        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
-                        t[i] = pack_half2(v.x * f2, v.y * f2);
-                    }
-                    tmem_st32(s_at + 64 + 32 * part, t);
+                for (int i = 0; i < 32; ++i) {  // in fp32: weights of up to 2^16 times a power of two that fp16 may not have
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
+                    t[i] = pack_half2(v.x * f2, v.y * f2);
                 }
+                tmem_st32(s_at + 64, t);
             }
             scale_sum(to);
             ref = to;
             *ref_at = ref;
             scale_acc(f);
-            if constexpr (!alone) sum = weights();
+            sum = weights();
         } else if (h == 1) {
             if (raise) {
                 if (lane == 0) *late_at = 1;
@@ -601,16 +593,15 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
                 ref = to;
                 *ref_at = ref;
                 scale_acc(f);
-                if constexpr (!alone) sum = weights();
+                sum = weights();
             } else if (lane == 0) {
                 *late_at = 0;
             }
         }
-        if constexpr (alone) sum = weights();
         if (last > 64) ++cnt.step2;
         l += sum;
         parts[(cnt.no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
-        if constexpr (!alone) tmem_st32(s_at, ph);
+        tmem_st32(s_at, ph);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -620,7 +611,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         }
     }
     if (!complete()) return false;
-    if (alone && x == 1) {  // A's warps read the accumulator
+    if (kFew && x == 1) {  // A's warps read the accumulator
         ++cnt.no;
         return true;
     }
@@ -637,7 +628,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
     };
     float2 y = sum_of(parts + (cnt.no & 1) * 4 * kRows, end > 64);
     float fa = 1.f, fb = 0.f;  // factors of the accumulators
-    if (alone && both) {
+    if (kFew && both) {
         const float2 yb = sum_of(parts + (cnt.nb & 1) * 4 * kRows + 2 * kRows, end - kRows > 64);
         const bool some_a = y.y != 0.f, some_b = yb.y != 0.f;
         const float top = some_b && (!some_a || yb.x > y.x) ? yb.x : y.x;
@@ -652,7 +643,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         tmem_ld32(o_at + h * 64 + c * 32, o);
         tmem_wait_ld();
         tmem_use32(o);
-        if (alone && both) {
+        if (kFew && both) {
             uint32_t ob[32];
             tmem_ld32(o_at + 128 + h * 64 + c * 32, ob);
             tmem_wait_ld();
@@ -663,11 +654,24 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
                                        (fb < 0.f ? 0.f : __uint_as_float(ob[i]) * fb));
         }
         if (c == 1) have_read();  // the next tiles' products may overwrite them
+        if (kFew && dup) {  // rows 64-127 hand over what they have; a row of 33 floats, so that lanes are in different banks
+            float* at = reinterpret_cast<float*>(smem + L::low) + (h * 64 + row) * 33;
+            if (low) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) at[i] = __uint_as_float(o[i]);
+            }
+            named_barrier_sync(1 + h * 2 + (warp & 1), 64);
+            if (!low) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + at[i]);
+            }
+            if (c == 0) named_barrier_sync(1 + h * 2 + (warp & 1), 64);  // before they hand over the next
+        }
     };
-    const bool mine = first_token() + row / G < end;
+    const bool mine = !low && first_token() + row / G < end;
     const int state = w.state;
     if (state >= 0) {  // columns in fours, rows side by side
-        float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)state * 2 + x) * 32 + h * 16) * kRows + row;
+        float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)state * kTiles + x) * 32 + h * 16) * kRows + row;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             uint32_t o[32];
@@ -679,9 +683,9 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
                                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
         }
-        if (h == 0 && mine) p.ml[((int64_t)state * 2 + x) * kRows + row] = y;
+        if (h == 0 && mine) p.ml[((int64_t)state * kTiles + x) * kRows + row] = y;
         ++cnt.no;
-        cnt.nb += both;
+        cnt.nb += kFew && both;
         return true;
     }
     const float inv = 1.f / total;
@@ -695,7 +699,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (row & ~3) + i, t = w.t0 + x * kTokens + r / G;
-        in[i] = first_token() + r / G < end;
+        in[i] = !low && first_token() + r / G < end;
         dst[i] = static_cast<__half*>(p.out) + (int64_t)(w.q.first + t) * p.out_stride + (w.h * G + r % G) * kHeadDim +
                  h * 64 + q4 * 8;
     }
@@ -725,7 +729,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
     }
     ++cnt.no;
-    cnt.nb += both;
+    cnt.nb += kFew && both;
     // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
     // themselves 1, or above 1/2.
     const bool low_sum = !(total >= 0.25f);
@@ -739,42 +743,46 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
     return true;
 }
 
-// A call of its own: inlined next to the other, it takes registers from it (8192 tokens 370 -> 396 us).
-template <int G>
-__device__ __noinline__ bool softmax_alone(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w, WaitCtx ctx,
-                                           Counts& cnt) {
-    return softmax_tile<G, true>(p, smem, tmem, w, ctx, cnt);
-}
-
 // ---- the tensor-core kernel ---------------------------------------------------------------------------------------
-template <int G>
+template <int G, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params prm) {
     constexpr int kTokens = kRows / G;  // tokens of a tile
+    using L = Layout<kFew>;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const ChunkParams& p = prm.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    Bars& bars = *reinterpret_cast<Bars*>(smem + off_bars);
-    const Work* work = reinterpret_cast<const Work*>(smem + off_work);  // [2]
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc);
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + off_misc + 4);
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + off_scan);
-    int64_t* begin_off = reinterpret_cast<int64_t*>(smem + off_begin);
-    int32_t* begin_seq = reinterpret_cast<int32_t*>(smem + off_begin + 8);
+    Bars& bars = *reinterpret_cast<Bars*>(smem + L::bars);
+    const Work* work = reinterpret_cast<const Work*>(smem + L::work);  // [2]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + L::misc + 4);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + L::scan);
+    int64_t* begin_off = reinterpret_cast<int64_t*>(smem + L::begin);
+    int32_t* begin_seq = reinterpret_cast<int32_t*>(smem + L::begin + 8);
     const WaitCtx ctx{abort_flag, &p.hdr->status, p.wait_ns};
 
-    grid_launch_dependents();
     // The line: up to 32 sequences are scanned by the warp that walks the piece, a lane each. Of more, every thread sums a run
     // (the first one's bounds are on their way while the barriers are set up), the CTA scans the sums, and the thread whose
     // run holds the piece's first unit finds its sequence.
     const bool few = p.num_seqs <= 32;
+    grid_launch_dependents();
+    if (few && p.split) {  // nothing for this kernel: every warp sees it
+        bool b;
+        const Seq q = lane < p.num_seqs ? own_seq<G, kFew>(p, lane, b) : Seq{0, 0, 0};
+        if (!__any_sync(0xffffffffu, q.n > 0)) {
+            if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
+            grid_dependency_wait();
+            return;
+        }
+    }
     const int per = few ? 1 : ceil_div(p.num_seqs, kThreads);
     const int self = few ? (warp == 18 ? lane : p.num_seqs) : (int)threadIdx.x * per;
     const int s0 = min(p.num_seqs, self), s1 = min(p.num_seqs, s0 + per);
     bool bad = false;
     Seq sq0{0, 0, 0};
-    if (s0 < s1) sq0 = load_seq(p, s0, bad);
+    if (s0 < s1) sq0 = own_seq<G, kFew>(p, s0, bad);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.kv_full[i], 1);
@@ -805,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     int64_t mine = s0 < s1 ? cost_of<G>(sq0) : 0;
     for (int s = s0 + 1; s < s1; ++s) {
         bool b;
-        mine += cost_of<G>(load_seq(p, s, b));
+        mine += cost_of<G>(own_seq<G, kFew>(p, s, b));
         bad |= b;
     }
     if (bad && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             int64_t at = before;
             for (int s = s0; s < s1; ++s) {
                 bool b;
-                const int64_t n = cost_of<G>(s == s0 ? sq0 : load_seq(p, s, b)) * head_groups;
+                const int64_t n = cost_of<G>(s == s0 ? sq0 : own_seq<G, kFew>(p, s, b)) * head_groups;
                 if (lo < at + n) {
                     *begin_seq = s;
                     *begin_off = lo - at;
@@ -882,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 int s;
                 int64_t rest;
                 auto take = [&](int i) {  // sequence i
-                    if (!few) return load_seq(p, i, b);
+                    if (!few) return own_seq<G, kFew>(p, i, b);
                     return Seq{__shfl_sync(0xffffffffu, sq0.first, i), __shfl_sync(0xffffffffu, sq0.n, i),
                                __shfl_sync(0xffffffffu, sq0.start, i)};
                 };
@@ -962,6 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (lane == 0) {
                 prefetch_tensormap(map);
                 if (!of_v) prefetch_tensormap(&prm.q);
+                if (!of_v) prefetch_tensormap(&prm.q64);
             }
             uint64_t ordinary;
             asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(ordinary));
@@ -983,11 +992,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (tile_end(w, x, kTokens) <= w.j0 * kRows) return true;
                     if (!warp_wait(&bars.q_empty[x], (nq[x] & 1) ^ 1, ctx)) return false;
                     if (lane == 0) {
-                        uint8_t* dst = smem + off_q + x * kTileBytes;
+                        uint8_t* dst = smem + L::q + x * kTileBytes;
+                        const bool dup = kFew && w.q.n <= kRows / 2 / G;
                         mbar_arrive_expect_tx(&bars.q_full[x], kTileBytes);
                         for (int b = 0; b < 2; ++b)
-                            tma_load_3d(dst + b * kBoxBytes, &prm.q, b * 64, w.h * G, w.q.first + w.t0 + x * kTokens,
-                                        &bars.q_full[x], stream);
+                            for (int i = 0; i <= dup; ++i)
+                                tma_load_3d(dst + b * kBoxBytes + i * kBoxBytes / 2, dup ? &prm.q64 : &prm.q, b * 64, w.h * G,
+                                            w.q.first + w.t0 + x * kTokens, &bars.q_full[x], stream);
                     }
                     __syncwarp();
                     ++nq[x];
@@ -1007,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     // cleared before the tile counts as loaded.
                     const bool tail = of_v && (j + 1) * kRows >= end && (end & 15);
                     uint64_t* bar = tail ? &bars.tail_full : &bars.kv_full[st];
-                    uint8_t* dst = smem + off_ring + st * kTileBytes;
+                    uint8_t* dst = smem + L::ring + st * kTileBytes;
                     // lane 2 i + half: half of the dims of the step's page i
                     const int page = __shfl_sync(0xffffffffu, ent, ((j - w.j0) & 3) * kStepPages + ((lane >> 1) & 7));
                     if (lane == 0) mbar_arrive_expect_tx(bar, n * 2 * kPageBox);
@@ -1035,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             // every copy that this warp issued lands before the CTA may end
             if (nc > 0) warp_drain(&bars.tail_full, (nc - 1) & 1);
-            for (int j = max(seq0, seq - kStages); j < seq; j += 2) warp_drain(&bars.kv_full[j % kStages], (j / kStages) & 1);
+            for (int j = max(seq0, seq - kStages / 2 * 2); j < seq; j += 2) warp_drain(&bars.kv_full[j % kStages], (j / kStages) & 1);
             for (int x = 0; x < 2; ++x)
                 if (nq[x] > 0) warp_drain(&bars.q_full[x], (nq[x] - 1) & 1);
         } else if (warp == 16) {
@@ -1055,18 +1066,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     const int end0 = min(tile_end(w, 0, kTokens) - w.j0 * kRows, most);
                     const int end1 = min(tile_end(w, 1, kTokens) - w.j0 * kRows, most);
                     // ring positions: K_j at kv + 2j, V_j one behind it
-                    const uint32_t ring = smem_addr(smem + off_ring);
+                    const uint32_t ring = smem_addr(smem + L::ring);
                     auto stage_addr = [&](int pos) { return ring + (pos % kStages) * kTileBytes; };
                     auto wait_stage = [&](int pos) { return thread_wait(&bars.kv_full[pos % kStages], (pos / kStages) & 1, ctx); };
                     auto release = [&](int pos) { mma_commit(&bars.kv_empty[pos % kStages]); };
                     constexpr uint32_t idesc_v = mma_idesc(kHeadDim, true);
-                    if (tile_b(w, kTokens)) {
+                    if constexpr (!kFew) {
                         // keys of the piece's step j that tile x needs (0: none)
                         auto keys = [&](int x, int j) { return max(0, min(kRows, (x ? end1 : end0) - j * kRows)); };
                         auto scores = [&](int x, int j) {  // S_x(j) = Q_x K_j^T
                             const int n = (keys(x, j) + 15) & ~15;
                             if (n == 0) return;
-                            const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q + x * kTileBytes));
+                            const uint64_t q = smem_desc_k_major(smem_addr(smem + L::q + x * kTileBytes));
                             const uint64_t kd = smem_desc_k_major(stage_addr(kv + 2 * j));
                             const uint32_t idesc = mma_idesc(n, false);
                             const bool last = keys(x, j + 1) == 0;  // the tile's last use of its queries
@@ -1126,12 +1137,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             }
                         }
                     } else {
-                        // A alone: its odd steps are B's. (The same in general terms for both: its operands leave the uniform registers, and
-                        // pairs take 7 % longer.)
+                        // One tile: its even steps are A's, its odd ones B's.
                         ok = thread_wait(&bars.q_full[0], nq[0] & 1, ctx);
                         ++nq[0];
                         tc_fence_after();
-                        const uint64_t q = smem_desc_k_major(smem_addr(smem + off_q));
+                        const uint64_t q = smem_desc_k_major(smem_addr(smem + L::q));
                         for (int i = 0; i < steps + 2 && ok; ++i) {  // values of step i - 2, scores of step i
                             const int x = i & 1, j = i - 2;
                             if (j >= 0) {
@@ -1146,12 +1156,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                     ok = thread_wait(&bars.p_full[x][half], np[x][half] & 1, ctx);
                                     ++np[x][half];
                                     tc_fence_after();
-                                    for (int k16 = 0; k16 < min(4, n - 4 * half); ++k16) {  // 32 keys: 16 columns of first parts, 16 of second
-                                        const uint32_t at = tmem + x * 128 + 64 * half + 32 * (k16 >> 1) + 8 * (k16 & 1);
-                                        const uint64_t vk = v + 512 * half + 128 * k16;
-                                        mma_ts(tmem + 256 + x * 128, at, vk, idesc_v, j > 1 || half > 0 || k16 > 0);
-                                        mma_ts(tmem + 256 + x * 128, at + 16, vk, idesc_v, true);
-                                    }
+                                    const uint32_t o = tmem + 256 + x * 128, pw = tmem + x * 128 + 64 * half;
+                                    const int c = min(4, n - 4 * half);
+                                    if (c == 4)
+                                        mma_ts_64(o, pw, v + 512 * half, idesc_v, j > 1 || half > 0);
+                                    else
+                                        for (int k16 = 0; k16 < c; ++k16)
+                                            mma_ts(o, pw + 8 * k16, v + 512 * half + 128 * k16, idesc_v, j > 1 || half > 0 || k16 > 0);
                                     if (half == 0) mma_commit(&bars.lo_done[x]);
                                     if (j + 2 >= steps && n - 4 * half <= 4) mma_commit(&bars.o_full[x]);
                                 }
@@ -1187,16 +1198,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (!warp_wait(&bars.w_full[k & 1], (k >> 1) & 1, ctx)) break;
             const volatile Work& w = reinterpret_cast<const volatile Work*>(work)[k & 1];
             if (w.h < 0) break;
-            if (tile_b(w, kTokens)) {
-                if (!softmax_tile<G, false>(p, smem, tmem, w, ctx, counts)) break;
-            } else {
-                Counts c = counts;  // (of which the call takes the address)
-                const bool ok = softmax_alone<G>(p, smem, tmem, w, ctx, c);
-                counts = c;
-                if (!ok) break;
-            }
+            if (!softmax_tile<G, kFew>(p, smem, tmem, w, ctx, counts)) break;
         }
     }
+    if (!kFew) grid_dependency_wait();  // the kernel before it, whose states are added up by the one behind it
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
@@ -1212,12 +1217,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 constexpr int kMergeWarps = 8;
 
 template <int G>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkParams first, const ChunkParams second) {
     constexpr int kTokens = kRows / G;
     __shared__ uint32_t s_bad[2], s_redo;  // rows with a value that is not finite, by half of the dims; wrong for certain
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
-    const Merge m = static_cast<const Merge*>(p.merges)[blockIdx.x];
+    const bool is_first = (int)blockIdx.x < first.grid;
+    const ChunkParams& p = is_first ? first : second;
+    const int cta = blockIdx.x - (is_first ? 0 : first.grid), tiles = p.tiles;
+    const Merge m = static_cast<const Merge*>(p.merges)[cta];
     const int r0 = (int)blockIdx.y * 32;  // of the pair's 256 rows
     const int valid = min(32, (min(m.q.n, m.t0 + 2 * kTokens) - m.t0) * G - r0);
     if (m.pieces <= 1 || valid <= 0) return;
@@ -1229,7 +1237,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
     const int rows = 32 / span, row = r0 + lane % rows, turn = lane / rows;
     const float2* ml = p.ml + row;
     const float4* acc = reinterpret_cast<const float4*>(p.acc) + ((row >> 7) * 32 + warp * 4) * kRows + (row & 127);
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i * p.lanes)); };
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * cta + 1 : 2 * (cta + i * p.lanes)); };
     // Four states at a time, all of their loads in flight together.
     constexpr int kBatch = 4;
     float top = -INFINITY, total = 0.f;
@@ -1249,9 +1257,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
             const int i = min(i0 + e * span, m.pieces - 1);
-            x[e] = __ldcg(ml + slot(i) * 2 * kRows);
+            x[e] = __ldcg(ml + slot(i) * tiles * kRows);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) a[e][c] = __ldcg(acc + slot(i) * 2 * 32 * kRows + c * kRows);
+            for (int c = 0; c < 4; ++c) a[e][c] = __ldcg(acc + slot(i) * tiles * 32 * kRows + c * kRows);
         }
         float to = top;
 #pragma unroll
@@ -1314,35 +1322,42 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
     if (warp < 2 && s_bad[warp]) finish_rows<G>(p, m.q, m.s, m.t0 + r0 / G, m.h, warp, s_bad[warp], s_redo & s_bad[warp]);
 }
 
-template <int G>
-int launch(const Params& prm, cudaStream_t stream) {
+template <int G, bool kFew>
+int launch_one(const Params& prm, bool behind, cudaStream_t stream) {
     static int configured_mask = 0;  // one bit per device ordinal (< 32)
+    constexpr int smem = Layout<kFew>::bytes;
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 32 || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
         cudaFuncAttributes a{};
-        cudaError_t e = cudaFuncGetAttributes(&a, chunk_kernel<G>);
+        cudaError_t e = cudaFuncGetAttributes(&a, chunk_kernel<G, kFew>);
         if (e != cudaSuccess) return e;
         // the warpgroups' register shares come out of what the launch gives them
         if (a.numRegs * kThreads < kSoftmax * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(chunk_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(chunk_kernel<G, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    const cudaError_t e = launch_kernel(chunk_kernel<G>, prm.p.grid, kThreads, kSmem, stream, prm);
+    return launch_behind(chunk_kernel<G, kFew>, dim3((unsigned)prm.p.grid), dim3(kThreads), smem, behind, stream, prm);
+}
+
+// Sequences of one tile of new tokens go to one kernel, those of more to the other, which is launched behind it and begins where
+// its CTAs end; both where the host cannot tell (the lengths are on the device). In this order, since a kernel that has no
+// sequences ends at once, behind the other in its CTAs' shadow, before it not (16 sequences of 2-8 tokens 212 -> @@ us).
+template <int G>
+int launch(const Params& prm, const Params& prm_few, cudaStream_t stream) {
+    const ChunkParams& p = prm.p;
+    const bool only_few = p.seq_lens || p.total_tokens <= kRows / G, only_many = !only_few && p.num_seqs == 1;
+    int e = cudaSuccess;
+    Params x = prm, y = prm_few;
+    x.p.split = y.p.split = !only_few && !only_many;
+    if (!only_many) e = launch_one<G, true>(y, false, stream);
+    if (e == cudaSuccess && !only_few) e = launch_one<G, false>(x, !only_many, stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     // 32 rows a block, of the most that a pair may have
-    const int64_t rows = prm.p.seq_lens ? G : std::min<int64_t>(2 * kRows, (int64_t)prm.p.total_tokens * G);
-    cfg.gridDim = dim3((unsigned)prm.p.grid, (unsigned)((rows + 31) / 32));
-    cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel<G>, prm.p);
+    const int64_t most = only_few ? kRows : 2 * kRows, rows = p.seq_lens ? G : std::min<int64_t>(most, (int64_t)p.total_tokens * G);
+    const dim3 grid((unsigned)(x.p.split ? 2 * p.grid : p.grid), (unsigned)((rows + 31) / 32));
+    return launch_behind(merge_kernel<G>, grid, dim3(kMergeWarps * 32), 0, true, stream, only_few ? y.p : x.p, y.p);
 }
 
 // KV heads whose CTAs read the same pages at the same time: of the divisors of Hkv up to 8 (a token's K of 8 heads are 2 KB
@@ -1354,12 +1369,24 @@ int head_lanes(int hkv, int num_sms) {
     return best;
 }
 
+// The workspace behind its header: a Merge a CTA of both kernels, then the states of both, two a CTA.
+struct ChunkLayout {
+    size_t merges, states, few, bytes;
+};
+
+ChunkLayout chunk_layout(int num_sms) {
+    const size_t row = sizeof(float2) + kRowBytes * 2, n = (size_t)num_sms;
+    ChunkLayout l;
+    l.merges = sizeof(pkv_ws_header);
+    l.states = l.merges + (2 * n * kChunkMergeBytes + kWsAlign - 1) / kWsAlign * kWsAlign;
+    l.few = l.states + n * 2 * 2 * kRows * row;
+    l.bytes = l.few + n * 2 * kRows * row;
+    return l;
+}
+
 }  // namespace
 
-size_t chunk_workspace_bytes(int num_sms) {
-    const size_t merges = ((size_t)num_sms * kChunkMergeBytes + kWsAlign - 1) / kWsAlign * kWsAlign;
-    return sizeof(pkv_ws_header) + merges + (size_t)num_sms * 2 * 2 * kRows * (sizeof(float2) + kRowBytes * 2);
-}
+size_t chunk_workspace_bytes(int num_sms) { return chunk_layout(num_sms).bytes; }
 
 int launch_chunk_attention(const ChunkParams& in, int num_sms, void* stream) {
     Params prm;
@@ -1367,25 +1394,32 @@ int launch_chunk_attention(const ChunkParams& in, int num_sms, void* stream) {
     p = in;
     p.lanes = head_lanes(p.Hkv, num_sms);
     p.grid = num_sms / p.lanes * p.lanes;
+    p.tiles = 2;
     uint8_t* ws = reinterpret_cast<uint8_t*>(p.hdr);
-    const size_t merges = ((size_t)num_sms * kChunkMergeBytes + kWsAlign - 1) / kWsAlign * kWsAlign;
-    p.merges = ws + sizeof(pkv_ws_header);
-    p.ml = reinterpret_cast<float2*>(ws + sizeof(pkv_ws_header) + merges);
+    const ChunkLayout l = chunk_layout(num_sms);
+    p.merges = ws + l.merges;
+    p.ml = reinterpret_cast<float2*>(ws + l.states);
     p.acc = reinterpret_cast<float*>(p.ml + (size_t)num_sms * 2 * 2 * kRows);
     p.wait_ns = kWaitLimitNs + std::min(kFinishMostNs, kFinishNs * kPageSize * (uint64_t)p.max_pages);
     const int g = p.Hq / p.Hkv;
     const int64_t token = (int64_t)p.Hkv * kHeadDim;
     if (!encode_rows(&prm.q, p.q, p.Hq, p.total_tokens, p.q_stride, g, kRows / g) ||
+        !encode_rows(&prm.q64, p.q, p.Hq, p.total_tokens, p.q_stride, g, kRows / 2 / g) ||
         !encode_rows(&prm.k, p.k_pool, p.Hkv, (int64_t)p.num_pages * kPageSize, token, 1, kPageSize) ||
         !encode_rows(&prm.v, p.v_pool, p.Hkv, (int64_t)p.num_pages * kPageSize, token, 1, kPageSize))
         return cudaErrorInvalidValue;
+    Params few = prm;
+    few.p.tiles = 1;
+    few.p.merges = ws + l.merges + (size_t)num_sms * kChunkMergeBytes;
+    few.p.ml = reinterpret_cast<float2*>(ws + l.few);
+    few.p.acc = reinterpret_cast<float*>(few.p.ml + (size_t)num_sms * 2 * kRows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (g) {
-        case 1: return launch<1>(prm, s);
-        case 2: return launch<2>(prm, s);
-        case 4: return launch<4>(prm, s);
-        case 8: return launch<8>(prm, s);
-        case 16: return launch<16>(prm, s);
+        case 1: return launch<1>(prm, few, s);
+        case 2: return launch<2>(prm, few, s);
+        case 4: return launch<4>(prm, few, s);
+        case 8: return launch<8>(prm, few, s);
+        case 16: return launch<16>(prm, few, s);
         default: return cudaErrorInvalidValue;
     }
 }

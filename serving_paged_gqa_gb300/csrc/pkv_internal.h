@@ -132,8 +132,9 @@ struct ChunkParams {
     float scale_log2;
     // set by the launcher
     int32_t lanes, grid;  // KV heads side by side, CTAs
+    int32_t split, tiles; // there is another kernel for sequences of the other kind; tiles of a state
     void* merges;         // a kChunkMergeBytes entry a CTA
-    float2* ml;           // [state][256]: (reference, sum) of a row
+    float2* ml;           // [state][tile][128]: (reference, sum) of a row
     float* acc;           // [state][tile][32][128][4]: its accumulator
     uint64_t wait_ns;     // limit of a wait
 };
@@ -171,6 +172,7 @@ struct SelectParams {
     double* exact;   // the same, of pages near the border
     float* tops;     // [B][Hkv][ceil(max_pages / 16)]: largest magnitude of 16 pages' finite bounds
     int32_t B, Hq, Hkv, num_pages, max_pages, select;
+    int32_t tiles;   // of 16 pages that a CTA scores (set by the launcher)
 };
 
 // Kernel launchers (defined in the .cu files). They return the CUDA error of the launch.
