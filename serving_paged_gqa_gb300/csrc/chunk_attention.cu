@@ -46,8 +46,10 @@ constexpr int kThreads = kSoftmax + 128;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96, what the launch has
 constexpr float kMost = 65504.f;             // sum of 64 weights above which the row's reference is raised
 constexpr float kLift = 5.f;                 // the largest weight where the reference was set, in powers of two
-// What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps.
-constexpr int kPairCost = 2;
+// What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps. A
+// sequence of one tile waits for memory meanwhile, which its copies ahead keep busy.
+template <bool kFew>
+constexpr int kPairCost = kFew ? 1 : 2;
 constexpr int kMinCost = 2;                  // of a piece, at least
 constexpr int kWhole = 5;                    // cost of a pair that is not cut where a piece has no more
 
@@ -157,11 +159,11 @@ __device__ __forceinline__ int keys_of(const Seq& q, int t0) {
 
 // Cost of the first m pairs, all of them whole: sum over i = 1..m of ceil((start + i T) / 128) + kPairCost, T = 256 / G tokens.
 // For G > 1 the quotient is ceil((c + i) / r) with c = ceil(start / T), r = 128 / T.
-template <int G>
+template <int G, bool kFew>
 __device__ __forceinline__ int64_t cost_before(const Seq& q, int m) {
     constexpr int T = 2 * kRows / G;
     if constexpr (T > kRows) {
-        return (int64_t)m * (ceil_div(q.start, kRows) + kPairCost) + (int64_t)m * (m + 1);
+        return (int64_t)m * (ceil_div(q.start, kRows) + kPairCost<kFew>) + (int64_t)m * (m + 1);
     } else {
         constexpr int r = kRows / T;
         const int64_t c = ceil_div(q.start, T);
@@ -169,14 +171,14 @@ __device__ __forceinline__ int64_t cost_before(const Seq& q, int m) {
             const int64_t a = x / r, b = x % r;
             return r * (a * (a + 1) / 2) + b * (a + 1);
         };
-        return upto(c + m) - upto(c) + (int64_t)m * kPairCost;
+        return upto(c + m) - upto(c) + (int64_t)m * kPairCost<kFew>;
     }
 }
 
-template <int G>
+template <int G, bool kFew>
 __device__ __forceinline__ int64_t cost_of(const Seq& q) {  // of one KV head
     const int m = pairs_of<G>(q);
-    return m == 0 ? 0 : cost_before<G>(q, m - 1) + kPairCost + ceil_div(q.start + q.n, kRows);
+    return m == 0 ? 0 : cost_before<G, kFew>(q, m - 1) + kPairCost<kFew> + ceil_div(q.start + q.n, kRows);
 }
 
 // Keys of tile x (0: A, 1: B) of a pair; 0: it has no rows.
@@ -763,26 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     int32_t* begin_seq = reinterpret_cast<int32_t*>(smem + L::begin + 8);
     const WaitCtx ctx{abort_flag, &p.hdr->status, p.wait_ns};
 
-    // The line: up to 32 sequences are scanned by the warp that walks the piece, a lane each. Of more, every thread sums a run
-    // (the first one's bounds are on their way while the barriers are set up), the CTA scans the sums, and the thread whose
-    // run holds the piece's first unit finds its sequence.
-    const bool few = p.num_seqs <= 32;
-    grid_launch_dependents();
-    if (few && p.split) {  // nothing for this kernel: every warp sees it
-        bool b;
-        const Seq q = lane < p.num_seqs ? own_seq<G, kFew>(p, lane, b) : Seq{0, 0, 0};
-        if (!__any_sync(0xffffffffu, q.n > 0)) {
-            if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
-            grid_dependency_wait();
-            return;
-        }
-    }
-    const int per = few ? 1 : ceil_div(p.num_seqs, kThreads);
-    const int self = few ? (warp == 18 ? lane : p.num_seqs) : (int)threadIdx.x * per;
-    const int s0 = min(p.num_seqs, self), s1 = min(p.num_seqs, s0 + per);
-    bool bad = false;
-    Seq sq0{0, 0, 0};
-    if (s0 < s1) sq0 = own_seq<G, kFew>(p, s0, bad);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.kv_full[i], 1);
@@ -809,11 +791,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *abort_flag = 0;
         mbar_fence_init();
     }
+    // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (The second of two
+    // kernels waits at its end: it begins when all CTAs of the first have got here.)
+    if (kFew || !p.split) grid_dependency_wait();
+    grid_launch_dependents();
+    // The line: up to 32 sequences are scanned by the warp that walks the piece, a lane each. Of more, every thread sums a run
+    // (the first one's bounds are on their way while the barriers are set up), the CTA scans the sums, and the thread whose
+    // run holds the piece's first unit finds its sequence.
+    const bool few = p.num_seqs <= 32;
+    if (few && p.split) {  // nothing for this kernel: every warp sees it
+        bool b;
+        const Seq q = lane < p.num_seqs ? own_seq<G, kFew>(p, lane, b) : Seq{0, 0, 0};
+        if (!__any_sync(0xffffffffu, q.n > 0)) {
+            if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
+            if (!kFew) grid_dependency_wait();
+            return;
+        }
+    }
+    const int per = few ? 1 : ceil_div(p.num_seqs, kThreads);
+    const int self = few ? (warp == 18 ? lane : p.num_seqs) : (int)threadIdx.x * per;
+    const int s0 = min(p.num_seqs, self), s1 = min(p.num_seqs, s0 + per);
+    bool bad = false;
+    Seq sq0{0, 0, 0};
+    if (s0 < s1) sq0 = own_seq<G, kFew>(p, s0, bad);
     if (warp == 16) tmem_alloc(tmem_at, 512);
-    int64_t mine = s0 < s1 ? cost_of<G>(sq0) : 0;
+    int64_t mine = s0 < s1 ? cost_of<G, kFew>(sq0) : 0;
     for (int s = s0 + 1; s < s1; ++s) {
         bool b;
-        mine += cost_of<G>(own_seq<G, kFew>(p, s, b));
+        mine += cost_of<G, kFew>(own_seq<G, kFew>(p, s, b));
         bad |= b;
     }
     if (bad && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
@@ -842,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             int64_t at = before;
             for (int s = s0; s < s1; ++s) {
                 bool b;
-                const int64_t n = cost_of<G>(s == s0 ? sq0 : own_seq<G, kFew>(p, s, b)) * head_groups;
+                const int64_t n = cost_of<G, kFew>(s == s0 ? sq0 : own_seq<G, kFew>(p, s, b)) * head_groups;
                 if (lo < at + n) {
                     *begin_seq = s;
                     *begin_off = lo - at;
@@ -880,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int near = total <= (int64_t)kWhole * pieces ? kWhole : 0;
             auto snap = [&](int u, int len) {
                 if (len <= near) return 2 * u <= len ? 0 : len;
-                return u <= kPairCost ? 0 : u >= len - 1 ? len : u;
+                return u <= kPairCost<kFew> ? 0 : u >= len - 1 ? len : u;
             };
             Merge merge{};
             int k = 0;
@@ -904,19 +909,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 Seq q = take(s);
                 int hg = 0;
                 if (head_groups > 1) {
-                    const int64_t of_head = cost_of<G>(q);
+                    const int64_t of_head = cost_of<G, kFew>(q);
                     hg = (int)(rest / of_head);
                     rest -= hg * of_head;
                 }
                 int left = 0, right = pairs_of<G>(q) - 1;  // the last pair that begins at or before `rest`
                 while (left < right) {
                     const int mid = (left + right + 1) >> 1;
-                    if (cost_before<G>(q, mid) <= rest)
+                    if (cost_before<G, kFew>(q, mid) <= rest)
                         left = mid;
                     else
                         right = mid - 1;
                 }
-                int pair = left, u = (int)(rest - cost_before<G>(q, pair));
+                int pair = left, u = (int)(rest - cost_before<G, kFew>(q, pair));
                 bool first = true;
                 for (int64_t at = lo - u; ok; first = false) {  // where the pair begins
                     Work w;
@@ -924,12 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     w.s = s;
                     w.t0 = pair * 2 * kTokens;
                     w.h = hg * p.lanes + (int)(blockIdx.x % p.lanes);
-                    const int steps = ceil_div(keys_of<G>(q, w.t0), kRows), len = steps + kPairCost;
+                    const int steps = ceil_div(keys_of<G>(q, w.t0), kRows), len = steps + kPairCost<kFew>;
                     if (first) u = snap(u, len);
                     const int end = at + len <= hi ? len : snap((int)(hi - at), len);
                     if (end > u) {
-                        w.j0 = max(0, u - kPairCost);  // (a cut leaves the pair's own cost to its first piece)
-                        w.j1 = end - kPairCost;
+                        w.j0 = max(0, u - kPairCost<kFew>);  // (a cut leaves the pair's own cost to its first piece)
+                        w.j1 = end - kPairCost<kFew>;
                         const bool whole = w.j0 == 0 && w.j1 == steps;
                         w.state = whole ? -1 : 2 * (int)blockIdx.x + (w.j0 == 0);
                         if (!whole && w.j0 == 0) {
@@ -1201,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (!softmax_tile<G, kFew>(p, smem, tmem, w, ctx, counts)) break;
         }
     }
-    if (!kFew) grid_dependency_wait();  // the kernel before it, whose states are added up by the one behind it
+    if (!kFew && p.split) grid_dependency_wait();  // the first kernel, whose states are added up by the one behind this
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
@@ -1221,7 +1226,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
     constexpr int kTokens = kRows / G;
     __shared__ uint32_t s_bad[2], s_redo;  // rows with a value that is not finite, by half of the dims; wrong for certain
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dependency_wait();
+    grid_dependency_wait();  // (and no dependents launched: the next step's kernels in the way, 32 sparse rows take 127 us, 117 without)
     const bool is_first = (int)blockIdx.x < first.grid;
     const ChunkParams& p = is_first ? first : second;
     const int cta = blockIdx.x - (is_first ? 0 : first.grid), tiles = p.tiles;
@@ -1323,7 +1328,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
 }
 
 template <int G, bool kFew>
-int launch_one(const Params& prm, bool behind, cudaStream_t stream) {
+int launch_one(const Params& prm, cudaStream_t stream) {
     static int configured_mask = 0;  // one bit per device ordinal (< 32)
     constexpr int smem = Layout<kFew>::bytes;
     int dev = 0;
@@ -1338,7 +1343,7 @@ int launch_one(const Params& prm, bool behind, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    return launch_behind(chunk_kernel<G, kFew>, dim3((unsigned)prm.p.grid), dim3(kThreads), smem, behind, stream, prm);
+    return launch_behind(chunk_kernel<G, kFew>, dim3((unsigned)prm.p.grid), dim3(kThreads), smem, stream, prm);
 }
 
 // Sequences of one tile of new tokens go to one kernel, those of more to the other, which is launched behind it and begins where
@@ -1351,13 +1356,13 @@ int launch(const Params& prm, const Params& prm_few, cudaStream_t stream) {
     int e = cudaSuccess;
     Params x = prm, y = prm_few;
     x.p.split = y.p.split = !only_few && !only_many;
-    if (!only_many) e = launch_one<G, true>(y, false, stream);
-    if (e == cudaSuccess && !only_few) e = launch_one<G, false>(x, !only_many, stream);
+    if (!only_many) e = launch_one<G, true>(y, stream);
+    if (e == cudaSuccess && !only_few) e = launch_one<G, false>(x, stream);
     if (e != cudaSuccess) return e;
     // 32 rows a block, of the most that a pair may have
     const int64_t most = only_few ? kRows : 2 * kRows, rows = p.seq_lens ? G : std::min<int64_t>(most, (int64_t)p.total_tokens * G);
     const dim3 grid((unsigned)(x.p.split ? 2 * p.grid : p.grid), (unsigned)((rows + 31) / 32));
-    return launch_behind(merge_kernel<G>, grid, dim3(kMergeWarps * 32), 0, true, stream, only_few ? y.p : x.p, y.p);
+    return launch_behind(merge_kernel<G>, grid, dim3(kMergeWarps * 32), 0, stream, only_few ? y.p : x.p, y.p);
 }
 
 // KV heads whose CTAs read the same pages at the same time: of the divisors of Hkv up to 8 (a token's K of 8 heads are 2 KB

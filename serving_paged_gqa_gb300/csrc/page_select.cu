@@ -55,6 +55,7 @@ __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_ca
 template <int G>
 __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectParams p) {
     constexpr int kNT = (G + 7) / 8;
+    grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const int b = blockIdx.y, first = blockIdx.x * p.tiles;
@@ -198,11 +199,18 @@ __device__ __forceinline__ Exact exact_score(const SelectParams& p, int b, int h
         int64_t x = 0, y = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            auto at = [&](const uint2& u) { return __half2float(__ushort_as_half((unsigned short)((i < 2 ? u.x : u.y) >> (16 * (i & 1))))); };
-            const float z = at(now), m = fmaxf(z * at(lo), z * at(hi));  // exact in fp32
-            const int64_t c = __float2ll_rd(m * 0x1p16f);
-            x += c;
-            y += __float2ll_rz((m - (float)c * 0x1p-16f) * 0x1p48f);  // all of it exact: 24 bits
+            auto at = [&](const uint2& u) { return (i < 2 ? u.x : u.y) >> (16 * (i & 1)) & 0xffffu; };
+            // |value| = mantissa (11 bits) * 2^(exponent - 25), exponent 1 .. 30. The greater product is with the greatest key where the
+            // query is positive, with the least one where it is negative.
+            auto mantissa = [](uint32_t u) { return (int)((u & 0x3ffu) | ((u & 0x7c00u) ? 0x400u : 0u)); };
+            auto exponent = [](uint32_t u) { return max((int)(u >> 10 & 31u), 1); };
+            const uint32_t a = at(now), c = a & 0x8000u ? at(lo) : at(hi);
+            const int64_t product = (a ^ c) & 0x8000u ? -(mantissa(a) * mantissa(c)) : mantissa(a) * mantissa(c);
+            const int shift = exponent(a) + exponent(c) - 2;  // in units of 2^-48
+            if (shift >= 32)
+                x += product << (shift - 32);
+            else
+                y += product << shift;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -249,6 +257,8 @@ struct SelectSmem {
 
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
     __shared__ SelectSmem sm;
+    // Behind a kernel of scores lengths and queries may be read at once: it began when every CTA of that one had waited itself.
+    if (p.max_pages <= p.select) grid_dependency_wait();
     const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t pair = (int64_t)b * p.Hkv + h;
     bool bad;
@@ -454,12 +464,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 
 template <int G>
 int launch_scores(const SelectParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
     const int tiles = (p.max_pages + kTile - 1) / kTile;
-    cfg.gridDim = dim3((unsigned)((tiles + p.tiles - 1) / p.tiles), (unsigned)p.B);
-    cfg.blockDim = dim3(kScoreWarps * 32);
-    cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, score_kernel<G>, p);
+    return launch_behind(score_kernel<G>, dim3((unsigned)((tiles + p.tiles - 1) / p.tiles), (unsigned)p.B), dim3(kScoreWarps * 32), 0,
+                         stream, p);
 }
 
 }  // namespace
@@ -494,16 +501,7 @@ int launch_select_pages(const SelectParams& in, int num_sms, void* stream) {
         }
     }
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.Hkv, (unsigned)p.B);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.max_pages > p.select ? 1 : 0;  // it may overlap the scores alone
-    return cudaLaunchKernelEx(&cfg, select_kernel, p);
+    return launch_behind(select_kernel, dim3((unsigned)p.Hkv, (unsigned)p.B), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace pkv

@@ -15,11 +15,10 @@ cudaError_t launch_kernel(void (*kernel)(Args...), int grid, int block, int smem
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The same on a grid of two dimensions; behind: its prologue may overlap the end of the kernel before it on the stream
-// (programmatic dependent launch), which it waits for itself.
+// The same on a grid of two dimensions, for a kernel whose beginning may overlap the end of the one before it on the stream
+// (programmatic dependent launch): it executes griddepcontrol.wait before it reads or writes what another may write or read.
 template <typename... Args>
-cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, dim3 block, int smem, bool behind, cudaStream_t stream,
-                          const Args&... args) {
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, dim3 block, int smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -29,7 +28,7 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, dim3 block, int sm
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = behind ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const PagesParams p) {
 // Bounds of pages: a warp per (page, 32 pieces of 16 bytes of a token's K), a lane per piece, all 16 tokens in flight. Bound:
 // HBM (the pages' K is read once, 512 bytes a (page, KV head) written).
 __global__ void __launch_bounds__(kThreads) bounds_kernel(const PagesParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int per = p.Hkv * 16, parts = (per + 31) / 32;
     for_items(
@@ -443,7 +445,7 @@ int launch_prompt_append(const PagesParams& p, int num_sms, void* stream) {
 int launch_page_bounds(const PagesParams& p, int num_sms, void* stream) {
     // (the number of new tokens is not known here, so more CTAs than are resident would start to find nothing)
     const int64_t items = page_items(p) / p.Hkv * ((p.Hkv + 1) / 2);
-    return launch_kernel(bounds_kernel, std::min(grid_for(num_sms, items), 2 * num_sms), kThreads, 0,
+    return launch_behind(bounds_kernel, dim3(std::min(grid_for(num_sms, items), 2 * num_sms)), dim3(kThreads), 0,
                          static_cast<cudaStream_t>(stream), p);
 }
 

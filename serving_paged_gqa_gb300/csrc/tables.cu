@@ -88,6 +88,8 @@ __device__ __forceinline__ bool last_cta(pkv_ws_header* hdr) {
 }
 
 __global__ void __launch_bounds__(kThreads) grow_kernel(const TablesParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     extern __shared__ int32_t s_rows[];  // of every row: first packed token, first of the new pages, tokens held
     __shared__ Two s_warp[kWarps];
     int32_t* s_tok = s_rows;
@@ -109,9 +111,16 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const TablesParams p) {
     };
     auto need = [](int len, int n) { return n == 0 ? 0 : pages_of((int64_t)len + n) - pages_of(len); };
     Two mine{0, 0}, total;
+    int len0 = 0, n0 = 0;  // the thread's first row (up to 512 rows its only one) is read once
+    if (b0 < b1) len0 = row(b0, n0);
+    auto again = [&](int b, int& n) {
+        if (b > b0) return row(b, n);
+        n = n0;
+        return len0;
+    };
     for (int b = b0; b < b1; ++b) {
         int n;
-        const int len = row(b, n);
+        const int len = again(b, n);
         mine.a += n;
         mine.b += need(len, n);
     }
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const TablesParams p) {
         Two upto = before, x{0, 0}, sum;
         for (int b = b0; b < b1; ++b) {
             int n;
-            const int len = row(b, n);
+            const int len = again(b, n);
             if (served(len, n, upto)) {
                 x.a += n;
                 x.b += need(len, n);
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const TablesParams p) {
         Two upto = before;
         for (int b = b0; b < b1; ++b) {
             int n;
-            const int len = row(b, n);
+            const int len = again(b, n);
             s_tok[b] = (int32_t)at.a;
             s_page[b] = (int32_t)min(at.b, (int64_t)INT32_MAX);
             s_len[b] = len;
@@ -190,6 +199,8 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const TablesParams p) {
 }
 
 __global__ void __launch_bounds__(kThreads) release_kernel(const TablesParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     extern __shared__ int32_t s_rows[];  // of every row: first of the released pages; its length afterwards
     __shared__ Two s_warp[kWarps];
     int32_t* s_page = s_rows;
@@ -256,12 +267,12 @@ int launch_tables_grow(const TablesParams& p, int num_sms, void* stream) {
         if (dev < 32) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
     const int64_t items = std::max<int64_t>(p.slots || p.positions ? p.capacity : 0, (int64_t)p.B * 32);
-    return launch_kernel(grow_kernel, grid_for(items, num_sms), kThreads, 3 * p.B * 4, static_cast<cudaStream_t>(stream), p);
+    return launch_behind(grow_kernel, dim3(grid_for(items, num_sms)), dim3(kThreads), 3 * p.B * 4, static_cast<cudaStream_t>(stream), p);
 }
 
 int launch_tables_release(const TablesParams& p, int num_sms, void* stream) {
     const int64_t items = std::min<int64_t>((int64_t)p.B * p.max_pages, p.num_pages);
-    return launch_kernel(release_kernel, grid_for(items, num_sms), kThreads, 2 * p.B * 4, static_cast<cudaStream_t>(stream), p);
+    return launch_behind(release_kernel, dim3(grid_for(items, num_sms)), dim3(kThreads), 2 * p.B * 4, static_cast<cudaStream_t>(stream), p);
 }
 
 }  // namespace pkv
