@@ -36,6 +36,7 @@ namespace {
 constexpr uint64_t kFinishNs = 32 * 1000;    // a warp's 32 rows, by the key that they are computed from again, at most
 constexpr uint64_t kFinishMostNs = 30000000000ull;  // (a million keys)
 constexpr int kRows = 128;                   // rows of a tile, keys of a step
+constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr int kStepPages = kRows / kPageSize;
 constexpr int kTileBytes = kRows * kRowBytes;  // 32 KB: two halves of 64 dims
 constexpr int kBoxBytes = kTileBytes / 2;
@@ -49,7 +50,7 @@ constexpr float kLift = 5.f;                 // the largest weight where the ref
 // What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps. A
 // sequence of one tile waits for memory meanwhile, which its copies ahead keep busy.
 template <bool kFew>
-constexpr int kPairCost = kFew ? 1 : 2;
+constexpr int kPairCost = kFew ? 3 : 2;
 constexpr int kMinCost = 2;                  // of a piece, at least
 constexpr int kWhole = 5;                    // cost of a pair that is not cut where a piece has no more
 
@@ -102,8 +103,9 @@ struct Layout {
     static constexpr int late = parts + 2 * 2 * 2 * kRows * 8;   // int [tile][warp of the half]: the second half raises
     static constexpr int scan = late + 8 * 4;                    // int64 [warp]: cost of the sequences of a warp's threads
     static constexpr int begin = scan + kThreads / 32 * 8;       // int64, int32: where the piece begins
-    static constexpr int low = begin + 16;                       // few: float [half][64][33]: second parts' accumulators
-    static constexpr int misc = low + (kFew ? 2 * 64 * 33 * 4 : 0);  // abort flag, TMEM address
+    static constexpr int low = begin + 16;                       // few: uint32 [tile][half][64][17]: second parts' accumulators
+    static constexpr int told = low + (kFew ? 4 * 64 * 17 * 4 : 0);  // few: uint32 [half][warp]: rows to be finished
+    static constexpr int misc = told + 8 * 4;                    // abort flag, TMEM address
     static constexpr int bytes = misc + 16 + 1024;               // slack to align the base to 1024 bytes
     static_assert(sizeof(Work) % 4 == 0 && bars % 8 == 0 && parts % 8 == 0 && scan % 8 == 0, "alignment");
     static_assert(kStages <= kMostStages && bytes <= 227 * 1024, "shared memory");
@@ -338,11 +340,141 @@ __device__ __noinline__ void finish_rows(const ChunkParams& p, const Seq& sq, in
 }
 
 // ---- softmax and output rows -----------------------------------------------------------------------------------------
-// What a warp of the softmax has counted: the tile's steps; tiles taken; those of B; steps with keys in the second half, as the
-// first half counts them.
+// What a warp of the softmax has counted: its tile's steps; works with a tile A, with a tile B; steps with keys in the second
+// half, as the first half counts them.
 struct Counts {
-    int ns, no, nb, step2;
+    int ns, na, nb, step2;
 };
+
+__device__ __forceinline__ float scaled(float y, float f) { return y == INFINITY && f == 0.f ? 0.f : y * f; }  // NaN only where a score is
+
+// A row's reference and sum from those of both halves of its keys, relative to the last reference (they only rise).
+__device__ __forceinline__ float2 sum_of(const float2* at, bool second_half) {
+    const float2 lo = at[0], hi = at[kRows];
+    if (!second_half) return lo;
+    const float top = fmaxf(lo.x, hi.x);
+    return make_float2(top, scaled(lo.y, lo.x == top ? 1.f : fast_exp2(lo.x - top)) +
+                                scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
+}
+
+// The rows of a tile that is alone, by the warps of both tiles: dims 64 h + 32 x .. + 31. keys: the piece's; own: this thread's row
+// is one to be stored; low: it holds second parts. (By A's warps alone, dims 64 h .. + 63 each, this took 3.3 us, during which
+// the next tile's scores wait.)
+template <int G>
+__device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w,
+                                             const WaitCtx& ctx, Counts& cnt, int keys, bool both, bool dup, bool idle) {
+    using L = Layout<true>;
+    Bars& bars = *reinterpret_cast<Bars*>(smem + L::bars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 3, h = (warp >> 2) & 1;
+    const int lane_row = threadIdx.x & 127, row = dup ? lane_row & 63 : lane_row;
+    const bool low = dup && lane_row >= 64, mine = !low && row / G < w.q.n;
+    if (!warp_wait(&bars.o_full[0], cnt.na & 1, ctx) || (both && !warp_wait(&bars.o_full[1], cnt.nb & 1, ctx))) return false;
+    auto have_read = [&]() {  // the next tile's products may overwrite them
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bars.o_free[0]);
+            if (both) mbar_arrive(&bars.o_free[1]);
+        }
+    };
+    const int na = cnt.na++, nb = cnt.nb;
+    cnt.nb += both;
+    if (idle) {
+        have_read();
+        return true;
+    }
+    tc_fence_after();
+    const float2* parts = reinterpret_cast<const float2*>(smem + L::parts) + lane_row;
+    float2 y = sum_of(parts + (na & 1) * 4 * kRows, keys > 64);
+    float fa = 1.f, fb = 0.f;  // factors of the accumulators; of one without a key that the row attends to, nothing is taken
+    bool some_a = true, some_b = false;
+    if (both) {
+        const float2 yb = sum_of(parts + (nb & 1) * 4 * kRows + 2 * kRows, keys - kRows > 64);
+        some_a = y.y != 0.f;
+        some_b = yb.y != 0.f;
+        const float top = some_b && (!some_a || yb.x > y.x) ? yb.x : y.x;
+        fa = y.x == top ? 1.f : fast_exp2(y.x - top);
+        fb = yb.x == top ? 1.f : fast_exp2(yb.x - top);
+        y = make_float2(top, (some_a ? scaled(y.y, fa) : 0.f) + (some_b ? scaled(yb.y, fb) : 0.f));
+    }
+    uint32_t o[32];
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + h * 64 + x * 32;
+    tmem_ld32(at, o);
+    if (both) {
+        uint32_t ob[32];
+        tmem_ld32(at + 128, ob);
+        tmem_wait_ld();
+        tmem_use32(o);
+        tmem_use32(ob);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint((some_a ? __uint_as_float(o[i]) * fa : 0.f) + (some_b ? __uint_as_float(ob[i]) * fb : 0.f));
+    } else {
+        tmem_wait_ld();
+        tmem_use32(o);
+    }
+    have_read();
+    if (dup) {
+        // Rows 64-127 hand over what they have, 2^-11 of the rows' values and less, in bfloat16 (17 words a row: lanes are in
+        // different banks).
+        uint32_t* to = reinterpret_cast<uint32_t*>(smem + L::low) + ((x * 2 + h) * 64 + row) * 17;
+        const int id = 1 + x * 4 + h * 2 + (warp & 1);
+        if (low) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) to[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+        }
+        named_barrier_sync(id, 64);
+        if (!low) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t u = to[i];
+                o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + __uint_as_float(u << 16));
+                o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) + __uint_as_float(u & 0xffff0000u));
+            }
+        }
+        if (low) return true;
+    }
+    const int state = w.state;
+    if (state >= 0) {  // columns in fours, rows side by side
+        float4* acc = reinterpret_cast<float4*>(p.acc) + ((int64_t)state * 32 + h * 16 + x * 8) * kRows + row;
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[i * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                             __uint_as_float(o[4 * i + 3]));
+            if (h == 0 && x == 0) p.ml[(int64_t)state * kRows + row] = y;
+        }
+        return true;
+    }
+    const float inv = 1.f / y.y;
+    __half2 probe = __float2half2_rn(0.f);  // stays 0 while every value is finite
+    const __half2 zero = probe;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + (int64_t)(w.q.first + row / G) * p.out_stride +
+                                          (w.h * G + row % G) * kHeadDim + h * 64 + x * 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            u[e] = pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            probe = __hfma2(*reinterpret_cast<const __half2*>(&u[e]), zero, probe);
+        }
+        if (mine) dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    // As in softmax_tile; B's warps tell A's, which finish the 64 dims of both.
+    const bool low_sum = !(y.y >= 0.25f);
+    const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
+    unsigned again = __ballot_sync(kAllLanes, mine && odd && !isnan(y.y));
+    const unsigned redo = __ballot_sync(kAllLanes, low_sum);
+    uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + h * 4 + (warp & 3);
+    if (x == 1 && lane == 0) *told = again;
+    named_barrier_sync(dup ? 9 + h * 2 + warp % 2 : 1 + h * 4 + (warp & 3), 64);
+    if (x == 1) return true;
+    again |= *told;
+    if (again)
+        finish_rows<G>(p, Seq{w.q.first, w.q.n, w.q.start}, w.s, (row & ~31) / G, w.h, h, again, redo & again);
+    return true;
+}
 
 // The tile of one work. Few: the tile is alone, and its rows are worked on by both tiles' warps, which take its even and odd steps
 // and the accumulators of A and B (few rows wait for K and V, and for one step's scores, weights and products after the
@@ -378,27 +510,16 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
     const int all = min(w.j1 - w.j0, ceil_div(max(end + skip, 0), kRows));
     const int steps = kFew ? (all + 1 - x) >> 1 : all;
     auto first_token = [&]() { return w.q.start - w.j0 * kRows + w.t0 + (kFew ? 0 : x * kTokens) - skip; };
-    if (steps == 0) {  // tile A may end before the piece begins
-        if (!kFew && w.state >= 0 && h == 0 && first_token() + row / G < end)
+    const int no = kFew && x == 1 ? cnt.nb : cnt.na;  // of this tile
+    const bool idle = first_token() + (row & ~31) / G >= end;  // none of the warp's rows is one
+    if (!kFew && steps == 0) {  // tile A may end before the piece begins, and B is not always there
+        if (w.state >= 0 && h == 0 && first_token() + row / G < end)
             p.ml[((int64_t)w.state * kTiles + x) * kRows + row] = make_float2(-INFINITY, 0.f);
-        cnt.nb += kFew && both;
         return true;
     }
-    // The accumulators are complete; then they have been read: A's warps read B's, too, where A is kFew.
-    auto complete = [&]() {
-        return warp_wait(&bars.o_full[x], cnt.no & 1, ctx) && (!kFew || x == 1 || !both || warp_wait(&bars.o_full[1], cnt.nb & 1, ctx));
-    };
-    auto have_read = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&bars.o_free[x]);
-            if (kFew && both) mbar_arrive(&bars.o_free[1]);
-        }
-    };
-    if (first_token() + (row & ~31) / G >= end) {
-        // None of the warp's rows is one, and nothing reads their weights or accumulators: it keeps the count of arrivals.
-        // (In the loop below this test costs every step of full tiles 80 cycles.)
+    if (idle) {
+        // Nothing reads the weights and accumulators of the warp's rows: it keeps the count of arrivals. (In the loop below this test
+        // costs every step of full tiles 80 cycles.)
         for (int j = 0; j < steps; ++j) {
             const int step = cnt.ns++, last = end - j * kNext - h * 64;
             if (last <= 0) continue;
@@ -411,18 +532,20 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             }
             __syncwarp();
         }
-        if (!complete()) return false;
-        if (!kFew || x == 0) have_read();
-        ++cnt.no;
-        cnt.nb += kFew && both;
-        return true;
+        if constexpr (!kFew) {
+            if (!warp_wait(&bars.o_full[x], no & 1, ctx)) return false;
+            if (lane == 0) mbar_arrive(&bars.o_free[x]);
+            __syncwarp();
+            ++cnt.na;
+            return true;
+        }
     }
     // Keys from `masked` on are in steps with keys behind the tile's first token; the others are whole. (It may begin before the
     // piece.)
     const int masked = max(first_token(), 0) / kRows * kRows;
     const int seen = min(first_token() + row / G, end - 1) - h * 64;  // the row's last key, from the half's first on
     float ref = -INFINITY, l = 0.f;
-    for (int j = 0; j < steps; ++j) {
+    for (int j = 0; j < steps && !(kFew && idle); ++j) {
         const int step = cnt.ns++;
         const int last = end - j * kNext - h * 64;  // keys of this half, counted from its first
         // The tile's last step ends in the first half: the second does not wait for its scores (nothing would keep
@@ -543,11 +666,11 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             __syncwarp();
             if (lane == 0) mbar_arrive(settled);
         } else {
-            if (!warp_wait(settled, cnt.no & 1, ctx)) return false;
+            if (!warp_wait(settled, no & 1, ctx)) return false;
             ref = *ref_at;
         }
         float sum = weights();
-        // (A row without a finite score has cnt.no reference yet, and asks for one. One whose scores are NaN, such as those
+        // (A row without a finite score has no reference yet, and asks for one. One whose scores are NaN, such as those
         // of garbage behind the sequence's end, has none to ask for, and would do so in every step.)
         const bool ask = ref == -INFINITY ? !isnan(sum) : sum > kMost;
         const bool raise = (j > 0 || h == 1) && __any_sync(0xffffffffu, ask);
@@ -602,7 +725,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         }
         if (last > 64) ++cnt.step2;
         l += sum;
-        parts[(cnt.no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
+        parts[(no & 1) * 4 * kRows + h * kRows] = make_float2(ref, l);
         tmem_st32(s_at, ph);
         tmem_wait_st();
         tc_fence_before();
@@ -612,65 +735,22 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             mbar_arrive(&bars.p_full[x][h]);
         }
     }
-    if (!complete()) return false;
-    if (kFew && x == 1) {  // A's warps read the accumulator
-        ++cnt.no;
-        return true;
-    }
+    if constexpr (kFew) return few_rows_out<G>(p, smem, tmem, w, ctx, cnt, end + skip, both, dup, idle);
+    if (!warp_wait(&bars.o_full[x], no & 1, ctx)) return false;
     tc_fence_after();
-    // The row's reference and sum: both halves', relative to the last reference (they only rise); those of both accumulators,
-    // of which one without a key that the row attends to counts for nothing.
-    auto scaled = [](float y, float f) { return y == INFINITY && f == 0.f ? 0.f : y * f; };  // NaN only where a score is
-    auto sum_of = [&](const float2* at, bool second_half) {
-        const float2 lo = at[0], hi = at[kRows];
-        if (!second_half) return lo;
-        const float top = fmaxf(lo.x, hi.x);
-        return make_float2(top, scaled(lo.y, lo.x == top ? 1.f : fast_exp2(lo.x - top)) +
-                                    scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
-    };
-    float2 y = sum_of(parts + (cnt.no & 1) * 4 * kRows, end > 64);
-    float fa = 1.f, fb = 0.f;  // factors of the accumulators
-    if (kFew && both) {
-        const float2 yb = sum_of(parts + (cnt.nb & 1) * 4 * kRows + 2 * kRows, end - kRows > 64);
-        const bool some_a = y.y != 0.f, some_b = yb.y != 0.f;
-        const float top = some_b && (!some_a || yb.x > y.x) ? yb.x : y.x;
-        fa = !some_a ? 0.f : y.x == top ? 1.f : fast_exp2(y.x - top);
-        fb = !some_b ? 0.f : yb.x == top ? 1.f : fast_exp2(yb.x - top);
-        y = make_float2(top, (some_a ? scaled(y.y, fa) : 0.f) + (some_b ? scaled(yb.y, fb) : 0.f));
-        if (!some_a) fa = -1.f;
-        if (!some_b) fb = -1.f;
-    }
+    const float2 y = sum_of(parts + (no & 1) * 4 * kRows, end > 64);
     const float total = y.y;
     auto fetch_o = [&](int c, uint32_t* o) {  // 32 of this half's dims
         tmem_ld32(o_at + h * 64 + c * 32, o);
         tmem_wait_ld();
         tmem_use32(o);
-        if (kFew && both) {
-            uint32_t ob[32];
-            tmem_ld32(o_at + 128 + h * 64 + c * 32, ob);
-            tmem_wait_ld();
-            tmem_use32(ob);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                o[i] = __float_as_uint((fa < 0.f ? 0.f : __uint_as_float(o[i]) * fa) +
-                                       (fb < 0.f ? 0.f : __uint_as_float(ob[i]) * fb));
-        }
-        if (c == 1) have_read();  // the next tiles' products may overwrite them
-        if (kFew && dup) {  // rows 64-127 hand over what they have; a row of 33 floats, so that lanes are in different banks
-            float* at = reinterpret_cast<float*>(smem + L::low) + (h * 64 + row) * 33;
-            if (low) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) at[i] = __uint_as_float(o[i]);
-            }
-            named_barrier_sync(1 + h * 2 + (warp & 1), 64);
-            if (!low) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + at[i]);
-            }
-            if (c == 0) named_barrier_sync(1 + h * 2 + (warp & 1), 64);  // before they hand over the next
+        if (c == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.o_free[x]);  // the next tile's products may overwrite it
         }
     };
-    const bool mine = !low && first_token() + row / G < end;
+    const bool mine = first_token() + row / G < end;
     const int state = w.state;
     if (state >= 0) {  // columns in fours, rows side by side
         float4* acc = reinterpret_cast<float4*>(p.acc) + (((int64_t)state * kTiles + x) * 32 + h * 16) * kRows + row;
@@ -686,8 +766,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
             }
         }
         if (h == 0 && mine) p.ml[((int64_t)state * kTiles + x) * kRows + row] = y;
-        ++cnt.no;
-        cnt.nb += kFew && both;
+        ++cnt.na;
         return true;
     }
     const float inv = 1.f / total;
@@ -701,7 +780,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (row & ~3) + i, t = w.t0 + x * kTokens + r / G;
-        in[i] = !low && first_token() + r / G < end;
+        in[i] = first_token() + r / G < end;
         dst[i] = static_cast<__half*>(p.out) + (int64_t)(w.q.first + t) * p.out_stride + (w.h * G + r % G) * kHeadDim +
                  h * 64 + q4 * 8;
     }
@@ -730,8 +809,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         for (int i = 0; i < 4; ++i)
             if (in[i]) *reinterpret_cast<uint4*>(dst[i] + c * 32) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
     }
-    ++cnt.no;
-    cnt.nb += kFew && both;
+    ++cnt.na;
     // The largest weight is 2^kLift, or half of that where the reference was raised, and next to scores that are it
     // themselves 1, or above 1/2.
     const bool low_sum = !(total >= 0.25f);
@@ -780,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(&bars.p_full[i][1], 4);
             mbar_init(&bars.o_full[i], 1);
             mbar_init(&bars.lo_done[i], 1);
-            mbar_init(&bars.o_free[i], 8);
+            mbar_init(&bars.o_free[i], kFew ? 16 : 8);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&bars.first_ref[0][i], 1);
@@ -791,10 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *abort_flag = 0;
         mbar_fence_init();
     }
-    // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (The second of two
-    // kernels waits at its end: it begins when all CTAs of the first have got here.)
-    if (kFew || !p.split) grid_dependency_wait();
-    grid_launch_dependents();
+    // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (Not so the second of
+    // two kernels: begun in the gaps of the first, 30 sequences of 64 tokens behind 1000 took 74 us, 66 one behind the other.)
+    grid_dependency_wait();
+    if (!(kFew && p.split)) grid_launch_dependents();
     // The line: up to 32 sequences are scanned by the warp that walks the piece, a lane each. Of more, every thread sums a run
     // (the first one's bounds are on their way while the barriers are set up), the CTA scans the sums, and the thread whose
     // run holds the piece's first unit finds its sequence.
@@ -804,7 +882,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const Seq q = lane < p.num_seqs ? own_seq<G, kFew>(p, lane, b) : Seq{0, 0, 0};
         if (!__any_sync(0xffffffffu, q.n > 0)) {
             if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
-            if (!kFew) grid_dependency_wait();
             return;
         }
     }
@@ -814,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     bool bad = false;
     Seq sq0{0, 0, 0};
     if (s0 < s1) sq0 = own_seq<G, kFew>(p, s0, bad);
-    if (warp == 16) tmem_alloc(tmem_at, 512);
+    if (few && warp == 16) tmem_alloc(tmem_at, 512);
     int64_t mine = s0 < s1 ? cost_of<G, kFew>(sq0) : 0;
     for (int s = s0 + 1; s < s1; ++s) {
         bool b;
@@ -834,7 +911,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at;
     int64_t before = incl - mine, total = 0;
     for (int i = few ? 18 : 0; i < (few ? 19 : kThreads / 32); ++i) {
         if (i < warp) before += scan[i];
@@ -843,6 +919,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int pieces = (int)min((int64_t)(gridDim.x / p.lanes), (total + kMinCost - 1) / kMinCost);
     const int64_t lo = group < pieces ? group * total / pieces : 0, hi = group < pieces ? (group + 1) * total / pieces : 0;
     if (!few) {
+        if (total == 0 && p.split) {  // nothing for this kernel
+            if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
+            return;
+        }
+        if (warp == 16) tmem_alloc(tmem_at, 512);
         if (lo < hi && before <= lo && lo < before + mine) {
             int64_t at = before;
             for (int s = s0; s < s1; ++s) {
@@ -856,8 +937,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 at += n;
             }
         }
+        tc_fence_before();
         __syncthreads();
+        tc_fence_after();
     }
+    const uint32_t tmem = *tmem_at;
     if (p.seq_lens) {  // rows without a token get 0
         for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
             bool b;
@@ -1206,7 +1290,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (!softmax_tile<G, kFew>(p, smem, tmem, w, ctx, counts)) break;
         }
     }
-    if (!kFew && p.split) grid_dependency_wait();  // the first kernel, whose states are added up by the one behind this
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
@@ -1261,15 +1344,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const ChunkPara
         float4 a[kBatch][4];
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
-            const int i = min(i0 + e * span, m.pieces - 1);
-            x[e] = __ldcg(ml + slot(i) * tiles * kRows);
+            const int i = i0 + e * span;
+            x[e] = make_float2(0.f, 0.f);
+            if (i < m.pieces) {
+                x[e] = __ldcg(ml + slot(i) * tiles * kRows);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) a[e][c] = __ldcg(acc + slot(i) * tiles * 32 * kRows + c * kRows);
+                for (int c = 0; c < 4; ++c) a[e][c] = __ldcg(acc + slot(i) * tiles * 32 * kRows + c * kRows);
+            }
         }
         float to = top;
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
-            if (i0 + e * span >= m.pieces) x[e].y = 0.f;
             nan |= isnan(x[e].y);
             if (x[e].y > 0.f) to = fmaxf(to, x[e].x);
         }
@@ -1346,9 +1431,8 @@ int launch_one(const Params& prm, cudaStream_t stream) {
     return launch_behind(chunk_kernel<G, kFew>, dim3((unsigned)prm.p.grid), dim3(kThreads), smem, stream, prm);
 }
 
-// Sequences of one tile of new tokens go to one kernel, those of more to the other, which is launched behind it and begins where
-// its CTAs end; both where the host cannot tell (the lengths are on the device). In this order, since a kernel that has no
-// sequences ends at once, behind the other in its CTAs' shadow, before it not (16 sequences of 2-8 tokens 212 -> @@ us).
+// Sequences of one tile of new tokens go to one kernel, those of more to another behind it; both where the host cannot tell (the
+// lengths are on the device). A kernel that has no sequences ends at once: 5 us.
 template <int G>
 int launch(const Params& prm, const Params& prm_few, cudaStream_t stream) {
     const ChunkParams& p = prm.p;
