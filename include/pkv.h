@@ -579,6 +579,7 @@ int pkv_tables_release(const pkv_problem* problem, const int32_t* released, cons
  * dim by dim, earlier tokens of the page included; a NaN among them is both. Other pages keep theirs. problem and prompt as
  * for pkv_prompt_append (k_stride and v_stride do not matter). Rows and pages that are not in order are skipped with the same
  * status bits. ws: PKV_PROMPT_WS_BYTES. bounds must not overlap the pool (the same address is refused).
+ * PKV_E_UNSUPPORTED where max_pages_per_seq * num_kv_heads / 2 exceeds 2^32.
  */
 int pkv_page_bounds(const pkv_problem* problem, const pkv_prompt* prompt, const int32_t* cu_seqlens, const int32_t* start,
                     const void* k_pool, const int32_t* block_table, void* bounds, int32_t num_sms, void* ws, size_t ws_bytes,
@@ -593,7 +594,8 @@ int pkv_sparse_workspace_bytes(const pkv_problem* problem, int32_t num_sms, size
  * pages [B][Hkv][select] int32 (logical pages of the row; -1 behind them). The score of a page is the greatest, over the G
  * query heads of h (q [B][Hq][d] fp16), of sum_d max(q_d lo_d, q_d hi_d) with the page's bounds (pkv_page_bounds): an upper
  * bound of q.k over its tokens. Scores are compared as exact sums (rounded to 64 bits where more than 256 pages are within
- * fp32's error of the last selected one); equal ones go to the lowest page, and a score whose bounds or whose queries (of any of the G heads) are not all finite counts as +inf. select >= 1.
+ * fp32's error of the last selected one); equal ones go to the lowest page, and a score whose bounds or whose queries (of any
+ * of the G heads) are not all finite counts as +inf. select >= 1.
  * A length that is negative or exceeds the table raises PKV_STATUS_BAD_LEN (no pages); a block-table entry outside the pool
  * raises PKV_STATUS_BAD_PAGE and counts as bounds of 0 (entries of rows with P <= select are not looked at). ws:
  * pkv_sparse_workspace_bytes.

@@ -185,6 +185,8 @@ extern "C" int pkv_page_bounds(const pkv_problem* pr, const pkv_prompt* pm, cons
     if (!aligned(k_pool, 16) || !aligned(bounds, 16) || !aligned(cu_seqlens, 4) || !aligned(start, 4) || !aligned(block_table, 4))
         return PKV_E_ALIGN;
     if (bounds == k_pool) return PKV_E_INVAL;
+    // the kernel counts a row's pages, 32 pieces of 16 bytes at a time, in 32 bits
+    if ((int64_t)pr->max_pages_per_seq * ((pm->num_kv_heads + 1) / 2) > UINT32_MAX) return PKV_E_UNSUPPORTED;
     PagesParams p{};
     p.k_pool = const_cast<void*>(k_pool);
     p.pool = bounds;

@@ -107,6 +107,7 @@ def bounds(pr=None, pm=None, cu=at(1), start=None, k=at(2), bt=at(3), bd=at(4), 
     (dict(k=ODD), ALIGN), (dict(bd=ODD), ALIGN), (dict(cu=ODD2), ALIGN), (dict(start=ODD2), ALIGN), (dict(bt=ODD2), ALIGN), (dict(ws=ODD), ALIGN),
     (dict(n=10), SMALL), (dict(sms=0), INVAL), (dict(pr=problem(batch=1)), INVAL), (dict(pr=problem(num_kv_heads=4, num_q_heads=32)), INVAL),
     (dict(bd=at(2)), INVAL), (dict(pm=prompt(total_tokens=0), k=None), OK),
+    (dict(pr=problem(num_q_heads=128, num_kv_heads=128, max_pages_per_seq=(1 << 27) - 1), pm=pkv.make_prompt(2, 50, 128, 128, 128)), UNSUPPORTED),
 ])
 def test_page_bounds_refuse_before_any_work(change, code):
     assert bounds(**change) == code
