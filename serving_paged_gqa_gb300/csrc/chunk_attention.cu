@@ -3,22 +3,39 @@
 //
 // For token i of a sequence (position start + i) and query head hq of KV head h: out = sum_j p_j v_j / sum_j p_j over the
 // positions j <= start + i, p_j = 2^(x_j - ref), x_j = scale * log2(e) * q_i.k_j. Products on the 5th-generation tensor
-// cores, tiles of 128 rows = 128 / G tokens x G heads, two tiles (A, B: a pair) a CTA at a time over 128 keys a step,
-// warp roles, references and precision as in prompt_attention.cu; what differs is where keys come from and who does what.
+// cores, tiles of 128 rows = 128 / G tokens x G heads, two tiles (A, B: a pair) a CTA at a time over 128 keys a step;
+// references and precision of the weights as in prompt_attention.cu. What differs is where keys come from and who does what.
 //
 // Keys: a step is 8 pages of 16 tokens. A page of one KV head is two TMA boxes (64 dims x 16 tokens) for K and two for V;
 // boxes of consecutive pages lie one behind the other in a stage, which gives the same operand layout as one box of 128
 // rows. Block-table entries are read 32 at a time ahead of their use. An entry outside the pool becomes a coordinate
-// outside the tensor: the copy brings zeros.
+// outside the tensor: the copy brings zeros. (A box of 128 rows would take 4 % less: 32 boxes a step keep the copy engine busy.)
 //
 // Division: a pair of tiles of one (sequence, KV head) has as many steps as its last token has keys. Neither one long
 // context with a few new tokens (one pair a KV head) nor a batch of unequal ones fills the GPU pair by pair, so the steps
 // of all pairs form one line, in the order (sequence, KV heads, pair, step), and it is cut into equal pieces wherever the
-// cuts fall. A piece belongs to `lanes` CTAs, one for each of `lanes` neighbouring KV heads, so that they read the same
-// pages at the same time (a token's heads are contiguous in a page). Every CTA finds its piece from a scan of the
-// sequences' lengths; there is no plan, and one captured graph serves every step. A pair that lies in one piece is
-// written out at once. The others leave a state a piece (ref, sum, accumulator, in fp32; a CTA leaves two at most), and a
-// second kernel, launched to overlap this one's end, adds them up in the order of the pieces.
+// cuts fall, but for what lies next to a pair's ends. A piece belongs to `lanes` CTAs, one for each of `lanes` neighbouring KV
+// heads, so that they read the same pages at the same time (a token's heads are contiguous in a page). Every CTA finds its piece
+// from a scan of the sequences' lengths; there is no plan, and one captured graph serves every step. A pair that lies in one
+// piece is written out at once. The others leave a state a piece (ref, sum, accumulator, in fp32; a CTA leaves two at most), and a
+// second kernel, launched to overlap this one's end, adds them up in the order of the pieces: results do not depend on timing.
+//
+// Two forms of the kernel: sequences of more than one tile of new tokens (pairs, bound by the tensor core), and sequences of one
+// tile (few rows, bound by HBM or latency: see softmax_tile). Warp roles of both:
+//   warps 0-15      softmax and output rows, thread = row; warps 0-3 and 4-7 the first and second 64 keys of tile A, 8-15 of B
+//   warp 16         one (elected) thread waits for and issues the matrix instructions
+//   warps 17, 19    copies of queries and K, and of V, whose rows behind the last key warp 19 clears
+//   warp 18         walks the piece and publishes its pairs, two ahead
+// Every wait is bounded (pkv_wait.cuh).
+//
+// Measured on GB300s (32 query heads, 8 KV heads): 4096 tokens behind 28672 1.44-1.51 ms, 1370-1430 TFLOP/s, 0.73-0.76 of the
+// measured cuBLAS burst under the power cap; 16384 without a prefix 1.40 ms (1570 TFLOP/s; prompt_attention.cu 1.30-1.39); 512
+// behind 8192 64 us, of which 28 steps take 46; 16 sequences of 2-8 tokens behind 1000-32000 201 us, 5.8 TB/s; 5 tokens behind 700
+// 14.5 us. Under ncu (512 behind 8192, cold) the tensor pipe is active 49 % of the time, warps wait for TMEM loads and for
+// instructions; a step of a pair takes 3060 cycles, of which the tensor core's share is 2048 (prompt_attention.cu 2820).
+// Tried and dropped: the next pair's first scores issued before the current pair's last products (nothing, and 3-6 % slower with
+// short pairs); a grid of merging blocks that share the items they count (2 us slower); both kinds of sequences in one
+// kernel (its registers spill: 8192 tokens 371 us, 420).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -47,8 +64,9 @@ constexpr int kThreads = kSoftmax + 128;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 640 * 96, what the launch has
 constexpr float kMost = 65504.f;             // sum of 64 weights above which the row's reference is raised
 constexpr float kLift = 5.f;                 // the largest weight where the reference was set, in powers of two
-// What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core runs dry), in steps. A
-// sequence of one tile waits for memory meanwhile, which its copies ahead keep busy.
+// What a pair takes beside its steps (its queries' way in, its rows' way out, during which the tensor core or the copies run dry), in
+// steps. (Many: 8192 tokens without a prefix 405 us with 0, 394 with 2. Few: 64 sequences of one token behind 1023 75 us with 2, 72
+// with 3.)
 template <bool kFew>
 constexpr int kPairCost = kFew ? 3 : 2;
 constexpr int kMinCost = 2;                  // of a piece, at least
@@ -86,6 +104,8 @@ struct Bars {
     uint64_t o_free[2];              // the accumulator has been read
     uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
     uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
+    uint64_t low_full[8], low_empty[8];  // few: [tile][half][warp of rows 0-63] second parts' accumulators are there, have been read
+    uint64_t told[8];                // few: [half][warp of the half] so are the rows that B's warp has found
     uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
     uint64_t drain;
 };
@@ -341,9 +361,9 @@ __device__ __noinline__ void finish_rows(const ChunkParams& p, const Seq& sq, in
 
 // ---- softmax and output rows -----------------------------------------------------------------------------------------
 // What a warp of the softmax has counted: its tile's steps; works with a tile A, with a tile B; steps with keys in the second
-// half, as the first half counts them.
+// half, as the first half counts them; few: tiles with second parts, and tiles that went to out.
 struct Counts {
-    int ns, na, nb, step2;
+    int ns, na, nb, step2, low, told;
 };
 
 __device__ __forceinline__ float scaled(float y, float f) { return y == INFINITY && f == 0.f ? 0.f : y * f; }  // NaN only where a score is
@@ -357,9 +377,19 @@ __device__ __forceinline__ float2 sum_of(const float2* at, bool second_half) {
                                 scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
 }
 
+// A wait for another warp of the softmax that is as far as this one: warp_wait's clock would take registers that the rows need.
+__device__ __forceinline__ bool short_wait(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
+    for (uint32_t it = 0; it < 1u << 20; ++it) {
+        if (__all_sync(kAllLanes, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(kAllLanes, *ctx.abort_flag != 0)) return false;
+    }
+    *ctx.abort_flag = 1;
+    raise_status(ctx.status, PKV_STATUS_TIMEOUT);
+    return false;
+}
+
 // The rows of a tile that is alone, by the warps of both tiles: dims 64 h + 32 x .. + 31. keys: the piece's; own: this thread's row
-// is one to be stored; low: it holds second parts. (By A's warps alone, dims 64 h .. + 63 each, this took 3.3 us, during which
-// the next tile's scores wait.)
+// is one to be stored; low: it holds second parts.
 template <int G>
 __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem, uint32_t tmem, const volatile Work& w,
                                              const WaitCtx& ctx, Counts& cnt, int keys, bool both, bool dup, bool idle) {
@@ -418,21 +448,26 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
         // Rows 64-127 hand over what they have, 2^-11 of the rows' values and less, in bfloat16 (17 words a row: lanes are in
         // different banks).
         uint32_t* to = reinterpret_cast<uint32_t*>(smem + L::low) + ((x * 2 + h) * 64 + row) * 17;
-        const int id = 1 + x * 4 + h * 2 + (warp & 1);
+        uint64_t* full = &bars.low_full[x * 4 + h * 2 + (warp & 1)];
+        uint64_t* empty = &bars.low_empty[x * 4 + h * 2 + (warp & 1)];
+        const int n = cnt.low++;
         if (low) {
+            if (!short_wait(empty, (n & 1) ^ 1, ctx)) return false;
 #pragma unroll
             for (int i = 0; i < 16; ++i) to[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            return true;
         }
-        named_barrier_sync(id, 64);
-        if (!low) {
+        if (!short_wait(full, n & 1, ctx)) return false;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t u = to[i];
-                o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + __uint_as_float(u << 16));
-                o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) + __uint_as_float(u & 0xffff0000u));
-            }
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t u = to[i];
+            o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + __uint_as_float(u << 16));
+            o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) + __uint_as_float(u & 0xffff0000u));
         }
-        if (low) return true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty);
     }
     const int state = w.state;
     if (state >= 0) {  // columns in fours, rows side by side
@@ -467,9 +502,16 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
     unsigned again = __ballot_sync(kAllLanes, mine && odd && !isnan(y.y));
     const unsigned redo = __ballot_sync(kAllLanes, low_sum);
     uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + h * 4 + (warp & 3);
-    if (x == 1 && lane == 0) *told = again;
-    named_barrier_sync(dup ? 9 + h * 2 + warp % 2 : 1 + h * 4 + (warp & 3), 64);
-    if (x == 1) return true;
+    uint64_t* told_full = &bars.told[h * 4 + (warp & 3)];
+    if (x == 1) {
+        if (lane == 0) {
+            *told = again;
+            mbar_arrive(told_full);
+        }
+        __syncwarp();
+        return true;
+    }
+    if (!short_wait(told_full, cnt.told++ & 1, ctx)) return false;
     again |= *told;
     if (again)
         finish_rows<G>(p, Seq{w.q.first, w.q.n, w.q.start}, w.s, (row & ~31) / G, w.h, h, again, redo & again);
@@ -518,8 +560,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         return true;
     }
     if (idle) {
-        // Nothing reads the weights and accumulators of the warp's rows: it keeps the count of arrivals. (In the loop below this test
-        // costs every step of full tiles 80 cycles.)
+        // Nothing reads the weights and accumulators of the warp's rows: it keeps the count of arrivals.
         for (int j = 0; j < steps; ++j) {
             const int step = cnt.ns++, last = end - j * kNext - h * 64;
             if (last <= 0) continue;
@@ -554,8 +595,7 @@ __device__ __forceinline__ bool softmax_tile(const ChunkParams& p, uint8_t* smem
         if (last <= 0) continue;
         if (!warp_wait(&bars.s_full[x], step & 1, ctx)) return false;
         tc_fence_after();
-        // Keys behind the row's token: -inf in TMEM, before anything reads the scores. (Masked as they are read, which unmasked steps
-        // skip, every step takes 7 % longer.)
+        // Keys behind the row's token: -inf in TMEM, before anything reads the scores, so that what reads them has no form with a mask.
         if (j * kNext >= masked) {
             const int lim = seen - j * kNext;
 #pragma unroll 1
@@ -869,6 +909,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *abort_flag = 0;
         mbar_fence_init();
     }
+    if (kFew && threadIdx.x >= 32 && threadIdx.x < 40) {
+        mbar_init(&bars.low_full[threadIdx.x - 32], 1);
+        mbar_init(&bars.low_empty[threadIdx.x - 32], 1);
+        mbar_init(&bars.told[threadIdx.x - 32], 1);
+    }
     // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (Not so the second of
     // two kernels: begun in the gaps of the first, 30 sequences of 64 tokens behind 1000 took 74 us, 66 one behind the other.)
     grid_dependency_wait();
@@ -878,9 +923,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // run holds the piece's first unit finds its sequence.
     const bool few = p.num_seqs <= 32;
     if (few && p.split) {  // nothing for this kernel: every warp sees it
-        bool b;
+        bool b = false;
         const Seq q = lane < p.num_seqs ? own_seq<G, kFew>(p, lane, b) : Seq{0, 0, 0};
         if (!__any_sync(0xffffffffu, q.n > 0)) {
+            if (b && warp == 0 && blockIdx.x == 0) raise_status(ctx.status, PKV_STATUS_BAD_LEN);
             if (threadIdx.x == 0) static_cast<Merge*>(p.merges)[blockIdx.x] = Merge{};
             return;
         }
@@ -942,6 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc_fence_after();
     }
     const uint32_t tmem = *tmem_at;
+    int oldest = -1;  // of an odd number of stages: ring position of a copy that may be in flight after a wait that ran out
     if (p.seq_lens) {  // rows without a token get 0
         for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
             bool b;
@@ -1136,6 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // every copy that this warp issued lands before the CTA may end
             if (nc > 0) warp_drain(&bars.tail_full, (nc - 1) & 1);
             for (int j = max(seq0, seq - kStages / 2 * 2); j < seq; j += 2) warp_drain(&bars.kv_full[j % kStages], (j / kStages) & 1);
+            if (kStages % 2 && seq - (kStages + 1) >= seq0) oldest = seq - (kStages + 1);
             for (int x = 0; x < 2; ++x)
                 if (nq[x] > 0) warp_drain(&bars.q_full[x], (nq[x] - 1) & 1);
         } else if (warp == 16) {
@@ -1279,7 +1327,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     } else {
         // ---------------------------------------------------------------------------- softmax and output rows
         regs_grow<kSoftmaxRegs>();
-        Counts counts{0, 0, 0, 0};
+        Counts counts{};
         for (int k = 0;; ++k) {
             // The slot is kept while it is worked on: what a step does not need is not kept in registers.
             __syncwarp();
@@ -1292,6 +1340,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    if (kStages % 2 && *abort_flag && oldest >= 0) warp_drain(&bars.kv_full[oldest % kStages], (oldest / kStages) & 1);
     if (warp == 16) {
         tc_fence_after();
         tmem_free(tmem, 512);

@@ -194,6 +194,15 @@ def test_sequences_out_of_order_are_skipped(ws):
         assert torch.equal(out[: skip.start], good[: skip.start]) and torch.equal(out[skip.stop:c.tokens], good[skip.stop:])
 
 
+@pytest.mark.parametrize("new", [[3], [300], [3, 4], [3, 300], [1] * 40])
+def test_no_sequence_in_order(ws, new):
+    c = Cache(new, [10] * len(new), 8, 2, seed=13)
+    out = torch.full((c.q.shape[0], 8, D), 7.0, dtype=torch.float16, device="cuda")
+    pkv.chunk_attention(c.q, c.k, c.v, c.cu, c.bt, start=torch.full_like(c.st, -1), out=out, ws=ws)
+    torch.cuda.synchronize()
+    assert pkv.pkv_read_status(ws) == pkv.PKV_STATUS_BAD_LEN and (out == 7.0).all()
+
+
 def test_rows_of_no_sequence(ws):
     c = Cache([5, 140], [10, 20], 8, 2, seed=12)
     q = torch.cat((torch.full((9, 8, D), math.nan, dtype=torch.float16, device="cuda"), c.q))
