@@ -4,7 +4,8 @@ One decode step of attention over a block-table FP16 KV cache with three schedul
 sequence split, compact device-built workqueue), a log-sum-exp merge, a device worklist builder and a host
 roofline cost-model planner, all in libpkv.so (C ABI: include/pkv.h). This package is its Python binding. Prompts:
 causal attention over packed sequences, their K/V into the FP16 pages or quantised into 4-bit pages, and the decode
-step over 4-bit pages.
+step over 4-bit pages. Growing caches: tables of a step from the rows' lengths, attention of chunks of new tokens over the
+pages, and a decode step over selected pages.
 """
 
 from ._lib import (EXPORTS, LIB_PATH, PKV_MAX_BATCH, PKV_MAX_ROWS_IN_DECODE, PKV_MAX_SMS,  # noqa: F401

@@ -30,8 +30,8 @@
 //
 // Measured on GB300s (32 query heads, 8 KV heads): 4096 tokens behind 28672 1.44-1.51 ms, 1370-1430 TFLOP/s, 0.73-0.76 of the
 // measured cuBLAS burst under the power cap; 16384 without a prefix 1.40 ms (1570 TFLOP/s; prompt_attention.cu 1.30-1.39); 512
-// behind 8192 64 us, of which 28 steps take 46; 16 sequences of 2-8 tokens behind 1000-32000 201 us, 5.8 TB/s; 5 tokens behind 700
-// 14.5 us. Under ncu (512 behind 8192, cold) the tensor pipe is active 49 % of the time, warps wait for TMEM loads and for
+// behind 8192 64 us, of which 28 steps take 46; 16 sequences of 2-8 tokens behind 1000-32000 204 us, 5.75 TB/s; 5 tokens behind 700
+// 14.6 us. Under ncu (512 behind 8192, cold) the tensor pipe is active 49 % of the time, warps wait for TMEM loads and for
 // instructions; a step of a pair takes 3060 cycles, of which the tensor core's share is 2048 (prompt_attention.cu 2820).
 // Tried and dropped: the next pair's first scores issued before the current pair's last products (nothing, and 3-6 % slower with
 // short pairs); a grid of merging blocks that share the items they count (2 us slower); both kinds of sequences in one
