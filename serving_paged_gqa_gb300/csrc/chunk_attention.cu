@@ -28,7 +28,7 @@
 //   warp 18         walks the piece and publishes its pairs, two ahead
 // Every wait is bounded (pkv_wait.cuh).
 //
-// Measured on GB300s (32 query heads, 8 KV heads): 4096 tokens behind 28672 1.44-1.51 ms, 1370-1430 TFLOP/s, 0.73-0.76 of the
+// Measured on GB300s (32 query heads, 8 KV heads): 4096 tokens behind 28672 1.38 ms, 1490 TFLOP/s, 0.79 of the
 // measured cuBLAS burst under the power cap; 16384 without a prefix 1.40 ms (1570 TFLOP/s; prompt_attention.cu 1.30-1.39); 512
 // behind 8192 64 us, of which 28 steps take 46; 16 sequences of 2-8 tokens behind 1000-32000 204 us, 5.75 TB/s; 5 tokens behind 700
 // 14.6 us. Under ncu (512 behind 8192, cold) the tensor pipe is active 49 % of the time, warps wait for TMEM loads and for
@@ -1054,6 +1054,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 int pair = left, u = (int)(rest - cost_before<G, kFew>(q, pair));
                 bool first = true;
+                // The last steps of the first pair: where about a whole pair follows they are kept for the end. CTAs that begin with
+                // whole pairs read a head's keys at the same time, once from HBM for all of them where a context does not fit L2 (4096
+                // tokens behind 28672: 1.46-1.48 ms in order, 1.38-1.39 so).
+                Work tail;
+                tail.h = -1;
                 for (int64_t at = lo - u; ok; first = false) {  // where the pair begins
                     Work w;
                     w.q = q;
@@ -1073,7 +1078,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             while (e > group && snap((int)((int64_t)e * total / pieces - at), len) == len) --e;
                             merge = Merge{q, s, w.t0, w.h, e - group + 1, 0};
                         }
-                        ok = publish(k++, w);
+                        if (!kFew && w.j0 > 0 && hi - (at + len) >= len)
+                            tail = w;
+                        else
+                            ok = publish(k++, w);
                     }
                     at += len;
                     u = 0;
@@ -1090,6 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         }
                     }
                 }
+                if (!kFew && ok && tail.h >= 0) ok = publish(k++, tail);
             }
             if (ok) {
                 Work w{};
