@@ -8,6 +8,7 @@ tensors. Argument marshalling only: the work runs in the library's CUDA kernels,
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -48,34 +49,87 @@ def pkv_chunk_attention(problem: Problem, prompt: Prompt, q, k_pool, v_pool, cu_
     _chunk(dev, problem, prompt, q, k_pool, v_pool, cu_seqlens, start, block_table, scale, ws, out, stream)
 
 
-def _ints(t, name: str, n: int, dtype=torch.int32) -> int | None:
-    """The address of a tensor of n integers (None: not given)."""
-    if t is not None and t.numel() != n:
+def _ptrs(dev: int, dtype, *wants) -> list:
+    """The addresses of tensors (tensor, entries, name) on the device; of None, None. (The calls on tables and bounds take less time
+    on the GPU than here, so a tensor is looked at once, and what was wrong with it is found out afterwards.)"""
+    at = []
+    for t, n, name in wants:
+        if t is None:
+            at.append(None)
+        elif t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+            at.append(t.data_ptr())
+        elif t.get_device() != dev:
+            raise ValueError(f"the tensors must be on one device: {name} is on {t.device}, others on cuda:{dev}")
+        elif t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+        else:
+            _addr(t, dtype, name)
+    return at
+
+
+def _ints(t, name: str, n: int) -> int:
+    """The address of a tensor of n integers."""
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return _addr(t, dtype, name)
+    return _addr(t, torch.int32, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _described(*args):
+    """A reference to the description of these sizes, for calls that only read it."""
+    return _byref(Problem(*args))
+
+
+@functools.lru_cache(maxsize=256)
+def _packed(num_seqs, tokens, hkv, d):
+    """The same for contiguous packed keys."""
+    return _byref(Prompt(num_seqs, tokens, hkv, hkv, d, 0, hkv * d, hkv * d, hkv * d, hkv * d))
+
+
+def _shape(block_table: torch.Tensor, batch: int | None = None, pages: int | None = None) -> tuple[int, int]:
+    if block_table.dim() != 2 or (batch is not None and tuple(block_table.shape) != (batch, pages)):
+        raise ValueError(f"block_table must have shape ({'B' if batch is None else batch}, {'max_pages' if pages is None else pages})")
+    return block_table.shape
+
+
+def _grow(dev, problem, b, num_pages, entries, new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots,
+          positions, seq_lens_out, free_count_out, ws, stream) -> None:
+    cap = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
+    n, lens, table, pages, count, cu, first, pos, lens_out, count_out = _ptrs(
+        dev, torch.int32, (new_tokens, b, "new_tokens"), (seq_lens, b, "seq_lens"), (block_table, entries, "block_table"),
+        (free_pages, num_pages, "free_pages"), (free_count, 1, "free_count"), (cu_seqlens, b + 1, "cu_seqlens"), (start, b, "start"),
+        (positions, cap, "positions"), (seq_lens_out, b, "seq_lens_out"), (free_count_out, 1, "free_count_out"))
+    to, = _ptrs(dev, torch.int64, (slots, cap, "slots"))
+    nbytes = ws.numel()
+    wsp, = _ptrs(dev, torch.uint8, (ws, nbytes, "ws"))
+    _call(dev, "pkv_tables_grow", problem, n, lens, table, pages, count, cu, first, to, pos, cap, lens_out, count_out, _num_sms(dev),
+          wsp, nbytes, _handle(stream, dev))
 
 
 def pkv_tables_grow(problem: Problem, new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots,
                     positions, seq_lens_out, free_count_out, ws, stream=None) -> None:
-    dev = _device(new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots, positions, seq_lens_out,
-                  free_count_out, ws)
-    b = problem.batch
-    cap = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
-    _call(dev, "pkv_tables_grow", _byref(problem), _ints(new_tokens, "new_tokens", b), _ints(seq_lens, "seq_lens", b),
-          _table(block_table, problem), _ints(free_pages, "free_pages", problem.num_pages), _ints(free_count, "free_count", 1),
-          _ints(cu_seqlens, "cu_seqlens", b + 1), _ints(start, "start", b), _ints(slots, "slots", cap, torch.int64),
-          _ints(positions, "positions", cap), cap, _ints(seq_lens_out, "seq_lens_out", b),
-          _ints(free_count_out, "free_count_out", 1), _num_sms(dev), _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    b, width = _shape(block_table, problem.batch, problem.max_pages_per_seq)
+    _grow(_device(new_tokens), _byref(problem), b, problem.num_pages, b * width, new_tokens, seq_lens, block_table, free_pages,
+          free_count, cu_seqlens, start, slots, positions, seq_lens_out, free_count_out, ws, stream)
+
+
+def _release(dev, problem, b, num_pages, entries, released, seq_lens, block_table, free_pages, free_count, seq_lens_out,
+             free_count_out, ws, stream) -> None:
+    ended, lens, table, pages, count, lens_out, count_out = _ptrs(
+        dev, torch.int32, (released, b, "released"), (seq_lens, b, "seq_lens"), (block_table, entries, "block_table"),
+        (free_pages, num_pages, "free_pages"), (free_count, 1, "free_count"), (seq_lens_out, b, "seq_lens_out"),
+        (free_count_out, 1, "free_count_out"))
+    nbytes = ws.numel()
+    wsp, = _ptrs(dev, torch.uint8, (ws, nbytes, "ws"))
+    _call(dev, "pkv_tables_release", problem, ended, lens, table, pages, count, lens_out, count_out, _num_sms(dev), wsp, nbytes,
+          _handle(stream, dev))
 
 
 def pkv_tables_release(problem: Problem, released, seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out,
                        ws, stream=None) -> None:
-    dev = _device(released, seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out, ws)
-    b = problem.batch
-    _call(dev, "pkv_tables_release", _byref(problem), _ints(released, "released", b), _ints(seq_lens, "seq_lens", b),
-          _table(block_table, problem), _ints(free_pages, "free_pages", problem.num_pages), _ints(free_count, "free_count", 1),
-          _ints(seq_lens_out, "seq_lens_out", b), _ints(free_count_out, "free_count_out", 1), _num_sms(dev),
-          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    b, width = _shape(block_table, problem.batch, problem.max_pages_per_seq)
+    _release(_device(released), _byref(problem), b, problem.num_pages, b * width, released, seq_lens, block_table, free_pages,
+             free_count, seq_lens_out, free_count_out, ws, stream)
 
 
 def _bounds(t: torch.Tensor, problem: Problem) -> int:
@@ -85,13 +139,22 @@ def _bounds(t: torch.Tensor, problem: Problem) -> int:
     return _addr(t, torch.float16, "bounds")
 
 
+def _page_bounds(dev, problem, prompt, n, entries, cu_seqlens, start, k_pool, block_table, bounds, ws, stream) -> None:
+    cu, first, table = _ptrs(dev, torch.int32, (cu_seqlens, n + 1, "cu_seqlens"), (start, n, "start"),
+                             (block_table, entries, "block_table"))
+    k, out = _ptrs(dev, torch.float16, (k_pool, k_pool.numel(), "k_pool"), (bounds, bounds.numel(), "bounds"))
+    nbytes = ws.numel()
+    wsp, = _ptrs(dev, torch.uint8, (ws, nbytes, "ws"))
+    _call(dev, "pkv_page_bounds", problem, prompt, cu, first, k, table, out, _num_sms(dev), wsp, nbytes, _handle(stream, dev))
+
+
 def pkv_page_bounds(problem: Problem, prompt: Prompt, cu_seqlens, start, k_pool, block_table, bounds, ws, stream=None) -> None:
-    dev = _device(k_pool, cu_seqlens, start, block_table, bounds, ws)
-    n = prompt.num_seqs
+    dev = _device(k_pool)
     _pool(k_pool, "k_pool", problem, prompt)
-    _call(dev, "pkv_page_bounds", _byref(problem), _byref(prompt), _seqs(cu_seqlens, n), _start(start, n),
-          _addr(k_pool, torch.float16, "k_pool"), _table(block_table, problem), _bounds(bounds, problem), _num_sms(dev),
-          _addr(ws, torch.uint8, "ws"), ws.numel(), _handle(stream, dev))
+    _bounds(bounds, problem)
+    b, width = _shape(block_table, problem.batch, problem.max_pages_per_seq)
+    _page_bounds(dev, _byref(problem), _byref(prompt), prompt.num_seqs, b * width, cu_seqlens, start, k_pool, block_table, bounds, ws,
+                 stream)
 
 
 def pkv_sparse_workspace_bytes(problem: Problem, num_sms: int | None = None) -> int:
@@ -194,10 +257,10 @@ def tables_grow(new_tokens: torch.Tensor, seq_lens: torch.Tensor, block_table: t
         cu_seqlens = _new((b + 1,), dev, stream, torch.int32)
     if start is None:
         start = _new((b,), dev, stream, torch.int32)
-    problem = Problem(b, 1, 1, 128, 16, free_pages.numel(), block_table.shape[1])
-    pkv_tables_grow(problem, new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens, start, slots, positions,
-                    seq_lens if seq_lens_out is None else seq_lens_out, free_count if free_count_out is None else free_count_out,
-                    _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    num_pages, width = free_pages.numel(), _shape(block_table)[1]
+    _grow(dev, _described(b, 1, 1, 128, 16, num_pages, width), b, num_pages, b * width, new_tokens, seq_lens, block_table, free_pages,
+          free_count, cu_seqlens, start, slots, positions, seq_lens if seq_lens_out is None else seq_lens_out,
+          free_count if free_count_out is None else free_count_out, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
     return cu_seqlens, start
 
 
@@ -208,11 +271,10 @@ def tables_release(released: torch.Tensor, seq_lens: torch.Tensor, block_table: 
     others as for tables_grow."""
     b = released.numel()
     dev = _device(released)
-    problem = Problem(b, 1, 1, 128, 16, free_pages.numel(), block_table.shape[1])
-    pkv_tables_release(problem, released, seq_lens, block_table, free_pages, free_count,
-                       seq_lens if seq_lens_out is None else seq_lens_out,
-                       free_count if free_count_out is None else free_count_out,
-                       _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    num_pages, width = free_pages.numel(), _shape(block_table)[1]
+    _release(dev, _described(b, 1, 1, 128, 16, num_pages, width), b, num_pages, b * width, released, seq_lens, block_table, free_pages,
+             free_count, seq_lens if seq_lens_out is None else seq_lens_out,
+             free_count if free_count_out is None else free_count_out, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
 
 
 def page_bounds(k_pool: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor, bounds: torch.Tensor,
@@ -226,12 +288,13 @@ def page_bounds(k_pool: torch.Tensor, cu_seqlens: torch.Tensor, block_table: tor
     if k_pool.dim() != 4:
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, d]")
     pages, ps, hkv, d = k_pool.shape
-    b, width = block_table.shape
-    dev = _device(k_pool, cu_seqlens, start, block_table, bounds, ws)
-    problem = Problem(b, hkv, hkv, d, ps, pages, width)
-    prompt = Prompt(cu_seqlens.numel() - 1, min(b * width * ps, 0x7fffffff), hkv, hkv, d, 0, hkv * d, hkv * d, hkv * d, hkv * d)
-    pkv_page_bounds(problem, prompt, cu_seqlens, start, k_pool, block_table, bounds,
-                    _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
+    if bounds.shape != (pages, hkv, 2, d):
+        raise ValueError(f"bounds must have shape ({pages}, {hkv}, 2, {d}), got {tuple(bounds.shape)}")
+    b, width = _shape(block_table)
+    dev = _device(k_pool)
+    n = cu_seqlens.numel() - 1
+    _page_bounds(dev, _described(b, hkv, hkv, d, ps, pages, width), _packed(n, min(b * width * ps, 0x7fffffff), hkv, d), n, b * width,
+                 cu_seqlens, start, k_pool, block_table, bounds, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
     return bounds
 
 
