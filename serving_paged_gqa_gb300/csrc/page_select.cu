@@ -16,9 +16,11 @@
 //
 // Two kernels: scores, bound by HBM (512 bytes a (page, KV head)), a warp per KV head and 16 pages, so that the heads of a page
 // are read together; and a CTA per (row, KV head) that selects, bound by latency.
-// Measured on a GB300 (32 query heads, 8 KV heads): one row of 2048 pages 14.5 us (the score kernel 4 us behind its predecessor, the
-// selection 8); 32 rows of 250-2048 pages 43 us: 24 us for the bounds' 133 MB (5.6 TB/s), 9 us behind them for 256 selections.
-// (The threshold bit by bit from counts of all keys took 10 us of a selection, the histogram takes 1.)
+// Measured on a GB300 (32 query heads, 8 KV heads): one row of 2048 pages 11.8 us, 32 rows of 250-2048 pages 36 us, of which the
+// bounds' 133 MB take 24 (5.6 TB/s). A selection takes 12000-14000 cycles: scores from L2 2500, the border 2000, what lies next to it
+// 1500, exact scores 4000-5000 (two dependent loads), the list 1500. What moved it: the threshold bit by bit from counts of all keys
+// took 10 us, the histogram takes 1; 512 threads 36 us for the 32 rows, 256 41, 1024 (one CTA an SM) 45; half a warp an exact score
+// 41, a warp 43.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -34,7 +36,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTile = 16;                 // pages of a tile
 constexpr int kBoundBytes = 2 * kRowBytes;  // of a (page, KV head)
 constexpr int kScoreWarps = 8;
-constexpr int kThreads = 256;             // of the selection
+constexpr int kThreads = 512;             // of the selection
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeld = 8192;               // keys in shared memory
 constexpr int kBins = 1024;
@@ -172,55 +174,56 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 __device__ __forceinline__ float from_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// A sum of products of two fp16 values, exact: these are multiples of 2^-48 below 2^32, here hi * 2^-16 + lo * 2^-48 with 0 <= lo <
-// 2^32. (In 64-bit floating point, of which an SM adds two a cycle, a page takes 2 us.)
+// A sum of products of two fp16 values, exact: these are multiples of 2^-48 below 2^32, here hi * 2^-19 + lo * 2^-48 with 0 <= lo <
+// 2^29. (In 64-bit floating point, of which an SM adds two a cycle, a page takes 2 us.)
 struct Exact {
     int64_t hi;
     uint32_t lo;
 };
 __device__ __forceinline__ bool operator>(const Exact& a, const Exact& b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 __device__ __forceinline__ bool operator==(const Exact& a, const Exact& b) { return a.hi == b.hi && a.lo == b.lo; }
-__device__ __forceinline__ double rounded(const Exact& x) { return (double)x.hi * 0x1p-16 + (double)x.lo * 0x1p-48; }
+__device__ __forceinline__ double rounded(const Exact& x) { return (double)x.hi * 0x1p-19 + (double)x.lo * 0x1p-48; }
 constexpr int64_t kMost = INT64_MAX;  // of a score of +inf
 
-// The exact score of a page for query heads g0 <= g < g1 of the group, by a warp: lane l sums dims 4 l .. 4 l + 3.
+// The exact score of a page for query heads g0 <= g < g1 of the group, by half a warp: lane l sums dims 8 l .. 8 l + 7. Both halves
+// are in it together.
 __device__ __forceinline__ Exact exact_score(const SelectParams& p, int b, int h, int lp, int g0, int g1) {
-    const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
-    const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + ((int64_t)b * p.Hq + h * G) * kHeadDim) + lane;
-    uint2 next = q[g0 * 32];  // on its way together with the table's entry
+    const int lane = threadIdx.x & 15, G = p.Hq / p.Hkv;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) + ((int64_t)b * p.Hq + h * G) * kHeadDim) + lane;
+    uint4 next = q[g0 * 16];  // on its way together with the table's entry
     const int page = page_of(p, b, lp);
-    uint2 lo = make_uint2(0u, 0u), hi = lo;
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
     if (page >= 0) {
-        const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.bounds) + ((int64_t)page * p.Hkv + h) * kBoundBytes);
+        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.bounds) + ((int64_t)page * p.Hkv + h) * kBoundBytes);
         lo = at[lane];
-        hi = at[32 + lane];
+        hi = at[16 + lane];
     }
     Exact best{0, 0};
     for (int g = g0; g < g1; ++g) {
-        const uint2 now = next;
-        if (g + 1 < g1) next = q[(g + 1) * 32];
+        const uint4 now = next;
+        if (g + 1 < g1) next = q[(g + 1) * 16];
         int64_t x = 0, y = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            auto at = [&](const uint2& u) { return (i < 2 ? u.x : u.y) >> (16 * (i & 1)) & 0xffffu; };
+        for (int i = 0; i < 8; ++i) {
+            auto at = [&](const uint4& u) { return reinterpret_cast<const uint32_t*>(&u)[i >> 1] >> (16 * (i & 1)) & 0xffffu; };
             // |value| = mantissa (11 bits) * 2^(exponent - 25), exponent 1 .. 30. The greater product is with the greatest key where the
             // query is positive, with the least one where it is negative.
-            auto mantissa = [](uint32_t u) { return (int)((u & 0x3ffu) | ((u & 0x7c00u) ? 0x400u : 0u)); };
-            auto exponent = [](uint32_t u) { return max((int)(u >> 10 & 31u), 1); };
+            auto mantissa = [](uint32_t u) { return (int)((u & 0x3ffu) + (min(u >> 10 & 31u, 1u) << 10)); };
+            auto exponent = [](uint32_t u) { return (int)max(u >> 10 & 31u, 1u); };
             const uint32_t a = at(now), c = a & 0x8000u ? at(lo) : at(hi);
-            const int64_t product = (a ^ c) & 0x8000u ? -(mantissa(a) * mantissa(c)) : mantissa(a) * mantissa(c);
-            const int shift = exponent(a) + exponent(c) - 2;  // in units of 2^-48
-            if (shift >= 32)
-                x += product << (shift - 32);
-            else
-                y += product << shift;
+            const int m = mantissa(a) * mantissa(c), product = (a ^ c) & 0x8000u ? -m : m;
+            const int shift = exponent(a) + exponent(c) - 2;  // in units of 2^-48: 0 .. 58
+            const bool upper = shift >= 29;
+            const int power = 1 << (upper ? shift - 29 : shift);
+            x += (int64_t)(upper ? product : 0) * power;
+            y += (int64_t)(upper ? 0 : product) * power;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+        for (int o = 8; o > 0; o >>= 1) {
             x += __shfl_xor_sync(kAll, x, o);
             y += __shfl_xor_sync(kAll, y, o);
         }
-        const Exact s{x + (y >> 32), (uint32_t)y};
+        const Exact s{x + (y >> 29), (uint32_t)y & 0x1fffffffu};
         if (g == g0 || s > best) best = s;
     }
     return best;
@@ -292,6 +295,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     grid_dependency_wait();
     float* scores = p.scores + pair * p.max_pages;
     double* exact = p.exact + pair * p.max_pages;
+    const int tiles = (p.max_pages + kTile - 1) / kTile;
+    const float* tops = p.tops + pair * tiles;
+    float mag = (int)threadIdx.x * kTile < pages ? __ldcg(tops + threadIdx.x) : 0.f;  // (on its way together with the scores)
     uint32_t low = 0xffffffffu, high = 0u;
 #pragma unroll 8
     for (int j = threadIdx.x; j < n; j += kThreads) {
@@ -300,9 +306,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         low = min(low, k);
         high = max(high, k);
     }
-    float mag = 0.f;
-    const int tiles = (p.max_pages + kTile - 1) / kTile;
-    for (int i = threadIdx.x; i * kTile < pages; i += kThreads) mag = fmaxf(mag, __ldcg(p.tops + pair * tiles + i));
+    for (int i = threadIdx.x + kThreads; i * kTile < pages; i += kThreads) mag = fmaxf(mag, __ldcg(tops + i));
     low = __reduce_min_sync(kAll, low);
     high = __reduce_max_sync(kAll, high);
 #pragma unroll
@@ -383,15 +387,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     int unused;
     in = block_scan(in, unused, sm.sum[1]);
     const int room = want - in, near = sm.near;  // pages next to the border that are selected; all of them
-    auto score = [&](int j, uint32_t k) { return k == key_of(INFINITY) ? Exact{kMost, 0} : exact_score(p, b, h, j, 0, G); };
+    auto score = [&](int j, int g0, int g1) {  // by half a warp
+        const Exact e = exact_score(p, b, h, j, g0, g1);
+        return key(j) == key_of(INFINITY) ? Exact{kMost, 0} : e;
+    };
+    const int half = (int)threadIdx.x >> 4, first_lane = (lane & 15) == 0;
     const int run = (n + kThreads - 1) / kThreads, p0 = min(n, (int)threadIdx.x * run), p1 = min(n, p0 + run);
     if (near <= kList) {
         if (near > room) {
-            if (near * G <= kList) {  // a warp for every head of every page
-                for (int i = warp; i < near * G; i += kWarps) {
-                    const int j = sm.list[i / G], g = i % G;
-                    const Exact e = key(j) == key_of(INFINITY) ? Exact{kMost, 0} : exact_score(p, b, h, j, g, g + 1);
-                    if (lane == 0) sm.exact[i] = e;
+            if (near * G <= kList) {  // half a warp for every head of every page
+                for (int i0 = 0; i0 + 2 * warp < near * G; i0 += 2 * kWarps) {
+                    const int i = min(i0 + half, near * G - 1), g = i % G;
+                    const Exact e = score(sm.list[i / G], g, g + 1);
+                    if (first_lane && i0 + half < near * G) sm.exact[i] = e;
                 }
                 __syncthreads();
                 Exact best{0, 0};
@@ -403,9 +411,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
                 __syncthreads();
                 if ((int)threadIdx.x < near) sm.exact[threadIdx.x] = best;
             } else {
-                for (int i = warp; i < near; i += kWarps) {
-                    const Exact e = score(sm.list[i], key(sm.list[i]));
-                    if (lane == 0) sm.exact[i] = e;
+                for (int i0 = 0; i0 + 2 * warp < near; i0 += 2 * kWarps) {
+                    const int i = min(i0 + half, near - 1);
+                    const Exact e = score(sm.list[i], 0, G);
+                    if (first_lane && i0 + half < near) sm.exact[i] = e;
                 }
             }
             __syncthreads();
@@ -421,11 +430,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     } else {
         // Many equal or nearly equal scores: the border among the exact ones (rounded to 64 bits), bit by bit, then the lowest of
         // the pages at it.
-        for (int j = warp; j < n; j += kWarps) {
+        for (int j0 = 0; j0 < n; j0 += 2 * kWarps) {
+            const int j = min(j0 + half, n - 1);
             const uint32_t k = key(j);
-            if (k < below || k > above) continue;
-            const Exact e = score(j, k);
-            if (lane == 0) __stcg(exact + j, rounded(e));
+            const bool wanted = k >= below && k <= above;
+            if (!__any_sync(kAll, wanted)) continue;
+            const Exact e = score(j, 0, G);
+            if (first_lane && wanted && j0 + half < n) __stcg(exact + j, rounded(e));
         }
         __syncthreads();
         auto key64 = [&](int j) {
