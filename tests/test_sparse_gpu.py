@@ -166,6 +166,37 @@ def test_scores_that_differ_less_than_fp32_has():
     assert set(want.flatten().tolist()) == top
 
 
+def whole(x):
+    """fp16 values as whole numbers of 2^-24."""
+    return [int(y * 2 ** 24) for y in x.double().flatten().tolist()]
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_scores_of_all_exponents(seed):
+    s = Step([1600], 4, 1, seed=8)
+    n, g = 100, torch.Generator().manual_seed(seed)
+    page = s.c.bt[0, :n].long()
+
+    def magnitudes(*shape):  # every exponent alike, numbers below the least normal one among them
+        return torch.randint(0, 0x7800, shape, generator=g, dtype=torch.int16)
+
+    s.q[0] = (magnitudes(4, D).view(torch.float16) * (1 - 2 * torch.randint(0, 2, (4, D), generator=g))).half().cuda()
+    bits = magnitudes(2, D).repeat(n, 1, 1)
+    for p in range(n):  # a page is the same as the others but for a few steps in one dim
+        bits[p, :, int(torch.randint(0, D, (1,), generator=g))] += int(torch.randint(0, 40, (1,), generator=g))
+    b = bits.view(torch.float16)
+    b = torch.stack((-b[:, 0], b[:, 1]), 1)
+    s.bounds[page, 0] = b.cuda()
+    heads = [whole(x) for x in s.q[0].cpu()]
+    score = []
+    for p in range(n):
+        lo, hi = whole(b[p, 0]), whole(b[p, 1])
+        score.append(max(sum(x * (h if x > 0 else l) for x, l, h in zip(q, lo, hi)) for q in heads))
+    for k in (2, 13, 50, 90):
+        want = sorted(sorted(range(n - 1), key=lambda p: (-score[p], p))[: k - 1]) + [n - 1]
+        assert s.select(k).flatten().tolist() == want
+
+
 def test_bounds_and_queries_that_are_not_finite():
     s = Step([2000, 900], 8, 2, seed=5)
     page = s.c.bt[0].long()
