@@ -9,8 +9,8 @@
 // the stack's height) is written by the CTA that ends last, when all have read it.
 //
 // Bound: latency (two dependent round trips, lengths, then table or stack, and the scan between them), then the
-// 12 bytes a token that are written. Measured on a GB300, in a captured graph: 256 rows of one new token 5.7 us, 64 rows of up to
-// 4096 (130k tokens) 8.0-9.0 us, 128 of 256 rows released (130k pages) 4.8 us; as calls 8.5-11 us, which the binding takes.
+// 12 bytes a token that are written. Measured on a GB300, in a captured graph: 256 rows of one new token 4.1 us, 64 rows of up to
+// 4096 (130k tokens) 6.0 us, 128 of 256 rows released (130k pages) 4.8 us; as calls 8.5-11 us, which the binding takes.
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -250,9 +250,10 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const TablesParams p)
     }
 }
 
-// CTAs for `items` tokens or pages: 4 a thread, so that a CTA's scan is worth it.
+// CTAs for `items` tokens or pages: one a thread, as every CTA's scan takes the same time side by side (130k tokens: 9.3 us with 8 a
+// thread, 7.2 with 4, 6.0 with one; 256 tokens 5.0, 4.5, 4.1-4.6).
 int grid_for(int64_t items, int num_sms) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>((items + 4 * kThreads - 1) / (4 * kThreads), num_sms));
+    return (int)std::max<int64_t>(1, std::min<int64_t>((items + kThreads - 1) / kThreads, num_sms));
 }
 
 }  // namespace
