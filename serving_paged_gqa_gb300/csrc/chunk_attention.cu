@@ -36,7 +36,8 @@
 // Tried and dropped: the next pair's first scores issued before the current pair's last products (nothing, and 3-6 % slower with
 // short pairs); a grid of merging blocks that share the items they count (2 us slower); both kinds of sequences in one
 // kernel (its registers spill: 8192 tokens 371 us, 420); one box of 4 KB a page, its halves side by side (16 sequences of 2-8 tokens
-// 205 -> 203 us, 12 of 1-1024 600 -> 610).
+// 205 -> 203 us, 12 of 1-1024 600 -> 610); the next pair's table entries read ahead, its queries behind its first keys, rows of few
+// written out in rolled loops (nothing, or 1 us more a call).
 #include <cuda_fp16.h>
 
 #include <algorithm>
