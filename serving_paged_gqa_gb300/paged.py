@@ -63,7 +63,7 @@ def _ptrs(dev: int, dtype, *wants) -> list:
         elif t.numel() != n:
             raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
         else:
-            _addr(t, dtype, name)
+            at.append(_addr(t, dtype, name))
     return at
 
 
