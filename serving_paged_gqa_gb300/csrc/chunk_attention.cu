@@ -107,7 +107,7 @@ struct Bars {
     uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
     uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
     uint64_t low_full[8], low_empty[8];  // few: [tile][half][warp of rows 0-63] second parts' accumulators are there, have been read
-    uint64_t told[8];                // few: [half][warp of the half] so are the rows that B's warp has found
+    uint64_t told[2][8];             // few: [turn][half][warp of the half] so are the rows that B's warp has found
     uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
     uint64_t drain;
 };
@@ -126,8 +126,8 @@ struct Layout {
     static constexpr int scan = late + 8 * 4;                    // int64 [warp]: cost of the sequences of a warp's threads
     static constexpr int begin = scan + kThreads / 32 * 8;       // int64, int32: where the piece begins
     static constexpr int low = begin + 16;                       // few: uint32 [tile][half][64][17]: second parts' accumulators
-    static constexpr int told = low + (kFew ? 4 * 64 * 17 * 4 : 0);  // few: uint32 [half][warp]: rows to be finished
-    static constexpr int misc = told + 8 * 4;                    // abort flag, TMEM address
+    static constexpr int told = low + (kFew ? 4 * 64 * 17 * 4 : 0);  // few: uint32 [turn][half][warp]: rows to be finished
+    static constexpr int misc = told + 16 * 4;                   // abort flag, TMEM address
     static constexpr int bytes = misc + 16 + 1024;               // slack to align the base to 1024 bytes
     static_assert(sizeof(Work) % 4 == 0 && bars % 8 == 0 && parts % 8 == 0 && scan % 8 == 0, "alignment");
     static_assert(kStages <= kMostStages && bytes <= 227 * 1024, "shared memory");
@@ -498,13 +498,16 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
         }
         if (mine) dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    // As in softmax_tile; B's warps tell A's, which finish the 64 dims of both.
+    // As in softmax_tile; B's warps tell A's, which finish the 64 dims of both. They take turns with two words: a tile of one step of
+    // 64 keys needs nothing of A's second-half warps, so B's may write for it while A's have not read what the tile before it left.
+    // No more than one tile lies between them (w_empty), and a third finds the first one's word read.
     const bool low_sum = !(y.y >= 0.25f);
     const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
     unsigned again = __ballot_sync(kAllLanes, mine && odd && !isnan(y.y));
     const unsigned redo = __ballot_sync(kAllLanes, low_sum);
-    uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + h * 4 + (warp & 3);
-    uint64_t* told_full = &bars.told[h * 4 + (warp & 3)];
+    const int n = cnt.told++;
+    uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + (n & 1) * 8 + h * 4 + (warp & 3);
+    uint64_t* told_full = &bars.told[n & 1][h * 4 + (warp & 3)];
     if (x == 1) {
         if (lane == 0) {
             *told = again;
@@ -513,7 +516,7 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
         __syncwarp();
         return true;
     }
-    if (!short_wait(told_full, cnt.told++ & 1, ctx)) return false;
+    if (!short_wait(told_full, (n >> 1) & 1, ctx)) return false;
     again |= *told;
     if (again)
         finish_rows<G>(p, Seq{w.q.first, w.q.n, w.q.start}, w.s, (row & ~31) / G, w.h, h, again, redo & again);
@@ -914,7 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (kFew && threadIdx.x >= 32 && threadIdx.x < 40) {
         mbar_init(&bars.low_full[threadIdx.x - 32], 1);
         mbar_init(&bars.low_empty[threadIdx.x - 32], 1);
-        mbar_init(&bars.told[threadIdx.x - 32], 1);
+        mbar_init(&bars.told[0][threadIdx.x - 32], 1);
+        mbar_init(&bars.told[1][threadIdx.x - 32], 1);
     }
     // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (Not so the second of
     // two kernels: begun in the gaps of the first, 30 sequences of 64 tokens behind 1000 took 74 us, 66 one behind the other.)
