@@ -508,6 +508,7 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
     const int n = cnt.told++;
     uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + (n & 1) * 8 + h * 4 + (warp & 3);
     uint64_t* told_full = &bars.told[n & 1][h * 4 + (warp & 3)];
+    __syncwarp();  // finish_rows reads rows that other lanes have stored; of B's warp they are told behind its lane 0
     if (x == 1) {
         if (lane == 0) {
             *told = again;

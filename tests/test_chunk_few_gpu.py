@@ -61,3 +61,19 @@ def test_short_sequences_with_values_that_are_not_finite(sms, new, start):
                 v[0, 3] = math.nan
             put(c, s, st + m - 1 if s % 3 else max(0, st + m // 2 - 1), v=v)
     check_not_finite(c, run_on(sms, c))
+
+
+@pytest.mark.parametrize("new,start", [([5], [40]), ([16], [300]), ([30], [20]), ([9], [5000])])
+def test_rows_that_other_lanes_have_stored(new, start):
+    """Values that are not finite in the dims that tile B's warps store, and finish by tile A's: the finite ones beside them stay, call
+    after call."""
+    c = Cache(new * 30, start * 30, 8, 2, seed=sum(new) + 2)
+    for s, (m, st) in enumerate(zip(c.new, c.start)):
+        v = torch.randn((2, D), generator=torch.Generator(device="cuda").manual_seed(s + 50), device="cuda").half()
+        v[:, (32, 45, 63, 96, 127)[s % 5]] = math.inf
+        v[0, 100] = -math.inf
+        put(c, s, st + s % m, v=v)
+    first = run_on(152, c)
+    check_not_finite(c, first)
+    for _ in range(20):
+        assert torch.equal(run_on(152, c).view(torch.int16), first.view(torch.int16))
