@@ -379,12 +379,20 @@ __device__ __forceinline__ float2 sum_of(const float2* at, bool second_half) {
                                 scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
 }
 
-// A wait for another warp of the softmax that is as far as this one: warp_wait's clock would take registers that the rows need.
+// A wait for another warp of the softmax. Mostly it is as far as this one, but where a tile has 64 keys or fewer one of its second half
+// may still finish rows of the tile before, which takes as long as their keys do: after some tries the clock decides, in steps of
+// 2^20 ns, as warp_wait's 64-bit times would take registers that the rows need.
 __device__ __forceinline__ bool short_wait(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
-    for (uint32_t it = 0; it < 1u << 20; ++it) {
+    for (uint32_t it = 0; it < 4096; ++it) {
         if (__all_sync(kAllLanes, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(kAllLanes, *ctx.abort_flag != 0)) return false;
     }
+    auto now = [] { return (uint32_t)(global_timer_ns() >> 20); };
+    const uint32_t begin = now();
+    do {
+        if (__all_sync(kAllLanes, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(kAllLanes, *ctx.abort_flag != 0)) return false;
+    } while (__all_sync(kAllLanes, now() - begin <= (uint32_t)(ctx.limit_ns >> 20)));
     *ctx.abort_flag = 1;
     raise_status(ctx.status, PKV_STATUS_TIMEOUT);
     return false;

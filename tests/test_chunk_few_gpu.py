@@ -15,7 +15,7 @@ from test_chunk_edges_gpu import check_not_finite, put
 pytestmark = pytest.mark.gpu
 
 
-def run_on(sms, c):
+def run_on(sms, c, q=None):
     """The call on a grid of `sms` CTAs."""
     lib, n = pkv.load(), ctypes.c_size_t()
     assert lib.pkv_chunk_workspace_bytes(sms, ctypes.byref(n)) == 0
@@ -23,7 +23,7 @@ def run_on(sms, c):
     t = c.q.shape[0]
     pr = pkv.make_problem(len(c.new), c.hq, c.hkv, D, PS, c.num_pages, c.bt.shape[1])
     pm = pkv.make_prompt(len(c.new), t, c.hq, c.hkv, D)
-    q, out = c.q.contiguous(), torch.full((t, c.hq, D), 7.0, dtype=torch.float16, device="cuda")
+    q, out = (c.q if q is None else q).contiguous(), torch.full((t, c.hq, D), 7.0, dtype=torch.float16, device="cuda")
     rc = lib.pkv_chunk_attention(ctypes.byref(pr), ctypes.byref(pm), q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.cu.data_ptr(),
                                  c.st.data_ptr(), c.bt.data_ptr(), ctypes.c_float(c.scale), sms, ws.data_ptr(), ws.numel(),
                                  out.data_ptr(), torch.cuda.current_stream().cuda_stream)
@@ -77,3 +77,23 @@ def test_rows_that_other_lanes_have_stored(new, start):
     check_not_finite(c, first)
     for _ in range(20):
         assert torch.equal(run_on(152, c).view(torch.int16), first.view(torch.int16))
+
+
+def test_a_warp_that_finishes_rows_of_a_long_context():
+    """A CTA's first tile leaves the third and fourth warps of the second half many rows to be computed again from all keys (and the first
+    and second none: NaN queries), while the first ones are at the next tile, of fewer than 64 keys, and wait for the others' part of it."""
+    c = Cache([32, 5, 16, 3], [60000, 10, 4, 30], 4, 1, seed=31)
+    q = c.q.clone()
+    q[:16] = math.nan
+    v = torch.zeros((1, D), dtype=torch.float16, device="cuda")
+    put(c, 0, 60031, v=v)
+    want, bound = c.attend()
+    v[0, 100] = math.inf
+    put(c, 0, 60031, v=v)
+    got = run_on(1, c, q)
+    assert torch.isnan(got[:16]).all()
+    ref.check(got[16:31], want[16:31], bound[16:31])
+    ref.check(got[32:], want[32:], bound[32:])
+    assert (got[31, :, 100] == math.inf).all()
+    rest = [d for d in range(D) if d != 100]
+    ref.check(got[31:32, :, rest], want[31:32, :, rest], bound[31:32, :, rest])
