@@ -446,8 +446,8 @@ int launch_prompt_append(const PagesParams& p, int num_sms, void* stream) {
 
 int launch_page_bounds(const PagesParams& p, int num_sms, void* stream) {
     // The number of new tokens is not known here, so more CTAs than are resident would start to find nothing; four an SM are. (33k
-    // tokens: 14.8 us with two an SM, 11.8 with four, 12.1 with eight.)
-    const int64_t items = page_items(p) / p.Hkv * ((p.Hkv + 1) / 2);
+    // tokens: 14.8 us with two an SM, 11.8 with four, 12.1 with eight.) No row has more pages than its table.
+    const int64_t items = std::min(page_items(p) / p.Hkv, (int64_t)p.num_seqs * p.max_pages) * ((p.Hkv + 1) / 2);
     return launch_behind(bounds_kernel, dim3(std::min(grid_for(num_sms, items), 4 * num_sms)), dim3(kThreads), 0,
                          static_cast<cudaStream_t>(stream), p);
 }

@@ -293,7 +293,8 @@ def page_bounds(k_pool: torch.Tensor, cu_seqlens: torch.Tensor, block_table: tor
     b, width = _shape(block_table)
     dev = _device(k_pool)
     n = cu_seqlens.numel() - 1
-    _page_bounds(dev, _described(b, hkv, hkv, d, ps, pages, width), _packed(n, min(b * width * ps, 0x7fffffff), hkv, d), n, b * width,
+    # Packed rows are not read, and where the sequences begin among them is not known: any place is in order.
+    _page_bounds(dev, _described(b, hkv, hkv, d, ps, pages, width), _packed(n, 0x7fffffff if width else 0, hkv, d), n, b * width,
                  cu_seqlens, start, k_pool, block_table, bounds, _scratch(PKV_PROMPT_WS_BYTES, ws, dev, stream), stream)
     return bounds
 
