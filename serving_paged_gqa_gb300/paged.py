@@ -102,6 +102,11 @@ def _grow(dev, problem, b, num_pages, entries, new_tokens, seq_lens, block_table
     to, = _ptrs(dev, torch.int64, (slots, cap, "slots"))
     nbytes = ws.numel()
     wsp, = _ptrs(dev, torch.uint8, (ws, nbytes, "ws"))
+    if cap == 0 and wsp:
+        # Slots or positions without entries have no address, which would say that none are asked for and any number fits. Any other
+        # address does: nothing is written to 0 entries.
+        to = None if slots is None else wsp
+        pos = None if positions is None else wsp + 16
     _call(dev, "pkv_tables_grow", problem, n, lens, table, pages, count, cu, first, to, pos, cap, lens_out, count_out, _num_sms(dev),
           wsp, nbytes, _handle(stream, dev))
 
@@ -249,7 +254,8 @@ def tables_grow(new_tokens: torch.Tensor, seq_lens: torch.Tensor, block_table: t
     pages. block_table gets the new pages' entries; seq_lens_out and free_count_out (None: seq_lens and free_count themselves)
     the lengths and the stack's height afterwards; cu_seqlens [B + 1] and start [B] (made here where they are not given) what
     prompt_append and chunk_attention take; slots (int64) and positions (int32), one entry for each packed new token, where
-    they are given, the token's page * 16 + slot and its position.
+    they are given, the token's page * 16 + slot and its position. Rows whose new tokens they have no entries for get nothing (none
+    has where they have no entries at all).
     """
     b = new_tokens.numel()
     dev = _device(new_tokens)
