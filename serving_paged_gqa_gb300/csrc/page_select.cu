@@ -166,11 +166,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectPar
 }
 
 // ---- selection -----------------------------------------------------------------------------------------------------
-// Keys in the order of the scores.
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
+// Keys in the order of the scores, from their bits. (Those of decided pages are not numbers, and what a float of such bits is loaded
+// and has its sign set as need not keep them.)
+__device__ __forceinline__ uint32_t key_of(uint32_t u) { return u & 0x80000000u ? ~u : u | 0x80000000u; }
 
 __device__ __forceinline__ float from_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
@@ -183,7 +181,8 @@ struct Exact {
 __device__ __forceinline__ bool operator>(const Exact& a, const Exact& b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 __device__ __forceinline__ bool operator==(const Exact& a, const Exact& b) { return a.hi == b.hi && a.lo == b.lo; }
 __device__ __forceinline__ double rounded(const Exact& x) { return (double)x.hi * 0x1p-19 + (double)x.lo * 0x1p-48; }
-constexpr int64_t kMost = INT64_MAX;  // of a score of +inf
+constexpr int64_t kMost = INT64_MAX;         // of a score of +inf
+constexpr uint32_t kInfinite = 0xff800000u;  // its key
 
 // The exact score of a page for query heads g0 <= g < g1 of the group, by half a warp: lane l sums dims 8 l .. 8 l + 7. Both halves
 // are in it together.
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         l1 = fmaxf(l1, isfinite(s) ? s : INFINITY);
     }
     grid_dependency_wait();
-    float* scores = p.scores + pair * p.max_pages;
+    uint32_t* scores = reinterpret_cast<uint32_t*>(p.scores) + pair * p.max_pages;
     double* exact = p.exact + pair * p.max_pages;
     const int tiles = (p.max_pages + kTile - 1) / kTile;
     const float* tops = p.tops + pair * tiles;
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         if (j < kHeld)
             sm.keys[j] = in ? 0xffffffffu : 0u;
         else
-            __stcg(scores + j, __uint_as_float(in ? 0x7fffffffu : 0xffffffffu));
+            __stcg(scores + j, in ? 0x7fffffffu : 0xffffffffu);
     };
     // The border, the greatest key that `want` keys reach, lies in one of 1024 equal parts of the keys' range, found from a
     // histogram; where that part has many keys, in one of 1024 parts of it, and so on.
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     const float delta = isfinite(q1) ? 0x1p-14f * q1 * top : 0.f;
     auto moved = [&](uint32_t k, float by, bool up) {
         const float x = from_key(k);
-        return isfinite(x) ? key_of(up ? __fadd_ru(x, by) : __fadd_rd(x, -by)) : k;
+        return isfinite(x) ? key_of(__float_as_uint(up ? __fadd_ru(x, by) : __fadd_rd(x, -by))) : k;
     };
     const uint32_t above = moved(high, delta, true), below = moved(low, delta, false);
     if (threadIdx.x == 0) sm.near = 0;
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     const int room = want - in, near = sm.near;  // pages next to the border that are selected; all of them
     auto score = [&](int j, int g0, int g1) {  // by half a warp
         const Exact e = exact_score(p, b, h, j, g0, g1);
-        return key(j) == key_of(INFINITY) ? Exact{kMost, 0} : e;
+        return key(j) == kInfinite ? Exact{kMost, 0} : e;
     };
     const int half = (int)threadIdx.x >> 4, first_lane = (lane & 15) == 0;
     const int run = (n + kThreads - 1) / kThreads, p0 = min(n, (int)threadIdx.x * run), p1 = min(n, p0 + run);

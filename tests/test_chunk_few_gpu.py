@@ -97,3 +97,14 @@ def test_a_warp_that_finishes_rows_of_a_long_context():
     assert (got[31, :, 100] == math.inf).all()
     rest = [d for d in range(D) if d != 100]
     ref.check(got[31:32, :, rest], want[31:32, :, rest], bound[31:32, :, rest])
+
+
+@pytest.mark.parametrize("new,start", [([700, 3, 90, 1, 33], [3000, 20000, 100, 5, 900]), ([5], [9000]), ([600], [4000])])
+def test_results_do_not_depend_on_timing(new, start):
+    c = Cache(new, start, 8, 2, seed=sum(new) + 3)
+    first = run_on(152, c)
+    busy = torch.randn((2048, 2048), device="cuda")
+    for i in range(10):
+        if i % 2:
+            busy = busy @ busy * 1e-3  # something before it on the stream
+        assert torch.equal(run_on(152, c), first)
