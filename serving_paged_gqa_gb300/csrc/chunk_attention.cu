@@ -103,11 +103,11 @@ struct Bars {
     uint64_t p_full[2][2];           // its weights of the step's first, second 64 keys are
     uint64_t o_full[2];              // its accumulator is complete
     uint64_t lo_done[2];             // the products of a step's first 64 keys are in the accumulator
-    uint64_t o_free[2];              // the accumulator has been read
+    uint64_t o_free[2];              // the accumulator has been read; few, of A: and the second half is done with the tile
     uint64_t first_ref[2][4];        // [tile][warp of the half]: the tile's first references are in shared memory
     uint64_t half_done[2][4];        // [tile][warp of the half]: the second half has settled its weights of the step
     uint64_t low_full[8], low_empty[8];  // few: [tile][half][warp of rows 0-63] second parts' accumulators are there, have been read
-    uint64_t told[2][8];             // few: [turn][half][warp of the half] so are the rows that B's warp has found
+    uint64_t told[8];                // few: [half][warp of the half] so are the rows that B's warp has found
     uint64_t tail_full;              // a tile of V with rows behind the pair's last key has come
     uint64_t drain;
 };
@@ -126,8 +126,8 @@ struct Layout {
     static constexpr int scan = late + 8 * 4;                    // int64 [warp]: cost of the sequences of a warp's threads
     static constexpr int begin = scan + kThreads / 32 * 8;       // int64, int32: where the piece begins
     static constexpr int low = begin + 16;                       // few: uint32 [tile][half][64][17]: second parts' accumulators
-    static constexpr int told = low + (kFew ? 4 * 64 * 17 * 4 : 0);  // few: uint32 [turn][half][warp]: rows to be finished
-    static constexpr int misc = told + 16 * 4;                   // abort flag, TMEM address
+    static constexpr int told = low + (kFew ? 4 * 64 * 17 * 4 : 0);  // few: uint32 [half][warp]: rows to be finished
+    static constexpr int misc = told + 8 * 4;                    // abort flag, TMEM address
     static constexpr int bytes = misc + 16 + 1024;               // slack to align the base to 1024 bytes
     static_assert(sizeof(Work) % 4 == 0 && bars % 8 == 0 && parts % 8 == 0 && scan % 8 == 0, "alignment");
     static_assert(kStages <= kMostStages && bytes <= 227 * 1024, "shared memory");
@@ -379,20 +379,13 @@ __device__ __forceinline__ float2 sum_of(const float2* at, bool second_half) {
                                 scaled(hi.y, hi.x == top ? 1.f : fast_exp2(hi.x - top)));
 }
 
-// A wait for another warp of the softmax. Mostly it is as far as this one, but where a tile has 64 keys or fewer one of its second half
-// may still finish rows of the tile before, which takes as long as their keys do: after some tries the clock decides, in steps of
-// 2^20 ns, as warp_wait's 64-bit times would take registers that the rows need.
+// A wait for another warp of the softmax that is as far as this one (done with the tile before: see o_free): warp_wait's clock would take
+// registers that the rows need.
 __device__ __forceinline__ bool short_wait(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
-    for (uint32_t it = 0; it < 4096; ++it) {
+    for (uint32_t it = 0; it < 1u << 20; ++it) {
         if (__all_sync(kAllLanes, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(kAllLanes, *ctx.abort_flag != 0)) return false;
     }
-    auto now = [] { return (uint32_t)(global_timer_ns() >> 20); };
-    const uint32_t begin = now();
-    do {
-        if (__all_sync(kAllLanes, mbar_try_wait(bar, parity))) return true;
-        if (__any_sync(kAllLanes, *ctx.abort_flag != 0)) return false;
-    } while (__all_sync(kAllLanes, now() - begin <= (uint32_t)(ctx.limit_ns >> 20)));
     *ctx.abort_flag = 1;
     raise_status(ctx.status, PKV_STATUS_TIMEOUT);
     return false;
@@ -409,11 +402,11 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
     const int lane_row = threadIdx.x & 127, row = dup ? lane_row & 63 : lane_row;
     const bool low = dup && lane_row >= 64, mine = !low && row / G < w.q.n;
     if (!warp_wait(&bars.o_full[0], cnt.na & 1, ctx) || (both && !warp_wait(&bars.o_full[1], cnt.nb & 1, ctx))) return false;
-    auto have_read = [&]() {  // the next tile's products may overwrite them
+    auto have_read = [&]() {  // the next tile's products may overwrite them (A's second half says so when it is done with the tile)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&bars.o_free[0]);
+            if (x == 1 || h == 0) mbar_arrive(&bars.o_free[0]);
             if (both) mbar_arrive(&bars.o_free[1]);
         }
     };
@@ -506,16 +499,14 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
         }
         if (mine) dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    // As in softmax_tile; B's warps tell A's, which finish the 64 dims of both. They take turns with two words: a tile of one step of
-    // 64 keys needs nothing of A's second-half warps, so B's may write for it while A's have not read what the tile before it left.
-    // No more than one tile lies between them (w_empty), and a third finds the first one's word read.
+    // As in softmax_tile; B's warps tell A's, which finish the 64 dims of both. A's have read a word before the next tile's accumulator is
+    // complete (the first half has made its weights, and the second half's arrivals are part of o_free), so no word is overwritten early.
     const bool low_sum = !(y.y >= 0.25f);
     const bool odd = __low2float(probe) != 0.f || __high2float(probe) != 0.f || low_sum;
     unsigned again = __ballot_sync(kAllLanes, mine && odd && !isnan(y.y));
     const unsigned redo = __ballot_sync(kAllLanes, low_sum);
-    const int n = cnt.told++;
-    uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + (n & 1) * 8 + h * 4 + (warp & 3);
-    uint64_t* told_full = &bars.told[n & 1][h * 4 + (warp & 3)];
+    uint32_t* told = reinterpret_cast<uint32_t*>(smem + L::told) + h * 4 + (warp & 3);
+    uint64_t* told_full = &bars.told[h * 4 + (warp & 3)];
     __syncwarp();  // finish_rows reads rows that other lanes have stored; of B's warp they are told behind its lane 0
     if (x == 1) {
         if (lane == 0) {
@@ -525,7 +516,7 @@ __device__ __forceinline__ bool few_rows_out(const ChunkParams& p, uint8_t* smem
         __syncwarp();
         return true;
     }
-    if (!short_wait(told_full, (n >> 1) & 1, ctx)) return false;
+    if (!short_wait(told_full, cnt.told++ & 1, ctx)) return false;
     again |= *told;
     if (again)
         finish_rows<G>(p, Seq{w.q.first, w.q.n, w.q.start}, w.s, (row & ~31) / G, w.h, h, again, redo & again);
@@ -926,8 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (kFew && threadIdx.x >= 32 && threadIdx.x < 40) {
         mbar_init(&bars.low_full[threadIdx.x - 32], 1);
         mbar_init(&bars.low_empty[threadIdx.x - 32], 1);
-        mbar_init(&bars.told[0][threadIdx.x - 32], 1);
-        mbar_init(&bars.told[1][threadIdx.x - 32], 1);
+        mbar_init(&bars.told[threadIdx.x - 32], 1);
     }
     // Everything before this kernel on the stream has completed, and what comes behind it may begin to begin. (Not so the second of
     // two kernels: begun in the gaps of the first, 30 sequences of 64 tokens behind 1000 took 74 us, 66 one behind the other.)
@@ -1355,7 +1345,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int k = 0;; ++k) {
             // The slot is kept while it is worked on: what a step does not need is not kept in registers.
             __syncwarp();
-            if (k > 0 && lane == 0) mbar_arrive(&bars.w_empty[(k - 1) & 1]);
+            if (k > 0 && lane == 0) {
+                mbar_arrive(&bars.w_empty[(k - 1) & 1]);
+                // A tile of 64 keys or fewer takes no weights from A's second half: without this its accumulator would be complete,
+                // and B's warps tell of its rows, while A's have not read what they told of the tile before, or finish its rows.
+                if (kFew && warp >> 2 == 1) mbar_arrive(&bars.o_free[0]);
+            }
             if (!warp_wait(&bars.w_full[k & 1], (k >> 1) & 1, ctx)) break;
             const volatile Work& w = reinterpret_cast<const volatile Work*>(work)[k & 1];
             if (w.h < 0) break;
