@@ -529,6 +529,7 @@ int pkv_chunk_workspace_bytes(int32_t num_sms, size_t* bytes);
  * Slots behind a row's last token may hold anything. Infinities and NaN of K and V reach the rows that attend to them alone,
  * as for pkv_prompt_attention. The division of the work over the GPU is worked out on the device: one captured graph
  * serves every step of a batch. out must not overlap q or the pools (the same address is refused).
+ * The weights of the values are fp16 with a row's largest at about 2^5: those below 2^-30 of it count as 0.
  * A sequence whose bounds are not ordered inside [0, total_tokens], or that would outgrow its block table, raises
  * PKV_STATUS_BAD_LEN and is skipped; a block-table entry outside the pool raises PKV_STATUS_BAD_PAGE and counts as a page
  * whose K and V are 0.

@@ -28,11 +28,18 @@
 //   warp 18         walks the piece and publishes its pairs, two ahead
 // Every wait is bounded (pkv_wait.cuh).
 //
+// Precision: sums, references and states are fp32; the second product takes its weights as fp16, like the values, as both of its operands
+// have one type. Relative error 2.9e-4 (the output's rounding alone 2.1e-4), in tiles of at most 64 rows 2.1e-4 from a second fp16 part:
+// a token's error depends on how many tokens come with it. Either way the largest weight of a row is about 2^5 and fp16's least 2^-24:
+// weights below 2^-30 of the row's largest are 0, and those below 2^-19 have less than 11 bits. Where a row's values are those of such weights
+// alone (6000 equal keys next to one 16 / 18 / 20 nats above them whose value is 0), the error is 1.8e-3 / 5.4e-3 / 2.3e-2.
+//
 // Measured on GB300s (32 query heads, 8 KV heads): 4096 tokens behind 28672 1.38 ms, 1490 TFLOP/s, 0.79 of the
 // measured cuBLAS burst under the power cap; 16384 without a prefix 1.40 ms (1570 TFLOP/s; prompt_attention.cu 1.30-1.39); 512
 // behind 8192 64 us, of which 28 steps take 46; 16 sequences of 2-8 tokens behind 1000-32000 204 us, 5.75 TB/s; 5 tokens behind 700
 // 14.6 us. Under ncu (512 behind 8192, cold) the tensor pipe is active 49 % of the time, warps wait for TMEM loads and for
-// instructions; a step of a pair takes 3060 cycles, of which the tensor core's share is 2048 (prompt_attention.cu 2820).
+// instructions; a step of a pair takes 3060 cycles, of which the tensor core's share is 2048 (prompt_attention.cu 2820, which spills no
+// register; here, at the same 96 a thread, the kernel for pairs spills 52 bytes and loads 284, that for few rows 64 and 84).
 // Tried and dropped: the next pair's first scores issued before the current pair's last products (nothing, and 3-6 % slower with
 // short pairs); a grid of merging blocks that share the items they count (2 us slower); both kinds of sequences in one
 // kernel (its registers spill: 8192 tokens 371 us, 420); one box of 4 KB a page, its halves side by side (16 sequences of 2-8 tokens

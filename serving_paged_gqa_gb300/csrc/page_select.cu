@@ -11,7 +11,8 @@
 // delta = 2^-15 max_g |q_g|_1 max |bound|: 16 instructions add 16 products and the sum before, each of which may lose 2^-23 of the
 // greatest magnitude (17 * 16 * 2^-23 = 2^-14.9 of the sum of magnitudes, half of which are zeros of q- or q+). With T the
 // (select - 1)-th greatest fp32 score, pages above T + 2 delta are in and those below T - 2 delta out whatever their exact scores
-// are; those between are scored again exactly, in integers (one to four of 2048 with normal values), and ranked by those.
+// are; those between are scored again exactly, in integers (one to four of 2048 with normal values), and ranked by those (by their sums
+// rounded to 64 bits where more than 256 pages lie between).
 // Bounds or queries that are not finite make a score of +inf: such pages come first.
 //
 // Two kernels: scores, bound by HBM (512 bytes a (page, KV head)), a warp per KV head and 16 pages, so that the heads of a page
@@ -21,6 +22,9 @@
 // 1500, exact scores 4000-5000 (two dependent loads), the list 1500. What moved it: the threshold bit by bit from counts of all keys
 // took 10 us, the histogram takes 1; 512 threads 36 us for the 32 rows, 256 41, 1024 (one CTA an SM) 45; half a warp an exact score
 // 41, a warp 43.
+// Where this is weak: delta takes the row's greatest bound, so one page with a bound of 6e4 among normal ones puts all pages next to the
+// border, and the selection of 32 rows of 2048 pages takes 665 us instead of 58. And a scoring CTA has a warp a KV head: 32 rows of 2048
+// pages take 58 us with 8 KV heads, 44 with 4, 38 with 2 or 1, where most warps have nothing to read (0.9 TB/s with one).
 #include <cuda_fp16.h>
 
 #include <algorithm>

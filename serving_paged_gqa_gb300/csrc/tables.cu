@@ -9,8 +9,8 @@
 // the stack's height) is written by the CTA that ends last, when all have read it.
 //
 // Bound: latency (two dependent round trips, lengths, then table or stack, and the scan between them), then the
-// 12 bytes a token that are written. Measured on a GB300, in a captured graph: 256 rows of one new token 4.1-5.3 us, 64 rows of up to
-// 4096 (130k tokens) 6.0-6.7 us, 128 of 256 rows released (130k pages) 4.8 us; as calls 8.5-11 us, which the binding takes.
+// 12 bytes a token that are written. Measured on a GB300, in a captured graph: 256 rows of one new token 4.1-5.5 us, 64 rows of up to
+// 4096 (130k tokens) 6.0-7.9 us, 128 of 256 rows released (130k pages) 4.8 us; as calls 8.5-11 us, which the binding takes.
 #include <algorithm>
 
 #include "pkv_internal.h"
